@@ -21,6 +21,8 @@ GDR_OK = 0
 GDR_DTYPE_F32, GDR_DTYPE_BF16, GDR_DTYPE_U32, GDR_DTYPE_I32 = 0, 1, 2, 3
 GDR_FLAG_L2NORM_QK = 1
 GDR_FLAG_CONV_SILU = 2
+GDR_FLAG_GATE_SIGMOID = 4
+GDR_FLAG_GATE_SILU = 8
 MAX_DIMS = 5
 
 _DTYPES = {torch.float32: GDR_DTYPE_F32, torch.bfloat16: GDR_DTYPE_BF16,
@@ -44,7 +46,9 @@ _lib = None
 EXPORTS = ("gdr_recurrence_fwd", "gdr_recurrence_verify_ring", "gdr_state_fold",
            "gdr_fused_recurrent_update", "gdr_snapshot_rollback", "gdr_causal_conv1d",
            "gdr_fwd_output_shape", "gdr_check_indices", "gdr_set_debug_checks",
-           "gdr_ring_record_elements", "gdr_last_error_message", "gdr_version")
+           "gdr_linear_attention_fwd", "gdr_linear_attention_step", "gdr_linear_attention_bwd",
+           "gdr_block_norm", "gdr_block_norm_bwd", "gdr_linear_attention_workspace",
+           "gdr_block_norm_workspace", "gdr_ring_record_elements", "gdr_last_error_message", "gdr_version")
 
 
 def lib():
@@ -68,11 +72,20 @@ def lib():
         i64 = ctypes.c_int64
         L.gdr_check_indices.argtypes = [i64, vp, i64, vp, i64, vp, i64, i64, vp]
         L.gdr_set_debug_checks.argtypes = [ctypes.c_int]
+        L.gdr_linear_attention_fwd.argtypes = [P] * 6 + [f32] + [P] * 5 + [vp]
+        L.gdr_linear_attention_step.argtypes = [P] * 7 + [f32, vp]
+        L.gdr_linear_attention_bwd.argtypes = [P] * 6 + [f32] + [P] * 8 + [vp]
+        L.gdr_block_norm.argtypes = [P] * 7 + [i64, f32, f32, u32, vp]
+        L.gdr_block_norm_bwd.argtypes = [P] * 12 + [i64, f32, f32, u32, P, vp]
+        L.gdr_linear_attention_workspace.argtypes = [i64, i64, i32, i32, i32, i32, ctypes.c_int]
+        L.gdr_block_norm_workspace.argtypes = [i64, i64]
+        for name in ("gdr_linear_attention_workspace", "gdr_block_norm_workspace"):
+            getattr(L, name).restype = i64
         L.gdr_ring_record_elements.argtypes = [i32, i32, i32]
         L.gdr_ring_record_elements.restype = ctypes.c_int64
         L.gdr_last_error_message.restype = ctypes.c_char_p
         L.gdr_version.restype = ctypes.c_char_p
-        for name in EXPORTS[:9]:
+        for name in EXPORTS[:14]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -250,6 +263,163 @@ def gdr_check_indices(rows, *, row_offsets=None, total_tokens=0, slots=None, num
 def gdr_set_debug_checks(enable):
     """Turn the per-call index checks on or off; returns the previous setting."""
     return bool(lib().gdr_set_debug_checks(1 if enable else 0))
+
+
+def _scratch(floats, like, stream):
+    """float32 workspace for a call on `stream` (torch's current one when None)."""
+    if floats <= 0:
+        return None
+    ws = torch.empty(floats, dtype=torch.float32, device=like.device)
+    if stream is not None:  # allocated on the current stream, used on the caller's
+        ws.record_stream(stream)
+    return ws
+
+
+def gdr_linear_attention_workspace(tokens, rows, num_key_heads, num_value_heads, key_head_dim,
+                                   value_head_dim, backward=False):
+    """float32 elements of workspace that one call needs (0: none)."""
+    return int(lib().gdr_linear_attention_workspace(tokens, rows, num_key_heads, num_value_heads,
+                                                    key_head_dim, value_head_dim,
+                                                    1 if backward else 0))
+
+
+def _attention_scratch(q, v, offsets, backward, workspace, stream):
+    if workspace is not None:
+        return workspace
+    n = gdr_linear_attention_workspace(q.shape[0], offsets.shape[0] - 1, q.shape[1], v.shape[1],
+                                       q.shape[2], v.shape[2], backward)
+    return _scratch(n, q, stream)
+
+
+def gdr_linear_attention_fwd(q, k, v, g, input_row_offsets, *, state=None, slot_idx=None,
+                             initial_state=None, final_state=None, output_final_state=False,
+                             scale=None, o=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head over ragged prompts:
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k [T, nk, K]; v [T, nv, V]; g [T, nv] log decay (expanded for a fixed
+    decay per head) or None.  Returns (o, final state): the pool itself,
+    updated in place at slot_idx, when `state` is given, else final_state
+    (allocated here when output_final_state is set), else None.  o and the
+    workspace are allocated here with torch when not passed in."""
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    if state is None and output_final_state and final_state is None:
+        dt = initial_state.dtype if initial_state is not None else torch.float32
+        final_state = torch.empty((input_row_offsets.shape[0] - 1, v.shape[1], q.shape[2],
+                                   v.shape[2]), dtype=dt, device=v.device)
+    ws = _attention_scratch(q, v, input_row_offsets, False, workspace, stream)
+    ds = [describe(x) for x in (o, q, k, v, g, input_row_offsets)]
+    more = [describe(x) for x in (initial_state, final_state, state, slot_idx, ws)]
+    rc = lib().gdr_linear_attention_fwd(*[_ref(d) for d in ds], _scale(scale),
+                                        *[_ref(d) for d in more], _stream(stream))
+    _check("gdr_linear_attention_fwd", rc)
+    return o, (state if state is not None else final_state)
+
+
+def gdr_linear_attention_step(q, k, v, g, state, slot_idx=None, *, scale=None, o=None,
+                              stream=None):
+    """One token for each row (q, k [B, nk, K]; v [B, nv, V]; g [B, nv] or
+    None), with the row's state updated in place in its slot.  Returns o."""
+    if o is None:
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    ds = [describe(x) for x in (o, q, k, v, g, state, slot_idx)]
+    rc = lib().gdr_linear_attention_step(*[_ref(d) for d in ds], _scale(scale), _stream(stream))
+    _check("gdr_linear_attention_step", rc)
+    return o
+
+
+def gdr_linear_attention_bwd(do, q, k, v, g, input_row_offsets, *, initial_state=None,
+                             dfinal_state=None, need_dg=True, need_dinitial_state=None,
+                             scale=None, dq=None, dk=None, dv=None, dg=None, dinitial_state=None,
+                             workspace=None, stream=None):
+    """Gradients of gdr_linear_attention_fwd (dense states).  Returns (dq, dk,
+    dv, dg, dinitial_state); dg is None without g or with need_dg=False,
+    dinitial_state None unless there is an initial_state (or
+    need_dinitial_state is set).  dg has one entry per token and head; a decay
+    that tokens share gets their sum.  Outputs and the workspace are allocated
+    here with torch when not passed in."""
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    dq = new(q) if dq is None else dq
+    dk = new(k) if dk is None else dk
+    dv = new(v) if dv is None else dv
+    if g is not None and need_dg and dg is None:
+        dg = new(g)
+    if need_dinitial_state is None:
+        need_dinitial_state = initial_state is not None
+    if need_dinitial_state and dinitial_state is None:
+        like = initial_state if initial_state is not None else dfinal_state
+        dt = like.dtype if like is not None else torch.float32
+        dinitial_state = torch.empty((input_row_offsets.shape[0] - 1, v.shape[1], q.shape[2],
+                                      v.shape[2]), dtype=dt, device=v.device)
+    ws = _attention_scratch(q, v, input_row_offsets, True, workspace, stream)
+    ds = [describe(x) for x in (do, q, k, v, g, input_row_offsets)]
+    more = [describe(x) for x in (initial_state, dfinal_state, dq, dk, dv, dg, dinitial_state,
+                                  ws)]
+    rc = lib().gdr_linear_attention_bwd(*[_ref(d) for d in ds], _scale(scale),
+                                        *[_ref(d) for d in more], _stream(stream))
+    _check("gdr_linear_attention_bwd", rc)
+    return dq, dk, dv, dg, dinitial_state
+
+
+_ACTIVATIONS = {None: 0, "sigmoid": GDR_FLAG_GATE_SIGMOID, "silu": GDR_FLAG_GATE_SILU}
+
+
+def gdr_block_norm(y, *, post_weight=None, group=0, gate=None, activation=None, residual=None,
+                   residual_scale=1.0, pre_weight=None, eps=1e-6, h=None, n=None, stream=None):
+    """The norms after and before a block, fused with its gate and residual
+    scale: p = y / rms_group(y) * post_weight, h = residual + residual_scale *
+    act(gate) * p, n = h / rms(h) * pre_weight.  y [T, D]; gate [T, D] or [D];
+    post_weight [D] or [group].  Every argument but y is optional.  Returns
+    (h, n), n None without pre_weight; both are allocated here with torch when
+    not passed in."""
+    if h is None:
+        h = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    if pre_weight is not None and n is None:
+        n = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+    ds = [describe(x) for x in (h, n, y, residual, gate, post_weight, pre_weight)]
+    rc = lib().gdr_block_norm(*[_ref(d) for d in ds], int(group), float(residual_scale),
+                              float(eps), _ACTIVATIONS[activation], _stream(stream))
+    _check("gdr_block_norm", rc)
+    return h, n
+
+
+def gdr_block_norm_workspace(tokens, dim):
+    """float32 elements of workspace that gdr_block_norm_bwd needs at most."""
+    return int(lib().gdr_block_norm_workspace(tokens, dim))
+
+
+def gdr_block_norm_bwd(dh, dn, y, h, *, post_weight=None, group=0, gate=None, activation=None,
+                       residual=True, residual_scale=1.0, pre_weight=None, eps=1e-6,
+                       dresidual=None, dy=None, dgate=None, dpost_weight=None, dpre_weight=None,
+                       workspace=None, stream=None):
+    """Gradients of gdr_block_norm given dh (of h, from everything but n) and
+    dn (of n, with pre_weight); h is the forward's output, needed with
+    pre_weight only.  Returns (dresidual, dgate, dy, dpost_weight,
+    dpre_weight), None for what the forward did not have.  Without pre_weight
+    dresidual is dh itself."""
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    dx = dresidual
+    if residual and dx is None and pre_weight is not None:
+        dx = new(y)
+    dy = new(y) if dy is None else dy
+    dgate = new(gate) if gate is not None and dgate is None else dgate
+    if post_weight is not None and dpost_weight is None:
+        dpost_weight = new(post_weight)
+    if pre_weight is not None and dpre_weight is None:
+        dpre_weight = new(pre_weight)
+    ws = workspace
+    if ws is None and y.dim() == 2:
+        ws = _scratch(gdr_block_norm_workspace(*y.shape), y, stream)
+    ds = [describe(x) for x in (dx, dy, dgate, dpost_weight, dpre_weight, dh, dn, y,
+                                h if pre_weight is not None else None, gate, post_weight,
+                                pre_weight)]
+    rc = lib().gdr_block_norm_bwd(*[_ref(d) for d in ds], int(group), float(residual_scale),
+                                  float(eps), _ACTIVATIONS[activation], _ref(describe(ws)),
+                                  _stream(stream))
+    _check("gdr_block_norm_bwd", rc)
+    return (dx if dx is not None else dh) if residual else None, dgate, dy, dpost_weight, \
+        dpre_weight
 
 
 def gdr_ring_record_elements(group, key_head_dim, value_head_dim):

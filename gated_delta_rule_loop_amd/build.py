@@ -21,13 +21,18 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdr.so")
 SOURCES = [os.path.join(CSRC, "gdr_api.cpp"), os.path.join(CSRC, "gdr_kernels.hip"),
-           os.path.join(CSRC, "gdr_conv.hip")]
+           os.path.join(CSRC, "gdr_conv.hip"), os.path.join(CSRC, "gdr_block_api.cpp"),
+           os.path.join(CSRC, "gdr_linattn.hip"), os.path.join(CSRC, "gdr_norm.hip")]
 TABLE_SOURCE = os.path.join(CSRC, "gdr_rec_table.hip")
 # (work type, state storage type, kernel mode) of each recurrence table:
 # types float or uint16_t (bf16 bits); modes kPlain 0, kVerify 1, kSnap 2,
 # plus kBetaCols 4 (per-column beta).
 TABLES = [(wt, st, mode) for wt in ("float", "uint16_t") for st in ("uint16_t", "float")
           for mode in (0, 1, 2, 4, 6)]
+
+# The walk kernels of linear attention, once per work type.
+WALK_SOURCE = os.path.join(CSRC, "gdr_linattn_walk.hip")
+WALKS = (("float", "f32"), ("uint16_t", "bf16"))
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -56,12 +61,17 @@ def compile_commands(objdir, defines=()):
         obj = os.path.join(objdir, f"table_{wt}_{st}_{mode}.o")
         jobs.append((obj, [HIPCC, *FLAGS, *defines, f"-DGDR_WT={wt}", f"-DGDR_ST={st}",
                            f"-DGDR_MODE={mode}", "-x", "hip", "-c", TABLE_SOURCE, "-o", obj]))
+    for wt, name in WALKS:
+        obj = os.path.join(objdir, f"walk_{name}.o")
+        jobs.append((obj, [HIPCC, *FLAGS, *defines, f"-DGDR_WT={wt}",
+                           f"-DGDR_LA_WALK=la_walks_{name}", f"-DGDR_LA_SEG=la_segments_{name}",
+                           "-x", "hip", "-c", WALK_SOURCE, "-o", obj]))
     return jobs
 
 
 def build(verbose: bool = False, defines=(), out: str = LIB, jobs: int | None = None) -> str:
     """Compile every translation unit in parallel and link libgdr.so."""
-    jobs = jobs or min(len(TABLES) + len(SOURCES), os.cpu_count() or 4)
+    jobs = jobs or min(len(TABLES) + len(SOURCES) + len(WALKS), os.cpu_count() or 4)
     with tempfile.TemporaryDirectory(prefix="gdr_build_") as objdir:
         units = compile_commands(objdir, defines)
         if verbose:

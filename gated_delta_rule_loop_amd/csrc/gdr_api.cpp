@@ -14,9 +14,10 @@
 #include <utility>
 #include <vector>
 
+#include "gdr_host.h"
 #include "gdr_internal.h"
 
-namespace {
+namespace gdr {
 
 thread_local std::string g_last_error;
 
@@ -112,6 +113,14 @@ int check_work_dtype(const char* fn, const char* name, const gdr_tensor* t, int3
 
 // Outer-stride multiple (in elements) that keeps 16-byte rows for a dtype.
 int64_t vec_mult(int32_t dtype) { return dtype == GDR_DTYPE_BF16 ? 8 : 4; }
+
+void clear_error() { g_last_error.clear(); }
+
+}  // namespace gdr
+
+using namespace gdr;
+
+namespace {
 
 bool head_dim_built(int64_t K) {
     return K == 16 || K == 32 || K == 64 || K == 128 || K == 256;
@@ -234,16 +243,9 @@ int fetch_indices(const char* fn, const char* name, const gdr_tensor* t, int64_t
     return GDR_OK;
 }
 
-// The checks of one call, on its device index vectors (nullptr: absent).
-struct IndexCheck {
-    const gdr_tensor* offsets = nullptr;
-    int64_t total_tokens = 0;
-    const gdr_tensor* slots = nullptr;
-    int64_t num_slots = 0;
-    const gdr_tensor* ring_idx = nullptr;
-    int64_t ring_rows = 0, ring_len = 0;
-    const gdr_tensor* accepted = nullptr;
-};
+}  // namespace
+
+namespace gdr {
 
 int run_debug_check(const char* fn, int64_t rows, const IndexCheck& c, void* stream) {
     if (!debug_checks_on()) return GDR_OK;
@@ -265,6 +267,21 @@ float resolve_scale(float scale, int64_t K) {
     if (!(scale > 0.0f)) return 1.0f / std::sqrt(static_cast<float>(K));
     return scale;
 }
+
+int hip_status(const char* fn, hipError_t e) {
+    if (e != hipSuccess)
+        return fail(GDR_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+    g_last_error.clear();
+    return GDR_OK;
+}
+
+const uint32_t* as_u32(const gdr_tensor* t) {
+    return present(t) ? static_cast<const uint32_t*>(t->data) : nullptr;
+}
+
+}  // namespace gdr
+
+namespace {
 
 // Launch shape, by entry and row length: about one token per row -> decode
 // tiles (one token per stage, high occupancy); short windows -> wider stages;
@@ -343,17 +360,6 @@ gdr::LaunchShape pick_shape(Entry e, int64_t K, int64_t V, int64_t G, int64_t to
     const int64_t units = G * tiles;
     s.wpg = units % 4 == 0 ? 4 : (units % 2 == 0 ? 2 : 1);
     return s;
-}
-
-int hip_status(const char* fn, hipError_t e) {
-    if (e != hipSuccess)
-        return fail(GDR_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
-    g_last_error.clear();
-    return GDR_OK;
-}
-
-const uint32_t* as_u32(const gdr_tensor* t) {
-    return present(t) ? static_cast<const uint32_t*>(t->data) : nullptr;
 }
 
 // Shared by the forward and the verify entry points.

@@ -75,7 +75,11 @@ extern "C" {
 /* gdr_causal_conv1d flag: apply SiLU, y * sigmoid(y), to the conv output. */
 #define GDR_FLAG_CONV_SILU 2u
 
-/* Head dims built: K == V in {16, 32, 64, 128, 256}; the fused update also
+/* gdr_block_norm flags: the gate's activation (none when neither is set). */
+#define GDR_FLAG_GATE_SIGMOID 4u
+#define GDR_FLAG_GATE_SILU 8u
+
+/* Head dims built (recurrence entries): K == V in {16, 32, 64, 128, 256}; the fused update also
  * takes (K, V) in {(64, 128), (128, 64), (128, 256), (256, 128)}. */
 #define GDR_MAX_HEAD_DIM 256
 
@@ -273,6 +277,149 @@ int gdr_causal_conv1d(const gdr_tensor* out, const gdr_tensor* x, const gdr_tens
                       const gdr_tensor* bias, const gdr_tensor* conv_state,
                       const gdr_tensor* slot_idx, const gdr_tensor* input_row_offsets,
                       uint32_t flags, void* stream);
+
+/*
+ * Linear attention with a decay for each head.  Per (row, value head) a K x V
+ * float32 state S is carried token by token:
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T;   o_t = scale S_t^T q_t
+ * (the recurrence above without its delta term).  Value head hv uses key head
+ * hv / (num_value_heads / num_key_heads).  Rows of more than a few tokens are
+ * computed in chunks as matrix products.
+ *
+ * Common arguments
+ *   q, k              [T, nk, K] work dtype: f32 or bf16 (float32 sums either
+ *                     way); K a multiple of 8 up to GDR_MAX_HEAD_DIM
+ *   v, o              [T, nv, V] work; nv a multiple of nk; V like K.  Heads
+ *                     and tokens take any strides that keep 16-byte rows, so
+ *                     channel ranges of a packed projection can be given as
+ *                     they are.
+ *   g                 [T, nv] f32 or bf16 log decay, any strides (a fixed
+ *                     decay per head: stride 0 over the tokens); -inf is a
+ *                     decay of 0; absent: no decay
+ *   input_row_offsets [B+1] u32|i32; tokens outside [off[0], off[B]) belong
+ *                     to no row, their outputs are not written
+ *   scale             <= 0 or NaN selects 1/sqrt(K)
+ *   workspace         f32 scratch of gdr_linear_attention_workspace() floats,
+ *                     16-byte aligned; may be absent when that is 0.  Held by
+ *                     the call until its work on `stream` is done.
+ * Outputs must not overlap inputs or one another.  A value that is not finite
+ * can reach every output of its row, but no other row's.
+ */
+
+/* Floats of workspace for one call (0: none), or -1 for arguments that are
+ * not positive.  `backward`: 0 for gdr_linear_attention_fwd, else for
+ * gdr_linear_attention_bwd.  Host only. */
+int64_t gdr_linear_attention_workspace(int64_t tokens, int64_t rows, int32_t num_key_heads,
+                                       int32_t num_value_heads, int32_t key_head_dim,
+                                       int32_t value_head_dim, int backward);
+
+/*
+ * gdr_linear_attention_fwd - ragged forward over prompts.
+ *   state             [slots, nv, K, V] bf16|f32 pool, read and written in
+ *                     place at slot_idx (at the row's number when slot_idx is
+ *                     absent); rows of length 0 leave their slot alone
+ *   slot_idx          [B] u32|i32; 0xFFFFFFFF marks a padding row (its tokens'
+ *                     outputs are +0.0, no state is touched)
+ *   initial_state     [B, nv, K, V] bf16|f32 or absent (zeros), and
+ *   final_state       [B, nv, K, V] (out) of the same dtype, or absent: dense
+ *                     states instead of a pool
+ */
+int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr_tensor* k,
+                             const gdr_tensor* v, const gdr_tensor* g,
+                             const gdr_tensor* input_row_offsets, float scale,
+                             const gdr_tensor* initial_state, const gdr_tensor* final_state,
+                             const gdr_tensor* state, const gdr_tensor* slot_idx,
+                             const gdr_tensor* workspace, void* stream);
+
+/*
+ * gdr_linear_attention_step - one token for each of T rows: token t is row t,
+ * with the state in slot slot_idx[t] (slot t when slot_idx is absent), updated
+ * in place.  Padding rows as above.
+ */
+int gdr_linear_attention_step(const gdr_tensor* o, const gdr_tensor* q, const gdr_tensor* k,
+                              const gdr_tensor* v, const gdr_tensor* g, const gdr_tensor* state,
+                              const gdr_tensor* slot_idx, float scale, void* stream);
+
+/*
+ * gdr_linear_attention_bwd - gradients of gdr_linear_attention_fwd with dense
+ * states:
+ *     D_t = scale q_t do_t^T + exp(g_{t+1}) D_{t+1}   (dfinal_state at the end)
+ *     dq_t = scale S_t do_t;  dk_t = D_t v_t;  dv_t = D_t^T k_t
+ *     dg_t = exp(g_t) <D_t, S_{t-1}>;  dinitial_state = exp(g_1) D_1
+ * dq and dk of a key head are the sums over its value heads.
+ *   do                [T, nv, V] work (in): gradient of o
+ *   initial_state     as in the forward, or absent
+ *   dfinal_state      [B, nv, K, V] bf16|f32: gradient of final_state, or
+ *                     absent (zeros)
+ *   dq, dk, dv        like q, k, v (out)
+ *   dg                [T, nv] f32|bf16 (out), any strides without overlap, or
+ *                     absent.  A decay that several tokens share gets the sum
+ *                     of its tokens' entries.
+ *   dinitial_state    [B, nv, K, V] bf16|f32 (out) or absent
+ * The sums' order is fixed: the same call gives the same bits.
+ */
+int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const gdr_tensor* k,
+                             const gdr_tensor* v, const gdr_tensor* g,
+                             const gdr_tensor* input_row_offsets, float scale,
+                             const gdr_tensor* initial_state, const gdr_tensor* dfinal_state,
+                             const gdr_tensor* dq, const gdr_tensor* dk, const gdr_tensor* dv,
+                             const gdr_tensor* dg, const gdr_tensor* dinitial_state,
+                             const gdr_tensor* workspace, void* stream);
+
+/*
+ * gdr_block_norm - the norms after and before a block, fused with the block's
+ * gate and residual scale:
+ *     p = y / sqrt(mean_group(y^2) + eps) * post_weight   (post_weight absent: p = y)
+ *     h = residual + residual_scale * act(gate) * p       (each factor or term if given)
+ *     n = h / sqrt(mean(h^2) + eps) * pre_weight          (with pre_weight)
+ * float32 arithmetic; n is computed from h before h is rounded.
+ *   y                 [T, D] work dtype: f32 or bf16; D a multiple of 8 up to
+ *                     16384; 16-byte rows at any stride, as for every [T, D]
+ *                     argument
+ *   group             the post-norm's means are over groups of this many
+ *                     neighbouring values (a multiple of 8 that divides D: the
+ *                     head dim of a norm per head); <= 0: the whole row
+ *   post_weight       [D], or [group] when all groups share it; f32 or work
+ *   gate              [T, D] work, or [D] f32 or work (a learned gate for each
+ *                     channel), or absent
+ *   residual          [T, D] work or absent
+ *   pre_weight        [D] f32 or work, or absent
+ *   h                 [T, D] work (out); may be residual or y themselves
+ *   n                 [T, D] work (out), given exactly when pre_weight is
+ *   flags             GDR_FLAG_GATE_SIGMOID or GDR_FLAG_GATE_SILU, or 0
+ */
+int gdr_block_norm(const gdr_tensor* h, const gdr_tensor* n, const gdr_tensor* y,
+                   const gdr_tensor* residual, const gdr_tensor* gate,
+                   const gdr_tensor* post_weight, const gdr_tensor* pre_weight, int64_t group,
+                   float residual_scale, float eps, uint32_t flags, void* stream);
+
+/* Floats of workspace that gdr_block_norm_bwd needs at most for [tokens, dim]
+ * rows, or -1 for arguments out of range.  Host only. */
+int64_t gdr_block_norm_workspace(int64_t tokens, int64_t dim);
+
+/*
+ * gdr_block_norm_bwd - gradients of gdr_block_norm.
+ *   dh                [T, D] work (in): gradient of h from everything but n
+ *   dn                [T, D] work (in), with pre_weight: gradient of n
+ *   y, gate, post_weight, pre_weight, group, residual_scale, eps, flags
+ *                     as in the forward; h [T, D] the forward's output,
+ *                     needed with pre_weight only
+ *   dresidual         [T, D] work (out) or absent.  Without pre_weight the
+ *                     residual's gradient is dh itself.
+ *   dy                [T, D] work (out)
+ *   dgate             like gate (out; a [D] gate's in f32 or work), with gate
+ *   dpost_weight      like post_weight (out, f32 or work), with post_weight
+ *   dpre_weight       [D] (out, f32 or work), with pre_weight
+ *   workspace         f32 scratch of gdr_block_norm_workspace() floats
+ * Outputs must not share memory with one another.  Sums over the tokens are
+ * float32 in a fixed order: the same call gives the same bits.
+ */
+int gdr_block_norm_bwd(const gdr_tensor* dresidual, const gdr_tensor* dy, const gdr_tensor* dgate,
+                       const gdr_tensor* dpost_weight, const gdr_tensor* dpre_weight,
+                       const gdr_tensor* dh, const gdr_tensor* dn, const gdr_tensor* y,
+                       const gdr_tensor* h, const gdr_tensor* gate, const gdr_tensor* post_weight,
+                       const gdr_tensor* pre_weight, int64_t group, float residual_scale,
+                       float eps, uint32_t flags, const gdr_tensor* workspace, void* stream);
 
 /*
  * gdr_fwd_output_shape - shape of recurrence_output for the given conv
