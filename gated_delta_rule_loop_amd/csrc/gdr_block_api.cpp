@@ -119,7 +119,8 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     const int64_t want = ceil_div(512, per_seg);
     p.segs = B;
     if (B < want) {
-        const int64_t len = std::max<int64_t>(256, ceil_div(ceil_div(T, want), 64) * 64);
+        const int64_t full = std::max<int64_t>(1, want - B / 2);  // rows end in part segments
+        const int64_t len = std::max<int64_t>(256, ceil_div(ceil_div(T, full), 64) * 64);
         if (len < T) {
             p.seg_len = len;
             p.segs = T / len + B;

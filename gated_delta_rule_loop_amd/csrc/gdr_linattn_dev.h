@@ -7,6 +7,7 @@
 namespace gdr {
 
 typedef float la_f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t la_u4 __attribute__((ext_vector_type(4)));
 typedef short la_s4 __attribute__((ext_vector_type(4)));
 typedef short la_s8 __attribute__((ext_vector_type(8)));
 typedef __bf16 la_b4 __attribute__((ext_vector_type(4)));

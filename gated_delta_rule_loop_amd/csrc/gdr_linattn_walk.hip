@@ -112,11 +112,14 @@ __device__ __forceinline__ void split(la_f4 v, typename Mat<T>::Fr (&out)[N]) {
 }
 
 // KP: Kd rounded up to the built size (the rest is zeros); 64 * NT columns per
-// workgroup; C tokens per chunk; SEG: only the segment's own sum of the state.
-template <typename T, int KP, int NT, int C, bool SEG>
+// workgroup; C tokens per chunk.  Modes: the walk; the walk with the sums for the
+// decays' gradient; only the segment's own sum of the state.
+enum { kWalk = 0, kWalkSums = 1, kSegment = 2 };
+template <typename T, int KP, int NT, int C, int MODE>
 __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* __restrict__ tot) {
     typedef Mat<T> M;
     typedef typename M::Fr Fr;
+    constexpr bool SEG = MODE == kSegment, SUMS = MODE == kWalkSums;
     constexpr int N = M::kTerms;
     constexpr int VEC = M::kVec;
     constexpr int XS = KP + VEC;          // LDS row strides: one 16-byte slot of padding
@@ -139,8 +142,9 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     const int id = la_logical(blockIdx.x, gridDim.x);
     const int tile = id % p.max_tiles;
     const int wi = (id / p.max_tiles) % p.nwalks;
-    const int head = (id / (p.max_tiles * p.nwalks)) % p.nv;
-    const int seg = id / (p.max_tiles * p.nwalks * p.nv);
+    // segments before heads: those past the last one are spread over the dies
+    const int seg = (id / (p.max_tiles * p.nwalks)) % p.segs;
+    const int head = id / (p.max_tiles * p.nwalks * p.segs);
     const LaWalk& w = p.w[wi];
     if (tile >= w.tiles) return;
     LaSpan sp;
@@ -151,101 +155,122 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     const int zbase = tile * ZC + wave * 16 * NT;   // this wave's columns
     const int lz = wave * 16 * NT;                  // the same within the workgroup's
     const uint32_t slot = p.slot_idx ? p.slot_idx[sp.row] : static_cast<uint32_t>(sp.row);
-    const bool at_last = w.reverse ? sp.s == 0 : sp.s == sp.count - 1;
+    const bool at_last = w.reverse != 0 ? sp.s == 0 : sp.s == sp.count - 1;
     if (SEG && at_last) return;           // no later segment needs its sum
 
+    const bool third = w.third != 0, reverse = w.reverse != 0, out_f32 = w.out_f32 != 0;
+    const bool sums = SUMS && w.row_sum != nullptr;
+    char* const out = static_cast<char*>(w.out);
+    const int64_t out_tok = w.out_tok, out_head = w.out_head;
+
     // Walk position r is token start + dir * r.
-    const int64_t start = w.reverse ? int64_t{sp.t0} + n - 1 : sp.t0;
-    const int64_t dir = w.reverse ? -1 : 1;
+    const int64_t start = reverse ? int64_t{sp.t0} + n - 1 : sp.t0;
+    const int64_t dir = reverse ? -1 : 1;
     if (!SEG && slot == kPadSlot) {       // a padding row: zeros out, no state
-        if (w.out_f32) {
-            float* out = static_cast<float*>(w.out) + head * w.out_head;
-            for (int64_t i = tid; i < int64_t{n} * ZC; i += 256) {
-                const int z = tile * ZC + static_cast<int>(i % ZC);
-                if (z < Vd) out[(sp.t0 + i / ZC) * w.out_tok + z] = 0.0f;
-            }
-        } else {
-            T* out = static_cast<T*>(w.out) + head * w.out_head;
-            for (int64_t i = tid; i < int64_t{n} * ZC; i += 256) {
-                const int z = tile * ZC + static_cast<int>(i % ZC);
-                if (z < Vd) out[(sp.t0 + i / ZC) * w.out_tok + z] = T(0);
+        for (int64_t i = tid; i < int64_t{n} * ZC; i += 256) {
+            const int z = tile * ZC + static_cast<int>(i % ZC);
+            const int64_t at = (sp.t0 + i / ZC) * out_tok + head * out_head + z;
+            if (z < Vd) {
+                if (out_f32) reinterpret_cast<float*>(out)[at] = 0.0f;
+                else reinterpret_cast<T*>(out)[at] = T(0);
             }
         }
         return;
     }
 
-    const T* xp = static_cast<const T*>(w.x.p) + (head / w.x.div) * w.x.head + start * w.x.tok;
-    const T* yp = static_cast<const T*>(w.y.p) + (head / w.y.div) * w.y.head + start * w.y.tok;
-    const T* zp = static_cast<const T*>(w.z.p) + (head / w.z.div) * w.z.head + start * w.z.tok +
-                  tile * ZC;
-    const int64_t xt = dir * w.x.tok, yt = dir * w.y.tok, zt_ = dir * w.z.tok;
-
-    // ---- the state
+    // ---- the state.  All loads are issued together: indices past the state
+    // are clamped into it and their values replaced.
     la_f4 S[KT][NT];
+    auto load_as = [&](const LaState& s, auto* base, auto&& use) {
+        base += (s.by_segment ? int64_t{seg} : int64_t{slot}) * s.outer + head * s.head;
+        int zo[NT];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int zt = 0; zt < NT; ++zt) S[kt][zt] = la_f4{0, 0, 0, 0};
-    auto load_state = [&](const LaState& s, auto&& use) {
-        const int64_t base = (s.by_segment ? int64_t{seg} : int64_t{slot}) * s.outer +
-                             head * s.head;
+        for (int zt = 0; zt < NT; ++zt) zo[zt] = min(zbase + zt * 16 + i16, Vd - 1) * s.sz;
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int zt = 0; zt < NT; ++zt)
+            for (int zt = 0; zt < NT; ++zt) {
+                la_f4 v;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int kd = kt * 16 + g4 + r, z = zbase + zt * 16 + i16;
-                    if (kd < Kd && z < Vd)
-                        use(kt, zt, r, s.mult * la_load(s.p, base + int64_t{kd} * s.sk +
-                                                                 int64_t{z} * s.sz, s.bf16));
+                    const int kd = kt * 16 + g4 + r;
+                    const auto raw = base[min(kd, Kd - 1) * s.sk + zo[zt]];
+                    float f;
+                    if constexpr (sizeof(raw) == 2) f = la_widen(raw);
+                    else f = raw;
+                    v[r] = kd < Kd && zbase + zt * 16 + i16 < Vd ? s.mult * f : 0.0f;
                 }
+                use(kt, zt, v);
+            }
     };
-    if (!SEG && w.in.p)
-        load_state(w.in, [&](int kt, int zt, int r, float v) { S[kt][zt][r] = v; });
+    auto load_state = [&](const LaState& s, auto&& use) {
+        if (s.bf16) load_as(s, static_cast<const uint16_t*>(s.p), use);
+        else load_as(s, static_cast<const float*>(s.p), use);
+    };
+    if (!SEG && w.in.p) {
+        load_state(w.in, [&](int kt, int zt, la_f4 v) { S[kt][zt] = v; });
+    } else {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int zt = 0; zt < NT; ++zt) S[kt][zt] = la_f4{0, 0, 0, 0};
+    }
 
-    // ---- a chunk's loads, held in registers until its LDS is free
-    uint4 px[SEG ? 1 : XV], py[XV], pz[ZV];
+    // ---- a chunk's loads, held in registers until its LDS is free.  They are
+    // unconditional too: rows past the end and columns past the head dim are
+    // clamped, and written to LDS as zeros.
+    constexpr int XR = 256 / (KP / VEC), ZR = 256 / (ZC / VEC);  // rows per load
+    const int xr0 = tid / (KP / VEC), xc = tid % (KP / VEC) * VEC;
+    const int zr0 = tid / (ZC / VEC), zc = tid % (ZC / VEC) * VEC;
+    const bool xok = xc < Kd, zok = tile * ZC + zc < Vd;
+    const int64_t xt = dir * w.x.tok, yt = dir * w.y.tok, zt_ = dir * w.z.tok;
+    const T* xp = static_cast<const T*>(w.x.p) + (head / w.x.div) * w.x.head + start * w.x.tok +
+                  (xok ? xc : 0);
+    const T* yp = static_cast<const T*>(w.y.p) + (head / w.y.div) * w.y.head + start * w.y.tok +
+                  (xok ? xc : 0);
+    const T* zp = static_cast<const T*>(w.z.p) + (head / w.z.div) * w.z.head + start * w.z.tok +
+                  (zok ? tile * ZC + zc : 0);
+    la_u4 px[SEG ? 1 : XV], py[XV], pz[ZV];
     float pg = 0.0f;
     const int64_t gdir = dir * p.g_tok;
     const char* gp = static_cast<const char*>(p.g) +
                      (start * p.g_tok + head * p.g_head) * (p.g_bf16 ? 2 : 4);
     auto fetch = [&](int c0) {
-        const int m = n - c0;             // tokens left
+        const int m = n - 1 - c0;         // the last token's place in the chunk
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
-            const int v = tid + 256 * i, r = v / (KP / VEC), c = v % (KP / VEC) * VEC;
-            const bool ok = r < m && c < Kd;
-            if constexpr (!SEG)
-                px[i] = ok ? *reinterpret_cast<const uint4*>(xp + (c0 + r) * xt + c)
-                           : make_uint4(0, 0, 0, 0);
-            py[i] = ok ? *reinterpret_cast<const uint4*>(yp + (c0 + r) * yt + c)
-                       : make_uint4(0, 0, 0, 0);
+            const int r = c0 + min(xr0 + i * XR, m);
+            if constexpr (!SEG) px[i] = *reinterpret_cast<const la_u4*>(xp + r * xt);
+            py[i] = *reinterpret_cast<const la_u4*>(yp + r * yt);
         }
 #pragma unroll
-        for (int i = 0; i < ZV; ++i) {
-            const int v = tid + 256 * i, r = v / (ZC / VEC), c = v % (ZC / VEC) * VEC;
-            pz[i] = r < m && tile * ZC + c < Vd
-                        ? *reinterpret_cast<const uint4*>(zp + (c0 + r) * zt_ + c)
-                        : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < ZV; ++i)
+            pz[i] = *reinterpret_cast<const la_u4*>(zp + (c0 + min(zr0 + i * ZR, m)) * zt_);
+        if (p.g && wave == 0) {
+            const int64_t at = (c0 + min(lane, m)) * gdir;
+            pg = p.g_bf16 ? la_widen(reinterpret_cast<const uint16_t*>(gp)[at])
+                          : reinterpret_cast<const float*>(gp)[at];
         }
-        pg = p.g && tid < C && tid < m ? la_load(gp, (c0 + tid) * gdir, p.g_bf16) : 0.0f;
     };
     double walked = 0.0;                  // log2 decay of the chunks before (SEG)
-    auto stage = [&]() {
+    auto stage = [&](int c0) {
+        const int m = n - c0;
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
-            const int v = tid + 256 * i, r = v / (KP / VEC), c = v % (KP / VEC) * VEC;
-            if constexpr (!SEG) *reinterpret_cast<uint4*>(&Xs[r * XS + c]) = px[i];
-            *reinterpret_cast<uint4*>(&Ys[r * XS + c]) = py[i];
+            const int r = xr0 + i * XR;
+            const uint32_t keep = xok && r < m ? ~0u : 0u;
+            if constexpr (!SEG) *reinterpret_cast<la_u4*>(&Xs[r * XS + xc]) = px[i] & keep;
+            *reinterpret_cast<la_u4*>(&Ys[r * XS + xc]) = py[i] & keep;
         }
 #pragma unroll
         for (int i = 0; i < ZV; ++i) {
-            const int v = tid + 256 * i, r = v / (ZC / VEC), c = v % (ZC / VEC) * VEC;
-            *reinterpret_cast<uint4*>(&Zs[r * ZS + c]) = pz[i];
+            const int r = zr0 + i * ZR;
+            const uint32_t keep = zok && r < m ? ~0u : 0u;
+            *reinterpret_cast<la_u4*>(&Zs[r * ZS + zc]) = pz[i] & keep;
         }
         if (wave == 0) {                  // the chunk's decay exponents, base 2
-            const double own_g = static_cast<double>(la_clamp_g(pg)) * kLog2e;
+            const double own_g = lane < C && lane < m ? static_cast<double>(la_clamp_g(pg)) * kLog2e
+                                                      : 0.0;
             double sum = own_g;
 #pragma unroll
             for (int d = 1; d < C; d <<= 1) {
@@ -253,7 +278,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                 if (lane >= d) sum += up;
             }
             const double all = __shfl(sum, C - 1);
-            if (w.reverse) sum -= own_g;
+            if (reverse) sum -= own_g;
             if (lane < C) {
                 const float hi = static_cast<float>(sum);
                 g_hi[lane] = hi;
@@ -267,9 +292,9 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     };
 
     const float scale = p.scale;
-    fetch(0);
+    if (n > 0) fetch(0);
     for (int c0 = 0; c0 < n; c0 += C) {
-        stage();
+        stage(c0);
         __syncthreads();
         if (c0 + C < n) fetch(c0 + C);
         la_f4 O[SEG ? 1 : IT][NT];
@@ -321,8 +346,8 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                 for (int r = 0; r < 4; ++r) {
                     const int j = jt * 16 + g4 + r;
                     const float e = exp2f((hi - g_hi[j]) + (lo - g_lo[j]));
-                    if (i == j) own[i] = acc[r];
-                    const bool keep = w.row_sum ? j < i : j <= i;
+                    if (SUMS && i == j) own[i] = acc[r];
+                    const bool keep = sums ? j < i : j <= i;
                     acc[r] = keep ? acc[r] * e : 0.0f;
                 }
                 Fr pf[N];
@@ -354,8 +379,11 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                         for (int zt = 0; zt < NT; ++zt)
                             O[it][zt] = M::mma(zf[jt][zt], zf[jt + 1][zt], p0, p1, O[it][zt]);
                     }
-            if (w.row_sum) {
+            if (sums) {
                 // partner . out without the token's own pair, then that pair
+                const int64_t qt = dir * w.partner.tok;
+                const T* qp = static_cast<const T*>(w.partner.p) +
+                              (head / w.partner.div) * w.partner.head + start * w.partner.tok;
                 float* rs = w.row_sum + (int64_t{tile} * kLaWaves + wave) * p.nv * p.T +
                             int64_t{head} * p.T;
 #pragma unroll
@@ -365,14 +393,11 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
 #pragma unroll
                     for (int zt = 0; zt < NT; ++zt) {
                         const int z = zbase + zt * 16 + g4;
-                        if (c0 + i < n && z < Vd) {
-                            const T* q = static_cast<const T*>(w.partner.p) +
-                                         (head / w.partner.div) * w.partner.head +
-                                         (start + dir * (c0 + i)) * w.partner.tok + z;
-                            const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(q));
+                        const T* q = qp + min(c0 + i, n - 1) * qt + min(z, Vd - 4);
+                        const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(q));
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) sum = fmaf(a[r], O[it][zt][r], sum);
-                        }
+                        for (int r = 0; r < 4; ++r)
+                            sum = z < Vd ? fmaf(a[r], O[it][zt][r], sum) : sum;
                     }
                     sum += __shfl_xor(sum, 16);
                     sum += __shfl_xor(sum, 32);
@@ -390,16 +415,16 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
             for (int it = 0; it < IT; ++it) {
                 const int i = it * 16 + i16;
                 if (c0 + i < n) {
-                    const int64_t at = (start + dir * (c0 + i)) * w.out_tok + head * w.out_head;
+                    const int64_t at = (start + dir * (c0 + i)) * out_tok + head * out_head;
 #pragma unroll
                     for (int zt = 0; zt < NT; ++zt) {
                         const int z = zbase + zt * 16 + g4;
                         if (z < Vd) {
                             const la_f4 o = O[it][zt] * scale;
-                            if (w.out_f32)
-                                *reinterpret_cast<la_f4*>(static_cast<float*>(w.out) + at + z) = o;
+                            if (out_f32)
+                                *reinterpret_cast<la_f4*>(reinterpret_cast<float*>(out) + at + z) = o;
                             else
-                                *reinterpret_cast<Fr*>(static_cast<T*>(w.out) + at + z) =
+                                *reinterpret_cast<Fr*>(reinterpret_cast<T*>(out) + at + z) =
                                     M::narrow(o);
                         }
                     }
@@ -433,7 +458,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                     for (int u = 0; u < N; ++u)
                         S[kt][zt] = M::mma(y0, y1, z0[zt][u], z1[zt][u], S[kt][zt]);
                     if constexpr (NW == 3)
-                        if (w.third)
+                        if (third)
                             S[kt][zt] = M::mma(y0, y1, z0[zt][2], z1[zt][2], S[kt][zt]);
                 }
             }
@@ -442,7 +467,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     }
 
     // ---- what is left
-    auto store_state = [&](const LaState& s, int64_t base) {
+    auto store_as = [&](const LaState& s, auto* base) {
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -450,22 +475,29 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int kd = kt * 16 + g4 + r, z = zbase + zt * 16 + i16;
-                    if (kd < Kd && z < Vd)
-                        la_store(s.p, base + int64_t{kd} * s.sk + int64_t{z} * s.sz, s.bf16,
-                                 s.mult * S[kt][zt][r]);
+                    if (kd < Kd && z < Vd) {
+                        const float v = s.mult * S[kt][zt][r];
+                        if constexpr (sizeof(*base) == 2) base[kd * s.sk + z * s.sz] = la_round(v);
+                        else base[kd * s.sk + z * s.sz] = v;
+                    }
                 }
+    };
+    auto store_state = [&](const LaState& s, int64_t at) {
+        if (s.bf16) store_as(s, static_cast<uint16_t*>(s.p) + at);
+        else store_as(s, static_cast<float*>(s.p) + at);
     };
     if (SEG) {
         store_state(w.last, int64_t{seg} * w.last.outer + head * w.last.head);
         if (tid == 0 && tile == 0 && tot)
-            tot[(int64_t{w.reverse} * p.segs + seg) * p.nv + head] = static_cast<float>(walked);
+            tot[(int64_t{reverse} * p.segs + seg) * p.nv + head] = static_cast<float>(walked);
         return;
     }
-    if (w.phi) {
+    if (SUMS && w.phi) {
         float sum = 0.0f;
         if (w.phi_in.p)
-            load_state(w.phi_in, [&](int kt, int zt, int r, float v) {
-                sum = fmaf(S[kt][zt][r], v, sum);
+            load_state(w.phi_in, [&](int kt, int zt, la_f4 v) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum = fmaf(S[kt][zt][r], v[r], sum);
             });
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
@@ -477,30 +509,35 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
         store_state(w.last, int64_t{slot} * w.last.outer + head * w.last.head);
 }
 
-template <int KP, int NT, int C, bool SEG>
+template <int KP, int NT, int C, int MODE>
 hipError_t run(const LaParams& p, float* tot, hipStream_t s) {
     const int64_t blocks = int64_t{p.segs} * p.nv * p.nwalks * p.max_tiles;
-    walk_kernel<GDR_WT, KP, NT, C, SEG><<<dim3(static_cast<uint32_t>(blocks)), 256, 0, s>>>(p, tot);
+    walk_kernel<GDR_WT, KP, NT, C, MODE><<<dim3(static_cast<uint32_t>(blocks)), 256, 0, s>>>(p, tot);
     return hipGetLastError();
 }
 
 // The walks of one call that share a built shape, in one launch.
-template <bool SEG>
+template <int MODE>
 hipError_t dispatch(const LaParams& p, float* tot, hipStream_t s) {
     const int Kd = p.w[0].Kd, cols = la_columns(Kd, p.w[0].Vd);
     constexpr bool b16 = sizeof(GDR_WT) == 2;
     constexpr int C = b16 ? 64 : 32;
-    if (Kd <= 64) return cols == 64 ? run<64, 1, C, SEG>(p, tot, s) : run<64, 2, C, SEG>(p, tot, s);
+    if (Kd <= 64)
+        return cols == 64 ? run<64, 1, C, MODE>(p, tot, s) : run<64, 2, C, MODE>(p, tot, s);
     if (Kd <= 128)
-        return cols == 64 ? run<128, 1, C, SEG>(p, tot, s) : run<128, 2, C, SEG>(p, tot, s);
-    return run<256, 1, 32, SEG>(p, tot, s);
+        return cols == 64 ? run<128, 1, C, MODE>(p, tot, s) : run<128, 2, C, MODE>(p, tot, s);
+    return run<256, 1, 32, MODE>(p, tot, s);
 }
 
 }  // namespace
 
-hipError_t GDR_LA_WALK(const LaParams& p, hipStream_t s) { return dispatch<false>(p, nullptr, s); }
+hipError_t GDR_LA_WALK(const LaParams& p, hipStream_t s) {
+    bool sums = false;
+    for (int i = 0; i < p.nwalks; ++i) sums = sums || p.w[i].row_sum != nullptr;
+    return sums ? dispatch<kWalkSums>(p, nullptr, s) : dispatch<kWalk>(p, nullptr, s);
+}
 hipError_t GDR_LA_SEG(const LaParams& p, float* tot, hipStream_t s) {
-    return dispatch<true>(p, tot, s);
+    return dispatch<kSegment>(p, tot, s);
 }
 
 }  // namespace gdr
