@@ -2,6 +2,7 @@
 // include/gdr.h: argument validation, workspace layout, launch choice.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <initializer_list>
 
 #include "gdr_host.h"
@@ -14,13 +15,20 @@ namespace {
 
 typedef long long ll;
 
+constexpr int64_t kLaMaxTokenStride = (int64_t{1} << 24) - 1;
+
 // [tokens, heads, dim] operand: unit innermost stride, 16-byte rows.
 int check_heads(const char* fn, const char* name, const gdr_tensor* t, int64_t T, int64_t heads,
                 int64_t dim, int32_t work) {
     const int64_t shape[3] = {T, heads, dim};
     int rc = check_tensor(fn, name, t, 3, shape, true, true, false);
     if (rc || (rc = check_work_dtype(fn, name, t, work))) return rc;
-    return check_layout(fn, name, t, vec_mult(work));
+    if ((rc = check_layout(fn, name, t, vec_mult(work)))) return rc;
+    // the kernels address a chunk's tokens from one 64-bit base by 32-bit offsets
+    if (T > 1 && heads > 0 && std::llabs(t->stride[0]) > kLaMaxTokenStride)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a token stride above %lld elements", fn, name,
+                    static_cast<ll>(kLaMaxTokenStride));
+    return GDR_OK;
 }
 
 // Outputs are written by many workgroups: no two elements may share memory.
@@ -65,7 +73,7 @@ int check_la_state(const char* fn, const char* name, const gdr_tensor* t, int64_
 LaTensor la_tensor(const gdr_tensor* t, int64_t div) {
     LaTensor r{};
     r.p = t->data;
-    r.tok = t->stride[0];
+    r.tok = t->shape[0] > 1 ? t->stride[0] : 0;  // a single token's stride can be anything
     r.head = t->stride[1];
     r.div = static_cast<int32_t>(div);
     return r;
@@ -399,7 +407,7 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
     LaParams p = la_params(d, pl, input_row_offsets, slot_idx, g, sc);
     LaWalk w = la_walk(la_tensor(q, G), la_tensor(k, G), la_tensor(v, 1), d.K, d.V, false);
     w.out = o->data;
-    w.out_tok = o->stride[0];
+    w.out_tok = d.T > 1 ? o->stride[0] : 0;
     w.out_head = o->stride[1];
     w.in = in;
     w.last = last;
@@ -539,7 +547,7 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         wk.in = la_segment_state(sr, d.nv, d.K, d.V, true);
     }
     wv.out = dv->data;
-    wv.out_tok = dv->stride[0];
+    wv.out_tok = d.T > 1 ? dv->stride[0] : 0;
     wv.out_head = dv->stride[1];
     if (parts) {
         wq.out = ws + pl.pq;
@@ -549,10 +557,10 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         wq.out_f32 = wk.out_f32 = 1;
     } else {
         wq.out = dq->data;
-        wq.out_tok = dq->stride[0];
+        wq.out_tok = d.T > 1 ? dq->stride[0] : 0;
         wq.out_head = dq->stride[1];
         wk.out = dk->data;
-        wk.out_tok = dk->stride[0];
+        wk.out_tok = d.T > 1 ? dk->stride[0] : 0;
         wk.out_head = dk->stride[1];
     }
     if (sums) {
@@ -592,7 +600,6 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         c.dg_tok = dg->stride[0];
         c.dg_head = dg->stride[1];
         c.dg_bf16 = dg->dtype == GDR_DTYPE_BF16;
-        c.scale = sc;
         e = launch_la_decay_grad(c, s);
     }
     if (parts && d.T > 0) {

@@ -48,7 +48,7 @@ struct LaWalk {
     LaState in, last;
     // Sums for the decays' gradient (row_sum != nullptr): row_sum[part, head,
     // token] += partner . out without the token's own pair, and phi[segment,
-    // head, part] = <state at the walk's end, phi_in>.
+    // head, part] = scale <state at the walk's end, phi_in>.
     LaTensor partner;
     float* row_sum;
     float* phi;
@@ -93,7 +93,6 @@ struct LaDecayGrad {
     const float* rk; int32_t rk_parts;
     const float* phi; int32_t phi_parts; // [segs, nv, parts] or nullptr
     void* dg; int64_t dg_tok, dg_head; int32_t dg_bf16;
-    float scale;
 };
 
 struct LaHeadSum {          // out[t, hk, :] = sum over the group of part[t, hv, :]

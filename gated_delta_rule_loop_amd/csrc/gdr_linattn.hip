@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const LaDecayGrad p) {
         }
         if (r < sp.n)
             la_store(p.dg, t * p.dg_tok + head * p.dg_head, p.dg_bf16,
-                     static_cast<float>(p.scale * (before + v)));
+                     static_cast<float>(before + v));
         carry += all;
         __syncthreads();
     }

@@ -76,17 +76,18 @@ __device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_le
         const uint64_t past = __ballot(base + sum > seg);
         if (past) {
             const int at = __ffsll(static_cast<unsigned long long>(past)) - 1;
+            auto of = [at](int v) { return __builtin_amdgcn_readlane(v, at); };
             o.row = b0 + at;
-            o.count = __shfl(c, at);
-            o.first = base + __shfl(sum, at) - o.count;
+            o.count = of(c);
+            o.first = base + of(sum) - o.count;
             o.s = seg - o.first;
-            const int ra = __shfl(a, at), rn = __shfl(n, at);
+            const int ra = of(a), rn = of(n);
             o.t0 = ra + o.s * seg_len;
             o.n = min(seg_len, rn - o.s * seg_len);
             if (o.n < 0) o.n = 0;
             return true;
         }
-        base += __shfl(sum, 63);
+        base += __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
 }

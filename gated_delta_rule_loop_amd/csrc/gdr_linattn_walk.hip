@@ -43,7 +43,17 @@ template <typename T> struct Mat;
 
 template <> struct Mat<uint16_t> {
     typedef la_s4 Fr;
-    enum { kTerms = 2, kVec = 8 };    // kVec: elements per 16 bytes
+    enum { kTerms = 2, kVec = 8, kPad = 0 };  // kVec: elements per 16 bytes
+    // Place of (row r0 + r, column c), r0 a multiple of 16, in a tile of rows
+    // of S elements (64 at least).  The 16-byte slots of a row are permuted by
+    // the row's number, so that neither the reads along rows (16 rows, 16
+    // bytes each) nor the transposing reads (8 rows, 32 bytes each) meet in a
+    // bank.  With padded rows one of the two did: 42% of the LDS cycles.
+    static __device__ __forceinline__ int at(int r0, int r, int c, int S) {
+        // rows of 64 lie two to a round of the banks: the row's parity tells them apart
+        const int h = S == 64 ? ((r >> 1 & 3) << 1 | r >> 3) : ((r & 7) << 1 | (r >> 3 & 1));
+        return (r0 + r) * S + (((c >> 3) ^ h) << 3) + (c & 7);
+    }
     // D[a][b] += sum over 32: two fragments of 16 on each side
     static __device__ __forceinline__ la_f4 mma(Fr a0, Fr a1, Fr b0, Fr b1, la_f4 c) {
         const la_s8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -54,12 +64,17 @@ template <> struct Mat<uint16_t> {
     static __device__ __forceinline__ Fr row(const uint16_t* p) {
         return *reinterpret_cast<const la_s4*>(p);
     }
-    // rows 4 * (lane / 16) + e, column lane % 16 of the 16 x 16 block at p
-    static __device__ __forceinline__ Fr col(const uint16_t* p, int stride, int lane) {
-        const int g = lane >> 4, i = lane & 15;
-        auto* q = (__attribute__((address_space(3))) la_s4*)(p + (4 * g + (i >> 2)) * stride +
-                                                             (i & 3) * 4);
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(q);
+    // The same for column c + 16 ct from the place `a` of column c (below 16):
+    // only the slot's number changes, by bits that are zero in it.
+    static __device__ __forceinline__ int step(int a, int ct) { return a ^ (ct * 16); }
+    // A fragment with rows r0 + 4 * (lane / 16) + e, column lane % 16 of a 16 x 16
+    // block is read from `a`, the place of its own lane
+    static __device__ __forceinline__ int col_place(int lane, int S) {
+        return at(0, 4 * (lane >> 4) + ((lane & 15) >> 2), (lane & 3) * 4, S);
+    }
+    static __device__ __forceinline__ Fr col(const uint16_t* p, int) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) la_s4*)p);
     }
     static __device__ __forceinline__ la_f4 widen(Fr f) {
         la_f4 r;
@@ -77,7 +92,10 @@ template <> struct Mat<uint16_t> {
 
 template <> struct Mat<float> {
     typedef la_f4 Fr;
-    enum { kTerms = 1, kVec = 4 };
+    enum { kTerms = 1, kVec = 4, kPad = 4 };
+    static __device__ __forceinline__ int at(int r0, int r, int c, int S) {
+        return (r0 + r) * S + c;
+    }
     static __device__ __forceinline__ la_f4 mma(Fr a0, Fr a1, Fr b0, Fr b1, la_f4 c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -90,11 +108,14 @@ template <> struct Mat<float> {
     static __device__ __forceinline__ Fr row(const float* p) {
         return *reinterpret_cast<const la_f4*>(p);
     }
-    static __device__ __forceinline__ Fr col(const float* p, int stride, int lane) {
-        const int g = lane >> 4, i = lane & 15;
+    static __device__ __forceinline__ int step(int a, int ct) { return a + ct * 16; }
+    static __device__ __forceinline__ int col_place(int lane, int S) {
+        return at(0, 4 * (lane >> 4), lane & 15, S);
+    }
+    static __device__ __forceinline__ Fr col(const float* p, int S) {
         Fr r;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = p[(4 * g + e) * stride + i];
+        for (int e = 0; e < 4; ++e) r[e] = p[e * S];
         return r;
     }
     static __device__ __forceinline__ la_f4 widen(Fr f) { return f; }
@@ -121,11 +142,11 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     typedef typename M::Fr Fr;
     constexpr bool SEG = MODE == kSegment, SUMS = MODE == kWalkSums;
     constexpr int N = M::kTerms;
-    constexpr int VEC = M::kVec;
-    constexpr int XS = KP + VEC;          // LDS row strides: one 16-byte slot of padding
+    constexpr int VEC = M::kVec, ES = sizeof(T);
+    constexpr int XS = KP + M::kPad;      // LDS rows
     constexpr int ZC = 64 * NT;
-    constexpr int ZS = ZC + VEC;
-    constexpr int PS = C + VEC;
+    constexpr int ZS = ZC + M::kPad;
+    constexpr int PS = C + VEC;           // one 16-byte slot of padding
     constexpr int IT = C / 16;            // token tiles
     constexpr int KT = KP / 16;           // state row tiles
     constexpr int XV = C * KP / VEC / 256;
@@ -136,8 +157,9 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     __shared__ __attribute__((aligned(16))) T Ys[C * XS];
     __shared__ __attribute__((aligned(16))) T Zs[C * ZS];
     __shared__ __attribute__((aligned(16))) T Ps[SEG ? 8 : N * C * PS];
-    __shared__ __attribute__((aligned(16))) float g_hi[C], g_lo[C], g_in[C], g_out[C], own[C];
-    __shared__ float g_all;
+    // decay exponents and factors of two chunks: the one at work and the next
+    __shared__ __attribute__((aligned(16))) float g_hi[2][C], g_lo[2][C], g_in[2][C], g_out[2][C];
+    __shared__ float g_all[2], own[SUMS ? C : 1];
 
     const int id = la_logical(blockIdx.x, gridDim.x);
     const int tile = id % p.max_tiles;
@@ -149,16 +171,18 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     if (tile >= w.tiles) return;
     LaSpan sp;
     if (!la_locate(p.offsets, p.B, p.seg_len, seg, sp)) return;
+    auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    sp = LaSpan{uniform(sp.row), uniform(sp.s), uniform(sp.count), uniform(sp.t0), uniform(sp.n),
+                uniform(sp.first)};
     const int Kd = w.Kd, Vd = w.Vd, n = sp.n;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g4 = (lane >> 4) * 4, i16 = lane & 15;
     const int zbase = tile * ZC + wave * 16 * NT;   // this wave's columns
-    const int lz = wave * 16 * NT;                  // the same within the workgroup's
     const uint32_t slot = p.slot_idx ? p.slot_idx[sp.row] : static_cast<uint32_t>(sp.row);
-    const bool at_last = w.reverse != 0 ? sp.s == 0 : sp.s == sp.count - 1;
-    if (SEG && at_last) return;           // no later segment needs its sum
-
     const bool third = w.third != 0, reverse = w.reverse != 0, out_f32 = w.out_f32 != 0;
+    const bool at_last = reverse ? sp.s == 0 : sp.s == sp.count - 1;
+    if (SEG && at_last) return;           // no later segment needs its sum
     const bool sums = SUMS && w.row_sum != nullptr;
     char* const out = static_cast<char*>(w.out);
     const int64_t out_tok = w.out_tok, out_head = w.out_head;
@@ -216,90 +240,132 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
             for (int zt = 0; zt < NT; ++zt) S[kt][zt] = la_f4{0, 0, 0, 0};
     }
 
-    // ---- a chunk's loads, held in registers until its LDS is free.  They are
-    // unconditional too: rows past the end and columns past the head dim are
-    // clamped, and written to LDS as zeros.
+    // ---- a chunk's loads, held in registers until its LDS is free.  A token is
+    // found from the chunk's first one in memory (a uniform address) by a
+    // 32-bit offset, in units of 16 bytes up to the last step.  Rows past the
+    // end are clamped; they, and columns past the head dim, are written to LDS
+    // as zeros.
     constexpr int XR = 256 / (KP / VEC), ZR = 256 / (ZC / VEC);  // rows per load
-    const int xr0 = tid / (KP / VEC), xc = tid % (KP / VEC) * VEC;
-    const int zr0 = tid / (ZC / VEC), zc = tid % (ZC / VEC) * VEC;
-    const bool xok = xc < Kd, zok = tile * ZC + zc < Vd;
-    const int64_t xt = dir * w.x.tok, yt = dir * w.y.tok, zt_ = dir * w.z.tok;
-    const T* xp = static_cast<const T*>(w.x.p) + (head / w.x.div) * w.x.head + start * w.x.tok +
-                  (xok ? xc : 0);
-    const T* yp = static_cast<const T*>(w.y.p) + (head / w.y.div) * w.y.head + start * w.y.tok +
-                  (xok ? xc : 0);
-    const T* zp = static_cast<const T*>(w.z.p) + (head / w.z.div) * w.z.head + start * w.z.tok +
-                  (zok ? tile * ZC + zc : 0);
-    la_u4 px[SEG ? 1 : XV], py[XV], pz[ZV];
-    float pg = 0.0f;
-    const int64_t gdir = dir * p.g_tok;
-    const char* gp = static_cast<const char*>(p.g) +
-                     (start * p.g_tok + head * p.g_head) * (p.g_bf16 ? 2 : 4);
-    auto fetch = [&](int c0) {
-        const int m = n - 1 - c0;         // the last token's place in the chunk
-#pragma unroll
-        for (int i = 0; i < XV; ++i) {
-            const int r = c0 + min(xr0 + i * XR, m);
-            if constexpr (!SEG) px[i] = *reinterpret_cast<const la_u4*>(xp + r * xt);
-            py[i] = *reinterpret_cast<const la_u4*>(yp + r * yt);
-        }
-#pragma unroll
-        for (int i = 0; i < ZV; ++i)
-            pz[i] = *reinterpret_cast<const la_u4*>(zp + (c0 + min(zr0 + i * ZR, m)) * zt_);
-        if (p.g && wave == 0) {
-            const int64_t at = (c0 + min(lane, m)) * gdir;
-            pg = p.g_bf16 ? la_widen(reinterpret_cast<const uint16_t*>(gp)[at])
-                          : reinterpret_cast<const float*>(gp)[at];
-        }
+    // A thread's row and column among the rows of a load.  What is derived from
+    // the thread's number is computed anew for each chunk (`fresh`): kept over
+    // the chunks it takes registers that others would have to be spilled from.
+    auto fresh = [](int v) {
+        asm volatile("" : "+v"(v));
+        return v;
     };
-    double walked = 0.0;                  // log2 decay of the chunks before (SEG)
-    auto stage = [&](int c0) {
-        const int m = n - c0;
+    struct Mine { int xr, xc, zr, zc; };
+    auto mine = [](int t) {
+        return Mine{t / (KP / VEC), t % (KP / VEC) * VEC, t / (ZC / VEC), t % (ZC / VEC) * VEC};
+    };
+    const char* const xp = static_cast<const char*>(w.x.p) + head / w.x.div * w.x.head * ES;
+    const char* const yp = static_cast<const char*>(w.y.p) + head / w.y.div * w.y.head * ES;
+    const char* const zp = static_cast<const char*>(w.z.p) + head / w.z.div * w.z.head * ES;
+    const int64_t x_tok = w.x.tok, y_tok = w.y.tok, z_tok = w.z.tok;
+    la_u4 px[SEG ? 1 : XV], py[XV], pz[ZV];
+    uint32_t pg = 0;                      // g as it is stored
+    // The first token in memory of the R at walk positions r, r + 1, ...
+    auto lead = [&](int r, int R) { return reverse ? start - r - (R - 1) : start + r; };
+    auto fetch = [&](int c0) {
+        const int t = fresh(tid);
+        const Mine at_ = mine(t);
+        const int m = n - 1 - c0;         // the last token's place in the chunk
+        if (p.g && wave == 0) {
+            const int64_t at = (start + dir * (c0 + min(t & 63, m))) * p.g_tok + head * p.g_head;
+            if (p.g_bf16) pg = static_cast<const uint16_t*>(p.g)[at];
+            else pg = static_cast<const uint32_t*>(p.g)[at];
+        }
+        const uint32_t xcol = at_.xc < Kd ? at_.xc / VEC : 0;
+        const uint32_t zcol = tile * ZC + at_.zc < Vd ? (tile * ZC + at_.zc) / VEC : 0;
+        const int64_t from = lead(c0, C);
+        auto load = [&](const char* q, int64_t tok, int r, uint32_t col) {
+            r = min(r, m);
+            const uint32_t at = __umul24(static_cast<uint32_t>(reverse ? C - 1 - r : r),
+                                         static_cast<uint32_t>(tok / VEC)) + col;
+            return *reinterpret_cast<const la_u4*>(q + from * (tok * ES) + (at << 4));
+        };
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
-            const int r = xr0 + i * XR;
+            if constexpr (!SEG) px[i] = load(xp, x_tok, at_.xr + i * XR, xcol);
+            py[i] = load(yp, y_tok, at_.xr + i * XR, xcol);
+        }
+#pragma unroll
+        for (int i = 0; i < ZV; ++i) pz[i] = load(zp, z_tok, at_.zr + i * ZR, zcol);
+    };
+    auto place = [](int r, int c, int stride) { return M::at(r & ~15, r & 15, c, stride); };
+    auto stage = [&](int c0) {
+        const Mine at_ = mine(fresh(tid));
+        const int xr0 = at_.xr, xc = at_.xc, zr0 = at_.zr, zc = at_.zc;
+        const bool xok = xc < Kd, zok = tile * ZC + zc < Vd;
+        const int m = n - c0;
+        if (m >= C && Kd == KP && (tile + 1) * ZC <= Vd) {
+#pragma unroll
+            for (int i = 0; i < XV; ++i) {
+                const int at = place(xr0 + i * XR, xc, XS);
+                if constexpr (!SEG) *reinterpret_cast<la_u4*>(&Xs[at]) = px[i];
+                *reinterpret_cast<la_u4*>(&Ys[at]) = py[i];
+            }
+#pragma unroll
+            for (int i = 0; i < ZV; ++i)
+                *reinterpret_cast<la_u4*>(&Zs[place(zr0 + i * ZR, zc, ZS)]) = pz[i];
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < XV; ++i) {
+            const int r = xr0 + i * XR, at = place(r, xc, XS);
             const uint32_t keep = xok && r < m ? ~0u : 0u;
-            if constexpr (!SEG) *reinterpret_cast<la_u4*>(&Xs[r * XS + xc]) = px[i] & keep;
-            *reinterpret_cast<la_u4*>(&Ys[r * XS + xc]) = py[i] & keep;
+            if constexpr (!SEG) *reinterpret_cast<la_u4*>(&Xs[at]) = px[i] & keep;
+            *reinterpret_cast<la_u4*>(&Ys[at]) = py[i] & keep;
         }
 #pragma unroll
         for (int i = 0; i < ZV; ++i) {
             const int r = zr0 + i * ZR;
             const uint32_t keep = zok && r < m ? ~0u : 0u;
-            *reinterpret_cast<la_u4*>(&Zs[r * ZS + zc]) = pz[i] & keep;
-        }
-        if (wave == 0) {                  // the chunk's decay exponents, base 2
-            const double own_g = lane < C && lane < m ? static_cast<double>(la_clamp_g(pg)) * kLog2e
-                                                      : 0.0;
-            double sum = own_g;
-#pragma unroll
-            for (int d = 1; d < C; d <<= 1) {
-                const double up = __shfl_up(sum, d);
-                if (lane >= d) sum += up;
-            }
-            const double all = __shfl(sum, C - 1);
-            if (reverse) sum -= own_g;
-            if (lane < C) {
-                const float hi = static_cast<float>(sum);
-                g_hi[lane] = hi;
-                g_lo[lane] = static_cast<float>(sum - static_cast<double>(hi));
-                g_in[lane] = exp2f(static_cast<float>(sum));
-                g_out[lane] = exp2f(static_cast<float>(all - sum));
-            }
-            if (lane == 0) g_all = exp2f(static_cast<float>(all));
-            if (SEG) walked += all;
+            *reinterpret_cast<la_u4*>(&Zs[place(r, zc, ZS)]) = pz[i] & keep;
         }
     };
-
     const float scale = p.scale;
-    if (n > 0) fetch(0);
-    for (int c0 = 0; c0 < n; c0 += C) {
+    double walked = 0.0;                  // log2 decay of the chunks so far (SEG)
+    // A chunk's decay exponents (base 2), by the first wave: a lane per token.
+    auto decays = [&](int c0, int b) {
+        const float g = __uint_as_float(p.g_bf16 ? pg << 16 : pg);
+        const double own_g = lane < C && lane < n - c0
+                                 ? static_cast<double>(la_clamp_g(g)) * kLog2e : 0.0;
+        double sum = own_g;
+#pragma unroll
+        for (int d = 1; d < C; d <<= 1) {
+            const double up = __shfl_up(sum, d);
+            if (lane >= d) sum += up;
+        }
+        const double all = __shfl(sum, C - 1);
+        if (reverse) sum -= own_g;
+        if (lane < C) {
+            const float hi = static_cast<float>(sum);
+            g_hi[b][lane] = hi;
+            g_lo[b][lane] = static_cast<float>(sum - static_cast<double>(hi));
+            g_in[b][lane] = scale * __builtin_amdgcn_exp2f(static_cast<float>(sum));
+            g_out[b][lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - sum));
+        }
+        if (lane == 0) g_all[b] = __builtin_amdgcn_exp2f(static_cast<float>(all));
+        if (SEG) walked += all;
+    };
+
+    if (n > 0) {
+        fetch(0);
+        if (wave == 0) decays(0, 0);
+    }
+    for (int c0 = 0, b = 0; c0 < n; c0 += C, b ^= 1) {
         stage(c0);
         __syncthreads();
-        if (c0 + C < n) fetch(c0 + C);
+        const bool more = c0 + C < n;
+        if (more) fetch(c0 + C);
+        const int ln = fresh(lane);
+        const int g4 = (ln >> 4) * 4, i16 = ln & 15;
+        const int row_x = M::at(0, i16, g4, XS), col_y = M::col_place(ln, XS);
+        // a wave's own columns start at a multiple of 16 within a tile's rows
+        const int col_z = M::step(M::col_place(ln, ZS), wave * NT);
         la_f4 O[SEG ? 1 : IT][NT];
         if constexpr (!SEG) {
-            // exp(G_i) (S^T X^T): rows are columns of the state, columns tokens
+            // scale exp(G_i) (S^T X^T): rows are columns of the state, columns tokens
 #pragma unroll
             for (int it = 0; it < IT; ++it)
 #pragma unroll
@@ -314,38 +380,41 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                 }
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    const T* xr = &Xs[(it * 16 + i16) * XS + kt * 16 + g4];
-                    const Fr x0 = M::row(xr), x1 = M::row(xr + 16);
+                    const Fr x0 = M::row(&Xs[it * 16 * XS + M::step(row_x, kt)]);
+                    const Fr x1 = M::row(&Xs[it * 16 * XS + M::step(row_x, kt + 1)]);
 #pragma unroll
-                    for (int zt = 0; zt < NT; ++zt)
+                    for (int t = 0; t < N; ++t)
 #pragma unroll
-                        for (int t = 0; t < N; ++t)
+                        for (int zt = 0; zt < NT; ++zt)
                             O[it][zt] = M::mma(s0[zt][t], s1[zt][t], x0, x1, O[it][zt]);
                 }
             }
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
-                const float wgt = g_in[it * 16 + i16];
+                const float wgt = g_in[b][it * 16 + i16];
 #pragma unroll
                 for (int zt = 0; zt < NT; ++zt) O[it][zt] *= wgt;
             }
-            // P by tiles of 16 x 16 on and below the diagonal, dealt to the waves
+            // scale P by tiles of 16 x 16 on and below the diagonal, dealt to the waves
             for (int t = wave; t < IT * (IT + 1) / 2; t += kLaWaves) {
                 const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
                 const int jt = t - it * (it + 1) / 2;
                 la_f4 acc = {0, 0, 0, 0};
-                const T* xr = &Xs[(it * 16 + i16) * XS + g4];
-                const T* yr = &Ys[(jt * 16 + i16) * XS + g4];
+                const int rx = row_x + it * 16 * XS, ry = row_x + jt * 16 * XS;
 #pragma unroll
                 for (int kt = 0; kt < KT; kt += 2)
-                    acc = M::mma(M::row(yr + kt * 16), M::row(yr + kt * 16 + 16),
-                                 M::row(xr + kt * 16), M::row(xr + kt * 16 + 16), acc);
+                    acc = M::mma(M::row(&Ys[M::step(ry, kt)]), M::row(&Ys[M::step(ry, kt + 1)]),
+                                 M::row(&Xs[M::step(rx, kt)]), M::row(&Xs[M::step(rx, kt + 1)]),
+                                 acc);
+                acc *= scale;
                 const int i = it * 16 + i16;
-                const float hi = g_hi[i], lo = g_lo[i];
+                const float hi = g_hi[b][i], lo = g_lo[b][i];
+                const la_f4 hj = *reinterpret_cast<const la_f4*>(&g_hi[b][jt * 16 + g4]);
+                const la_f4 lj = *reinterpret_cast<const la_f4*>(&g_lo[b][jt * 16 + g4]);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = jt * 16 + g4 + r;
-                    const float e = exp2f((hi - g_hi[j]) + (lo - g_lo[j]));
+                    const float e = __builtin_amdgcn_exp2f((hi - hj[r]) + (lo - lj[r]));
                     if (SUMS && i == j) own[i] = acc[r];
                     const bool keep = sums ? j < i : j <= i;
                     acc[r] = keep ? acc[r] * e : 0.0f;
@@ -364,7 +433,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
         for (int jt = 0; jt < IT; ++jt)
 #pragma unroll
             for (int zt = 0; zt < NT; ++zt)
-                zf[jt][zt] = M::col(&Zs[jt * 16 * ZS + lz + zt * 16], ZS, lane);
+                zf[jt][zt] = M::col(&Zs[jt * 16 * ZS + M::step(col_z, zt)], ZS);
         if constexpr (!SEG) {
             const Fr none = M::narrow(la_f4{0, 0, 0, 0});
 #pragma unroll
@@ -381,85 +450,114 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                     }
             if (sums) {
                 // partner . out without the token's own pair, then that pair
-                const int64_t qt = dir * w.partner.tok;
-                const T* qp = static_cast<const T*>(w.partner.p) +
-                              (head / w.partner.div) * w.partner.head + start * w.partner.tok;
-                float* rs = w.row_sum + (int64_t{tile} * kLaWaves + wave) * p.nv * p.T +
-                            int64_t{head} * p.T;
+                const int64_t from = lead(c0, C);
+                const char* const qp = static_cast<const char*>(w.partner.p) +
+                                       (head / w.partner.div * w.partner.head +
+                                        from * w.partner.tok) * ES;
+                const int row_z = M::step(M::at(0, i16, g4, ZS), wave * NT);
+                const uint32_t q_tok = static_cast<uint32_t>(w.partner.tok / 4);
+                float* const rs = w.row_sum + (int64_t{tile} * kLaWaves + wave) * p.nv * p.T +
+                                  int64_t{head} * p.T + from;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
+                    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
                     const int i = it * 16 + i16;
                     float sum = 0.0f;
 #pragma unroll
                     for (int zt = 0; zt < NT; ++zt) {
                         const int z = zbase + zt * 16 + g4;
-                        const T* q = qp + min(c0 + i, n - 1) * qt + min(z, Vd - 4);
-                        const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(q));
+                        const int r0 = min(i, n - 1 - c0);
+                        const uint32_t at = __umul24(reverse ? C - 1 - r0 : r0, q_tok) +
+                                            static_cast<uint32_t>(min(z, Vd - 4)) / 4;
+                        const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(
+                            qp + at * static_cast<uint32_t>(4 * ES)));
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
                             sum = z < Vd ? fmaf(a[r], O[it][zt][r], sum) : sum;
                     }
                     sum += __shfl_xor(sum, 16);
                     sum += __shfl_xor(sum, 32);
-                    if (lane < 16 && c0 + i < n) rs[start + dir * (c0 + i)] = sum;
+                    if (ln < 16 && c0 + i < n) rs[reverse ? C - 1 - i : i] = sum;
                     const float d = own[i];
 #pragma unroll
                     for (int zt = 0; zt < NT; ++zt) {
-                        const la_f4 z = M::widen(M::row(&Zs[i * ZS + lz + zt * 16 + g4]));
+                        const la_f4 z = M::widen(M::row(&Zs[it * 16 * ZS +
+                                                          M::step(row_z, zt)]));
 #pragma unroll
                         for (int r = 0; r < 4; ++r) O[it][zt][r] = fmaf(d, z[r], O[it][zt][r]);
                     }
                 }
             }
+            auto put = [&](auto narrow) {
+                typedef decltype(narrow(O[0][0])) Vec;
+                constexpr int OES = sizeof(Vec) / 4;
+                const uint32_t row = __umul24(static_cast<uint32_t>(reverse ? 15 - i16 : i16),
+                                              static_cast<uint32_t>(out_tok / 4)) * sizeof(Vec);
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const int i = it * 16 + i16;
-                if (c0 + i < n) {
-                    const int64_t at = (start + dir * (c0 + i)) * out_tok + head * out_head;
+                for (int it = 0; it < IT; ++it) {
+                    char* const base = out + (lead(c0 + it * 16, 16) * out_tok +
+                                              head * out_head + zbase) * OES;
+                    if (c0 + it * 16 + i16 < n) {
 #pragma unroll
-                    for (int zt = 0; zt < NT; ++zt) {
-                        const int z = zbase + zt * 16 + g4;
-                        if (z < Vd) {
-                            const la_f4 o = O[it][zt] * scale;
-                            if (out_f32)
-                                *reinterpret_cast<la_f4*>(reinterpret_cast<float*>(out) + at + z) = o;
-                            else
-                                *reinterpret_cast<Fr*>(reinterpret_cast<T*>(out) + at + z) =
-                                    M::narrow(o);
-                        }
+                        for (int zt = 0; zt < NT; ++zt)
+                            if (zbase + zt * 16 + g4 < Vd)
+                                *reinterpret_cast<Vec*>(base + (row + (zt * 16 + g4) * OES)) =
+                                    narrow(O[it][zt]);
                     }
                 }
-            }
+            };
+            if (out_f32) put([](la_f4 v) { return v; });
+            else put([](la_f4 v) { return M::narrow(v); });
         }
+        if (more && wave == 0) decays(c0 + C, b ^ 1);
         // ---- S <- exp(G_C) S + Y^T (decayed Z)
-        const float all = g_all;
+        const float all = g_all[b];
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
             for (int zt = 0; zt < NT; ++zt) S[kt][zt] *= all;
 #pragma unroll
         for (int jt = 0; jt < IT; jt += 2) {
-            const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[jt * 16 + g4]);
-            const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[jt * 16 + 16 + g4]);
-            constexpr int NW = N == 1 ? 1 : 3;
-            Fr z0[NT][NW], z1[NT][NW];
+            const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + g4]);
+            const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + 16 + g4]);
+            Fr z0[NT][N], z1[NT][N];
 #pragma unroll
             for (int zt = 0; zt < NT; ++zt) {
-                split<T, NW>(M::widen(zf[jt][zt]) * w0, z0[zt]);
-                split<T, NW>(M::widen(zf[jt + 1][zt]) * w1, z1[zt]);
+                split<T, N>(M::widen(zf[jt][zt]) * w0, z0[zt]);
+                split<T, N>(M::widen(zf[jt + 1][zt]) * w1, z1[zt]);
             }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
-                const Fr y0 = M::col(&Ys[jt * 16 * XS + kt * 16], XS, lane);
-                const Fr y1 = M::col(&Ys[(jt + 1) * 16 * XS + kt * 16], XS, lane);
+                const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
+                const Fr y1 = M::col(&Ys[(jt + 1) * 16 * XS + M::step(col_y, kt)], XS);
 #pragma unroll
-                for (int zt = 0; zt < NT; ++zt) {
+                for (int u = 0; u < N; ++u)
 #pragma unroll
-                    for (int u = 0; u < N; ++u)
+                    for (int zt = 0; zt < NT; ++zt)
                         S[kt][zt] = M::mma(y0, y1, z0[zt][u], z1[zt][u], S[kt][zt]);
-                    if constexpr (NW == 3)
-                        if (third)
+            }
+        }
+        if constexpr (N > 1) {
+            if (third) {                  // what two terms leave, for a float32 state
+#pragma unroll 1
+                for (int jt = 0; jt < IT; jt += 2) {
+                    const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + g4]);
+                    const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + 16 + g4]);
+                    Fr z0[NT][3], z1[NT][3];
+#pragma unroll
+                    for (int zt = 0; zt < NT; ++zt) {
+                        const T* z = &Zs[jt * 16 * ZS + M::step(col_z, zt)];
+                        split<T, 3>(M::widen(M::col(z, ZS)) * w0, z0[zt]);
+                        split<T, 3>(M::widen(M::col(z + 16 * ZS, ZS)) * w1, z1[zt]);
+                    }
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt) {
+                        const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
+                        const Fr y1 = M::col(&Ys[(jt + 1) * 16 * XS + M::step(col_y, kt)], XS);
+#pragma unroll
+                        for (int zt = 0; zt < NT; ++zt)
                             S[kt][zt] = M::mma(y0, y1, z0[zt][2], z1[zt][2], S[kt][zt]);
+                    }
                 }
             }
         }
@@ -502,7 +600,8 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
         if (lane == 0)
-            w.phi[(int64_t{seg} * p.nv + head) * w.tiles * kLaWaves + tile * kLaWaves + wave] = sum;
+            w.phi[(int64_t{seg} * p.nv + head) * w.tiles * kLaWaves + tile * kLaWaves + wave] =
+                scale * sum;
     }
     // a row without tokens leaves its pool slot alone
     if (w.last.p && at_last && (n > 0 || w.last.p != w.in.p))
