@@ -117,9 +117,9 @@ struct LaPlan {
 
 LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t V, bool backward) {
     LaPlan p{};
-    const int k = static_cast<int>(K), v = static_cast<int>(V);
-    p.v_tiles = ceil_div(V, la_columns(k, v));
-    p.q_tiles = ceil_div(K, la_columns(v, k));
+    const int64_t q_waves = la_waves(static_cast<int>(K));
+    p.v_tiles = ceil_div(V, 16 * la_waves(static_cast<int>(V)));
+    p.q_tiles = ceil_div(K, 16 * q_waves);
     // Rows are walked token by token, so few (row, head) pairs leave most of
     // the 256 compute units idle: rows are cut into segments, whose own sums a
     // first pass takes, until about two workgroups a unit are walking.
@@ -146,9 +146,9 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
         p.tot = take(2 * p.segs * nv);
     }
     if (backward) {
-        p.rq = take(p.q_tiles * kLaWaves * nv * T);
-        p.rk = take(p.q_tiles * kLaWaves * nv * T);
-        p.phi = take(p.segs * nv * p.q_tiles * kLaWaves);
+        p.rq = take(p.q_tiles * q_waves * nv * T);
+        p.rk = take(p.q_tiles * q_waves * nv * T);
+        p.phi = take(p.segs * nv * p.q_tiles * q_waves);
         if (nv != nk) {
             p.pq = take(T * nv * K);
             p.pk = take(T * nv * K);
@@ -254,7 +254,7 @@ LaWalk la_walk(const LaTensor& x, const LaTensor& y, const LaTensor& z, int64_t 
     w.z = z;
     w.Kd = static_cast<int32_t>(Kd);
     w.Vd = static_cast<int32_t>(Vd);
-    w.tiles = static_cast<int32_t>(ceil_div(Vd, la_columns(w.Kd, w.Vd)));
+    w.tiles = static_cast<int32_t>(ceil_div(Vd, 16 * la_waves(w.Vd)));
     w.reverse = reverse;
     return w;
 }
@@ -270,7 +270,8 @@ hipError_t run_walks(LaParams p, const LaWalk* w, int n, bool b16, hipStream_t s
     return launch_la_walks(p, b16, s);
 }
 
-int size_class(int Kd, int Vd) { return (Kd <= 64 ? 0 : Kd <= 128 ? 2 : 4) + (la_columns(Kd, Vd) > 64); }
+// Walks of one class run the same kernel.
+int size_class(int Kd, int Vd) { return (Kd <= 64 ? 0 : Kd <= 128 ? 1 : 2) * 16 + la_waves(Vd); }
 
 LaScan la_scan(const LaParams& p, const LaDims& d, float* state, const float* tot, bool reverse,
                const LaState& in) {
@@ -593,9 +594,9 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         c.offsets = p.offsets;
         c.rq = ws + pl.rq;
         c.rk = ws + pl.rk;
-        c.rq_parts = c.rk_parts = wq.tiles * kLaWaves;
+        c.rq_parts = c.rk_parts = wq.tiles * la_waves(wq.Vd);
         c.phi = wq.phi;
-        c.phi_parts = wq.tiles * kLaWaves;
+        c.phi_parts = wq.tiles * la_waves(wq.Vd);
         c.dg = dg->data;
         c.dg_tok = dg->stride[0];
         c.dg_head = dg->stride[1];

@@ -57,7 +57,6 @@ struct LaWalk {
 
 constexpr int kLaMaxWalks = 3;
 constexpr int kLaStepTokens = 4;  // tokens a row, on average, up to which rows go token by token
-constexpr int kLaWaves = 4;
 
 struct LaParams {
     int32_t B, nv, T;
@@ -115,8 +114,8 @@ struct LaStep {
     float scale;
 };
 
-// Columns of the state per workgroup for a walk over [Kd, Vd] states.
-inline int la_columns(int Kd, int Vd) { return Kd > 128 || Vd <= 64 ? 64 : 128; }
+// Waves of a walk's workgroup, of 16 columns of the state each.
+inline int la_waves(int Vd) { return Vd <= 64 ? 4 : 8; }
 
 hipError_t launch_la_walks(const LaParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_la_segments(const LaParams& p, bool work_bf16, float* tot, hipStream_t s);

@@ -2,13 +2,13 @@
 // chunked matrix form.  Compiled once per work type (GDR_WT: float, or
 // uint16_t for bf16 bits).
 //
-// A workgroup of four waves walks one segment of a row for one value head and
-// up to 128 columns of the state, C tokens (a chunk) at a time:
+// A workgroup of four or eight waves walks one segment of a row for one value
+// head and 64 or 128 columns of the state, C tokens (a chunk) at a time:
 //     P_ij = exp(G_i - G_j) (x_i . y_j), j <= i         (C x C, per chunk)
 //     out  = scale (P Z + diag(exp(G)) X S)
 //     S   <- exp(G_C) S + Y^T diag(exp(G_C - G)) Z
 // The state stays in registers for the whole segment: each wave owns all Kd
-// rows of 16 NT columns, in the accumulator layout of the matrix
+// rows of 16 columns, in the accumulator layout of the matrix
 // instructions, which is at once the operand layout of the product X S (the
 // order of a contraction is free as long as both operands agree on it), so
 // the state is never moved.  X, Y and Z are staged row by row in LDS; the
@@ -132,25 +132,25 @@ __device__ __forceinline__ void split(la_f4 v, typename Mat<T>::Fr (&out)[N]) {
     }
 }
 
-// KP: Kd rounded up to the built size (the rest is zeros); 64 * NT columns per
-// workgroup; C tokens per chunk.  Modes: the walk; the walk with the sums for the
+// KP: Kd rounded up to the built size (the rest is zeros); W waves of 16
+// columns per workgroup; C tokens per chunk.  Modes: the walk; the walk with the sums for the
 // decays' gradient; only the segment's own sum of the state.
 enum { kWalk = 0, kWalkSums = 1, kSegment = 2 };
-template <typename T, int KP, int NT, int C, int MODE>
-__global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* __restrict__ tot) {
+template <typename T, int KP, int W, int C, int MODE>
+__global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kernel(const LaParams p, float* __restrict__ tot) {
     typedef Mat<T> M;
     typedef typename M::Fr Fr;
     constexpr bool SEG = MODE == kSegment, SUMS = MODE == kWalkSums;
     constexpr int N = M::kTerms;
     constexpr int VEC = M::kVec, ES = sizeof(T);
     constexpr int XS = KP + M::kPad;      // LDS rows
-    constexpr int ZC = 64 * NT;
+    constexpr int TH = 64 * W, ZC = 16 * W;
     constexpr int ZS = ZC + M::kPad;
     constexpr int PS = C + VEC;           // one 16-byte slot of padding
     constexpr int IT = C / 16;            // token tiles
     constexpr int KT = KP / 16;           // state row tiles
-    constexpr int XV = C * KP / VEC / 256;
-    constexpr int ZV = C * ZC / VEC / 256;
+    constexpr int XV = C * KP / VEC / TH;
+    constexpr int ZV = C * ZC / VEC / TH;
     static_assert(XV >= 1 && ZV >= 1, "a chunk fills the workgroup's loads");
 
     __shared__ __attribute__((aligned(16))) T Xs[SEG ? 8 : C * XS];
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g4 = (lane >> 4) * 4, i16 = lane & 15;
-    const int zbase = tile * ZC + wave * 16 * NT;   // this wave's columns
+    const int zbase = tile * ZC + wave * 16;        // this wave's columns
     const uint32_t slot = p.slot_idx ? p.slot_idx[sp.row] : static_cast<uint32_t>(sp.row);
     const bool third = w.third != 0, reverse = w.reverse != 0, out_f32 = w.out_f32 != 0;
     const bool at_last = reverse ? sp.s == 0 : sp.s == sp.count - 1;
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     const int64_t start = reverse ? int64_t{sp.t0} + n - 1 : sp.t0;
     const int64_t dir = reverse ? -1 : 1;
     if (!SEG && slot == kPadSlot) {       // a padding row: zeros out, no state
-        for (int64_t i = tid; i < int64_t{n} * ZC; i += 256) {
+        for (int64_t i = tid; i < int64_t{n} * ZC; i += TH) {
             const int z = tile * ZC + static_cast<int>(i % ZC);
             const int64_t at = (sp.t0 + i / ZC) * out_tok + head * out_head + z;
             if (z < Vd) {
@@ -204,40 +204,34 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
 
     // ---- the state.  All loads are issued together: indices past the state
     // are clamped into it and their values replaced.
-    la_f4 S[KT][NT];
+    la_f4 S[KT];
     auto load_as = [&](const LaState& s, auto* base, auto&& use) {
         base += (s.by_segment ? int64_t{seg} : int64_t{slot}) * s.outer + head * s.head;
-        int zo[NT];
+        const int zo = min(zbase + i16, Vd - 1) * s.sz;
 #pragma unroll
-        for (int zt = 0; zt < NT; ++zt) zo[zt] = min(zbase + zt * 16 + i16, Vd - 1) * s.sz;
+        for (int kt = 0; kt < KT; ++kt) {
+            la_f4 v;
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int zt = 0; zt < NT; ++zt) {
-                la_f4 v;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kd = kt * 16 + g4 + r;
-                    const auto raw = base[min(kd, Kd - 1) * s.sk + zo[zt]];
-                    float f;
-                    if constexpr (sizeof(raw) == 2) f = la_widen(raw);
-                    else f = raw;
-                    v[r] = kd < Kd && zbase + zt * 16 + i16 < Vd ? s.mult * f : 0.0f;
-                }
-                use(kt, zt, v);
+            for (int r = 0; r < 4; ++r) {
+                const int kd = kt * 16 + g4 + r;
+                const auto raw = base[min(kd, Kd - 1) * s.sk + zo];
+                float f;
+                if constexpr (sizeof(raw) == 2) f = la_widen(raw);
+                else f = raw;
+                v[r] = kd < Kd && zbase + i16 < Vd ? s.mult * f : 0.0f;
             }
+            use(kt, v);
+        }
     };
     auto load_state = [&](const LaState& s, auto&& use) {
         if (s.bf16) load_as(s, static_cast<const uint16_t*>(s.p), use);
         else load_as(s, static_cast<const float*>(s.p), use);
     };
     if (!SEG && w.in.p) {
-        load_state(w.in, [&](int kt, int zt, la_f4 v) { S[kt][zt] = v; });
+        load_state(w.in, [&](int kt, la_f4 v) { S[kt] = v; });
     } else {
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int zt = 0; zt < NT; ++zt) S[kt][zt] = la_f4{0, 0, 0, 0};
+        for (int kt = 0; kt < KT; ++kt) S[kt] = la_f4{0, 0, 0, 0};
     }
 
     // ---- a chunk's loads, held in registers until its LDS is free.  A token is
@@ -245,7 +239,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     // 32-bit offset, in units of 16 bytes up to the last step.  Rows past the
     // end are clamped; they, and columns past the head dim, are written to LDS
     // as zeros.
-    constexpr int XR = 256 / (KP / VEC), ZR = 256 / (ZC / VEC);  // rows per load
+    constexpr int XR = TH / (KP / VEC), ZR = TH / (ZC / VEC);  // rows per load
     // A thread's row and column among the rows of a load.  What is derived from
     // the thread's number is computed anew for each chunk (`fresh`): kept over
     // the chunks it takes registers that others would have to be spilled from.
@@ -362,41 +356,29 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
         const int g4 = (ln >> 4) * 4, i16 = ln & 15;
         const int row_x = M::at(0, i16, g4, XS), col_y = M::col_place(ln, XS);
         // a wave's own columns start at a multiple of 16 within a tile's rows
-        const int col_z = M::step(M::col_place(ln, ZS), wave * NT);
-        la_f4 O[SEG ? 1 : IT][NT];
+        const int col_z = M::step(M::col_place(ln, ZS), wave);
+        la_f4 O[SEG ? 1 : IT];
         if constexpr (!SEG) {
             // scale exp(G_i) (S^T X^T): rows are columns of the state, columns tokens
 #pragma unroll
-            for (int it = 0; it < IT; ++it)
-#pragma unroll
-                for (int zt = 0; zt < NT; ++zt) O[it][zt] = la_f4{0, 0, 0, 0};
+            for (int it = 0; it < IT; ++it) O[it] = la_f4{0, 0, 0, 0};
 #pragma unroll
             for (int kt = 0; kt < KT; kt += 2) {
-                Fr s0[NT][N], s1[NT][N];
-#pragma unroll
-                for (int zt = 0; zt < NT; ++zt) {
-                    split<T, N>(S[kt][zt], s0[zt]);
-                    split<T, N>(S[kt + 1][zt], s1[zt]);
-                }
+                Fr s0[N], s1[N];
+                split<T, N>(S[kt], s0);
+                split<T, N>(S[kt + 1], s1);
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     const Fr x0 = M::row(&Xs[it * 16 * XS + M::step(row_x, kt)]);
                     const Fr x1 = M::row(&Xs[it * 16 * XS + M::step(row_x, kt + 1)]);
 #pragma unroll
-                    for (int t = 0; t < N; ++t)
-#pragma unroll
-                        for (int zt = 0; zt < NT; ++zt)
-                            O[it][zt] = M::mma(s0[zt][t], s1[zt][t], x0, x1, O[it][zt]);
+                    for (int t = 0; t < N; ++t) O[it] = M::mma(s0[t], s1[t], x0, x1, O[it]);
                 }
             }
 #pragma unroll
-            for (int it = 0; it < IT; ++it) {
-                const float wgt = g_in[b][it * 16 + i16];
-#pragma unroll
-                for (int zt = 0; zt < NT; ++zt) O[it][zt] *= wgt;
-            }
+            for (int it = 0; it < IT; ++it) O[it] *= g_in[b][it * 16 + i16];
             // scale P by tiles of 16 x 16 on and below the diagonal, dealt to the waves
-            for (int t = wave; t < IT * (IT + 1) / 2; t += kLaWaves) {
+            for (int t = wave; t < IT * (IT + 1) / 2; t += W) {
                 const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
                 const int jt = t - it * (it + 1) / 2;
                 la_f4 acc = {0, 0, 0, 0};
@@ -428,12 +410,9 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
             __syncthreads();
         }
         // Z by columns: operand of P Z as it is, of the state's sum with its decay
-        Fr zf[IT][NT];
+        Fr zf[IT];
 #pragma unroll
-        for (int jt = 0; jt < IT; ++jt)
-#pragma unroll
-            for (int zt = 0; zt < NT; ++zt)
-                zf[jt][zt] = M::col(&Zs[jt * 16 * ZS + M::step(col_z, zt)], ZS);
+        for (int jt = 0; jt < IT; ++jt) zf[jt] = M::col(&Zs[jt * 16 * ZS + col_z], ZS);
         if constexpr (!SEG) {
             const Fr none = M::narrow(la_f4{0, 0, 0, 0});
 #pragma unroll
@@ -444,9 +423,7 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                     for (int u = 0; u < N; ++u) {
                         const T* pr = &Ps[(u * C + it * 16 + i16) * PS + jt * 16 + g4];
                         const Fr p0 = M::row(pr), p1 = jt + 1 <= it ? M::row(pr + 16) : none;
-#pragma unroll
-                        for (int zt = 0; zt < NT; ++zt)
-                            O[it][zt] = M::mma(zf[jt][zt], zf[jt + 1][zt], p0, p1, O[it][zt]);
+                        O[it] = M::mma(zf[jt], zf[jt + 1], p0, p1, O[it]);
                     }
             if (sums) {
                 // partner . out without the token's own pair, then that pair
@@ -454,56 +431,44 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                 const char* const qp = static_cast<const char*>(w.partner.p) +
                                        (head / w.partner.div * w.partner.head +
                                         from * w.partner.tok) * ES;
-                const int row_z = M::step(M::at(0, i16, g4, ZS), wave * NT);
+                const int row_z = M::step(M::at(0, i16, g4, ZS), wave);
                 const uint32_t q_tok = static_cast<uint32_t>(w.partner.tok / 4);
-                float* const rs = w.row_sum + (int64_t{tile} * kLaWaves + wave) * p.nv * p.T +
+                float* const rs = w.row_sum + (int64_t{tile} * W + wave) * p.nv * p.T +
                                   int64_t{head} * p.T + from;
+                const int z = zbase + g4;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
                     const int i = it * 16 + i16;
+                    const int r0 = min(i, n - 1 - c0);
+                    const uint32_t at = __umul24(reverse ? C - 1 - r0 : r0, q_tok) +
+                                        static_cast<uint32_t>(min(z, Vd - 4)) / 4;
+                    const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(
+                        qp + at * static_cast<uint32_t>(4 * ES)));
                     float sum = 0.0f;
 #pragma unroll
-                    for (int zt = 0; zt < NT; ++zt) {
-                        const int z = zbase + zt * 16 + g4;
-                        const int r0 = min(i, n - 1 - c0);
-                        const uint32_t at = __umul24(reverse ? C - 1 - r0 : r0, q_tok) +
-                                            static_cast<uint32_t>(min(z, Vd - 4)) / 4;
-                        const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(
-                            qp + at * static_cast<uint32_t>(4 * ES)));
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            sum = z < Vd ? fmaf(a[r], O[it][zt][r], sum) : sum;
-                    }
+                    for (int r = 0; r < 4; ++r) sum = fmaf(a[r], O[it][r], sum);
+                    sum = z < Vd ? sum : 0.0f;
                     sum += __shfl_xor(sum, 16);
                     sum += __shfl_xor(sum, 32);
                     if (ln < 16 && c0 + i < n) rs[reverse ? C - 1 - i : i] = sum;
                     const float d = own[i];
+                    const la_f4 zz = M::widen(M::row(&Zs[it * 16 * ZS + row_z]));
 #pragma unroll
-                    for (int zt = 0; zt < NT; ++zt) {
-                        const la_f4 z = M::widen(M::row(&Zs[it * 16 * ZS +
-                                                          M::step(row_z, zt)]));
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) O[it][zt][r] = fmaf(d, z[r], O[it][zt][r]);
-                    }
+                    for (int r = 0; r < 4; ++r) O[it][r] = fmaf(d, zz[r], O[it][r]);
                 }
             }
             auto put = [&](auto narrow) {
-                typedef decltype(narrow(O[0][0])) Vec;
+                typedef decltype(narrow(O[0])) Vec;
                 constexpr int OES = sizeof(Vec) / 4;
-                const uint32_t row = __umul24(static_cast<uint32_t>(reverse ? 15 - i16 : i16),
-                                              static_cast<uint32_t>(out_tok / 4)) * sizeof(Vec);
+                const uint32_t at = __umul24(static_cast<uint32_t>(reverse ? 15 - i16 : i16),
+                                             static_cast<uint32_t>(out_tok / 4)) * sizeof(Vec) +
+                                    g4 * OES;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     char* const base = out + (lead(c0 + it * 16, 16) * out_tok +
                                               head * out_head + zbase) * OES;
-                    if (c0 + it * 16 + i16 < n) {
-#pragma unroll
-                        for (int zt = 0; zt < NT; ++zt)
-                            if (zbase + zt * 16 + g4 < Vd)
-                                *reinterpret_cast<Vec*>(base + (row + (zt * 16 + g4) * OES)) =
-                                    narrow(O[it][zt]);
-                    }
+                    if (c0 + it * 16 + i16 < n && zbase + g4 < Vd)
+                        *reinterpret_cast<Vec*>(base + at) = narrow(O[it]);
                 }
             };
             if (out_f32) put([](la_f4 v) { return v; });
@@ -513,28 +478,20 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
         // ---- S <- exp(G_C) S + Y^T (decayed Z)
         const float all = g_all[b];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int zt = 0; zt < NT; ++zt) S[kt][zt] *= all;
+        for (int kt = 0; kt < KT; ++kt) S[kt] *= all;
 #pragma unroll
         for (int jt = 0; jt < IT; jt += 2) {
             const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + g4]);
             const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + 16 + g4]);
-            Fr z0[NT][N], z1[NT][N];
-#pragma unroll
-            for (int zt = 0; zt < NT; ++zt) {
-                split<T, N>(M::widen(zf[jt][zt]) * w0, z0[zt]);
-                split<T, N>(M::widen(zf[jt + 1][zt]) * w1, z1[zt]);
-            }
+            Fr z0[N], z1[N];
+            split<T, N>(M::widen(zf[jt]) * w0, z0);
+            split<T, N>(M::widen(zf[jt + 1]) * w1, z1);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
                 const Fr y1 = M::col(&Ys[(jt + 1) * 16 * XS + M::step(col_y, kt)], XS);
 #pragma unroll
-                for (int u = 0; u < N; ++u)
-#pragma unroll
-                    for (int zt = 0; zt < NT; ++zt)
-                        S[kt][zt] = M::mma(y0, y1, z0[zt][u], z1[zt][u], S[kt][zt]);
+                for (int u = 0; u < N; ++u) S[kt] = M::mma(y0, y1, z0[u], z1[u], S[kt]);
             }
         }
         if constexpr (N > 1) {
@@ -543,20 +500,15 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
                 for (int jt = 0; jt < IT; jt += 2) {
                     const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + g4]);
                     const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + 16 + g4]);
-                    Fr z0[NT][3], z1[NT][3];
-#pragma unroll
-                    for (int zt = 0; zt < NT; ++zt) {
-                        const T* z = &Zs[jt * 16 * ZS + M::step(col_z, zt)];
-                        split<T, 3>(M::widen(M::col(z, ZS)) * w0, z0[zt]);
-                        split<T, 3>(M::widen(M::col(z + 16 * ZS, ZS)) * w1, z1[zt]);
-                    }
+                    Fr z0[3], z1[3];
+                    const T* z = &Zs[jt * 16 * ZS + col_z];
+                    split<T, 3>(M::widen(M::col(z, ZS)) * w0, z0);
+                    split<T, 3>(M::widen(M::col(z + 16 * ZS, ZS)) * w1, z1);
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt) {
                         const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
                         const Fr y1 = M::col(&Ys[(jt + 1) * 16 * XS + M::step(col_y, kt)], XS);
-#pragma unroll
-                        for (int zt = 0; zt < NT; ++zt)
-                            S[kt][zt] = M::mma(y0, y1, z0[zt][2], z1[zt][2], S[kt][zt]);
+                        S[kt] = M::mma(y0, y1, z0[2], z1[2], S[kt]);
                     }
                 }
             }
@@ -569,16 +521,14 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int zt = 0; zt < NT; ++zt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kd = kt * 16 + g4 + r, z = zbase + zt * 16 + i16;
-                    if (kd < Kd && z < Vd) {
-                        const float v = s.mult * S[kt][zt][r];
-                        if constexpr (sizeof(*base) == 2) base[kd * s.sk + z * s.sz] = la_round(v);
-                        else base[kd * s.sk + z * s.sz] = v;
-                    }
+            for (int r = 0; r < 4; ++r) {
+                const int kd = kt * 16 + g4 + r, z = zbase + i16;
+                if (kd < Kd && z < Vd) {
+                    const float v = s.mult * S[kt][r];
+                    if constexpr (sizeof(*base) == 2) base[kd * s.sk + z * s.sz] = la_round(v);
+                    else base[kd * s.sk + z * s.sz] = v;
                 }
+            }
     };
     auto store_state = [&](const LaState& s, int64_t at) {
         if (s.bf16) store_as(s, static_cast<uint16_t*>(s.p) + at);
@@ -593,14 +543,14 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
     if (SUMS && w.phi) {
         float sum = 0.0f;
         if (w.phi_in.p)
-            load_state(w.phi_in, [&](int kt, int zt, la_f4 v) {
+            load_state(w.phi_in, [&](int kt, la_f4 v) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sum = fmaf(S[kt][zt][r], v[r], sum);
+                for (int r = 0; r < 4; ++r) sum = fmaf(S[kt][r], v[r], sum);
             });
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
         if (lane == 0)
-            w.phi[(int64_t{seg} * p.nv + head) * w.tiles * kLaWaves + tile * kLaWaves + wave] =
+            w.phi[((int64_t{seg} * p.nv + head) * w.tiles + tile) * W + wave] =
                 scale * sum;
     }
     // a row without tokens leaves its pool slot alone
@@ -608,24 +558,27 @@ __global__ void __launch_bounds__(256, 2) walk_kernel(const LaParams p, float* _
         store_state(w.last, int64_t{slot} * w.last.outer + head * w.last.head);
 }
 
-template <int KP, int NT, int C, int MODE>
+template <int KP, int W, int C, int MODE>
 hipError_t run(const LaParams& p, float* tot, hipStream_t s) {
     const int64_t blocks = int64_t{p.segs} * p.nv * p.nwalks * p.max_tiles;
-    walk_kernel<GDR_WT, KP, NT, C, MODE><<<dim3(static_cast<uint32_t>(blocks)), 256, 0, s>>>(p, tot);
+    walk_kernel<GDR_WT, KP, W, C, MODE>
+        <<<dim3(static_cast<uint32_t>(blocks)), 64 * W, 0, s>>>(p, tot);
     return hipGetLastError();
 }
 
 // The walks of one call that share a built shape, in one launch.
 template <int MODE>
 hipError_t dispatch(const LaParams& p, float* tot, hipStream_t s) {
-    const int Kd = p.w[0].Kd, cols = la_columns(Kd, p.w[0].Vd);
-    constexpr bool b16 = sizeof(GDR_WT) == 2;
-    constexpr int C = b16 ? 64 : 32;
-    if (Kd <= 64)
-        return cols == 64 ? run<64, 1, C, MODE>(p, tot, s) : run<64, 2, C, MODE>(p, tot, s);
-    if (Kd <= 128)
-        return cols == 64 ? run<128, 1, C, MODE>(p, tot, s) : run<128, 2, C, MODE>(p, tot, s);
-    return run<256, 1, 32, MODE>(p, tot, s);
+    constexpr int C = sizeof(GDR_WT) == 2 ? 64 : 32;
+    const int Kd = p.w[0].Kd;
+    if (la_waves(p.w[0].Vd) == 4) {
+        if (Kd <= 64) return run<64, 4, C, MODE>(p, tot, s);
+        if (Kd <= 128) return run<128, 4, C, MODE>(p, tot, s);
+        return run<256, 4, 32, MODE>(p, tot, s);
+    }
+    if (Kd <= 64) return run<64, 8, C, MODE>(p, tot, s);
+    if (Kd <= 128) return run<128, 8, C, MODE>(p, tot, s);
+    return run<256, 8, 32, MODE>(p, tot, s);
 }
 
 }  // namespace
