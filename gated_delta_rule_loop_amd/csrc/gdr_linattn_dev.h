@@ -33,6 +33,24 @@ __device__ __forceinline__ void la_store(void* p, int64_t i, int bf16, float x) 
 }
 __device__ __forceinline__ float la_clamp_g(float g) { return g < kLogDecayMin ? kLogDecayMin : g; }
 
+// A double from the lane that the DPP control names, 0 where there is none or
+// the lane's row is not in ROWS.
+template <int CTRL, int ROWS> __device__ __forceinline__ double la_lanes(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        0, static_cast<int>(u), CTRL, ROWS, 0xf, false));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, false));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double la_lane(double v, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u), lane));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u >> 32),
+                                                                        lane));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+
 // Segments of a row of n tokens (one at least: it carries the row's state).
 __device__ __forceinline__ int la_row_segs(int n, int seg_len) {
     return n <= seg_len ? 1 : (n + seg_len - 1) / seg_len;

@@ -46,9 +46,8 @@ template <> struct Mat<uint16_t> {
     enum { kTerms = 2, kVec = 8, kPad = 0 };  // kVec: elements per 16 bytes
     // Place of (row r0 + r, column c), r0 a multiple of 16, in a tile of rows
     // of S elements (64 at least).  The 16-byte slots of a row are permuted by
-    // the row's number, so that neither the reads along rows (16 rows, 16
-    // bytes each) nor the transposing reads (8 rows, 32 bytes each) meet in a
-    // bank.  With padded rows one of the two did: 42% of the LDS cycles.
+    // the row's number, so that the lanes of a transposing read (16 at a time:
+    // 4 rows, 32 bytes each) do not meet in a bank.
     static __device__ __forceinline__ int at(int r0, int r, int c, int S) {
         // rows of 64 lie two to a round of the banks: the row's parity tells them apart
         const int h = S == 64 ? ((r >> 1 & 3) << 1 | r >> 3) : ((r & 7) << 1 | (r >> 3 & 1));
@@ -63,6 +62,51 @@ template <> struct Mat<uint16_t> {
     }
     static __device__ __forceinline__ Fr row(const uint16_t* p) {
         return *reinterpret_cast<const la_s4*>(p);
+    }
+    // v as a sum of terms, largest first.  What a pair's rounding leaves comes
+    // from one dot product a value: v - 1 * (its own half) - 0 * (the other).
+    template <int N> static __device__ __forceinline__ void split(la_f4 v, Fr (&out)[N]) {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        // (-1, 0) and (0, -1), from registers: as an inline constant of this
+        // instruction -1.0 stands for the float32 pattern, which is (0, -1)
+        uint32_t low = 0x0000BF80u, high = 0xBF800000u;
+        asm("" : "+s"(low), "+s"(high));
+        const b2 first = __builtin_bit_cast(b2, low), second = __builtin_bit_cast(b2, high);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            u2 packed;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const b2 b = {static_cast<__bf16>(v[2 * h]), static_cast<__bf16>(v[2 * h + 1])};
+                packed[h] = __builtin_bit_cast(uint32_t, b);
+                if (i + 1 < N) {
+                    v[2 * h] = __builtin_amdgcn_fdot2_f32_bf16(b, first, v[2 * h], false);
+                    v[2 * h + 1] = __builtin_amdgcn_fdot2_f32_bf16(b, second, v[2 * h + 1], false);
+                }
+            }
+            out[i] = __builtin_bit_cast(la_s4, packed);
+        }
+    }
+    // X is only read along its rows, 32 values a time: their order in LDS is that
+    // of the state's registers (4 g + e, then 16 + 4 g + e), so that a lane reads
+    // them as 16 bytes.  Its slots are permuted so that 8 lanes of such a read
+    // do not meet in a bank.
+    static __device__ __forceinline__ void put_x(uint16_t* p, int r, int c, int S, la_u4 v) {
+        const int q = c >> 3 & 3;
+        const int a = r * S + ((((c >> 5) * 4 + (q & 1) * 2) ^ (r & 7)) << 3) + (q >> 1) * 4;
+        typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+        *reinterpret_cast<u2*>(p + a) = u2{v[0], v[1]};
+        *reinterpret_cast<u2*>(p + (a ^ 8)) = u2{v[2], v[3]};
+    }
+    static __device__ __forceinline__ int x_place(int lane, int S) {
+        const int r = lane & 15;
+        return r * S + (((lane >> 4) ^ (r & 7)) << 3);
+    }
+    static __device__ __forceinline__ void x_pair(const uint16_t* p, int a, int kt, Fr& f0, Fr& f1) {
+        const la_s8 v = *reinterpret_cast<const la_s8*>(p + (a ^ (kt * 16)));
+        f0 = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+        f1 = __builtin_shufflevector(v, v, 4, 5, 6, 7);
     }
     // The same for column c + 16 ct from the place `a` of column c (below 16):
     // only the slot's number changes, by bits that are zero in it.
@@ -96,6 +140,20 @@ template <> struct Mat<float> {
     static __device__ __forceinline__ int at(int r0, int r, int c, int S) {
         return (r0 + r) * S + c;
     }
+    template <int N> static __device__ __forceinline__ void split(la_f4 v, Fr (&out)[N]) {
+        static_assert(N == 1, "float32 operands are exact");
+        out[0] = v;
+    }
+    static __device__ __forceinline__ void put_x(float* p, int r, int c, int S, la_u4 v) {
+        *reinterpret_cast<la_u4*>(p + r * S + c) = v;
+    }
+    static __device__ __forceinline__ int x_place(int lane, int S) {
+        return (lane & 15) * S + (lane >> 4) * 4;
+    }
+    static __device__ __forceinline__ void x_pair(const float* p, int a, int kt, Fr& f0, Fr& f1) {
+        f0 = row(p + a + kt * 16);
+        f1 = row(p + a + kt * 16 + 16);
+    }
     static __device__ __forceinline__ la_f4 mma(Fr a0, Fr a1, Fr b0, Fr b1, la_f4 c) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -121,16 +179,6 @@ template <> struct Mat<float> {
     static __device__ __forceinline__ la_f4 widen(Fr f) { return f; }
     static __device__ __forceinline__ Fr narrow(la_f4 v) { return v; }
 };
-
-// v as a sum of N work-type terms, largest first.
-template <typename T, int N>
-__device__ __forceinline__ void split(la_f4 v, typename Mat<T>::Fr (&out)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        out[i] = Mat<T>::narrow(v);
-        if (i + 1 < N) v = v - Mat<T>::widen(out[i]);
-    }
-}
 
 // KP: Kd rounded up to the built size (the rest is zeros); W waves of 16
 // columns per workgroup; C tokens per chunk.  Modes: the walk; the walk with the sums for the
@@ -234,15 +282,15 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         for (int kt = 0; kt < KT; ++kt) S[kt] = la_f4{0, 0, 0, 0};
     }
 
-    // ---- a chunk's loads, held in registers until its LDS is free.  A token is
-    // found from the chunk's first one in memory (a uniform address) by a
-    // 32-bit offset, in units of 16 bytes up to the last step.  Rows past the
-    // end are clamped; they, and columns past the head dim, are written to LDS
-    // as zeros.
-    constexpr int XR = TH / (KP / VEC), ZR = TH / (ZC / VEC);  // rows per load
-    // A thread's row and column among the rows of a load.  What is derived from
-    // the thread's number is computed anew for each chunk (`fresh`): kept over
-    // the chunks it takes registers that others would have to be spilled from.
+    // ---- a chunk's loads, held in registers until its LDS is free.  A load
+    // takes XR (ZR) rows: its first token in memory is a uniform address that
+    // moves on by `inc`, a thread's own row and column a 32-bit offset from it.
+    // In the last chunk, rows past the end are clamped instead; they, and
+    // columns past the head dim, are written to LDS as zeros.
+    constexpr int XR = TH / (KP / VEC), ZR = TH / (ZC / VEC);
+    // What is derived from the thread's number is computed anew for each chunk
+    // (`fresh`): kept over the chunks it takes registers that others would have
+    // to be spilled from.
     auto fresh = [](int v) {
         asm volatile("" : "+v"(v));
         return v;
@@ -251,39 +299,60 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     auto mine = [](int t) {
         return Mine{t / (KP / VEC), t % (KP / VEC) * VEC, t / (ZC / VEC), t % (ZC / VEC) * VEC};
     };
-    const char* const xp = static_cast<const char*>(w.x.p) + head / w.x.div * w.x.head * ES;
-    const char* const yp = static_cast<const char*>(w.y.p) + head / w.y.div * w.y.head * ES;
-    const char* const zp = static_cast<const char*>(w.z.p) + head / w.z.div * w.z.head * ES;
-    const int64_t x_tok = w.x.tok, y_tok = w.y.tok, z_tok = w.z.tok;
+    struct Stream {
+        const char* q;                    // the next load's first token in memory
+        int64_t tok;                      // bytes from token to token
+    };
+    auto stream = [&](const LaTensor& t, int R) {
+        return Stream{static_cast<const char*>(t.p) +
+                          (head / t.div * t.head + (reverse ? start - (R - 1) : start) * t.tok) * ES,
+                      t.tok * ES};
+    };
+    Stream xs = stream(w.x, XR), ys = stream(w.y, XR), zs = stream(w.z, ZR);
     la_u4 px[SEG ? 1 : XV], py[XV], pz[ZV];
     uint32_t pg = 0;                      // g as it is stored
     // The first token in memory of the R at walk positions r, r + 1, ...
     auto lead = [&](int r, int R) { return reverse ? start - r - (R - 1) : start + r; };
     auto fetch = [&](int c0) {
         const int t = fresh(tid);
-        const Mine at_ = mine(t);
+        const Mine at = mine(t);
         const int m = n - 1 - c0;         // the last token's place in the chunk
-        if (p.g && wave == 0) {
-            const int64_t at = (start + dir * (c0 + min(t & 63, m))) * p.g_tok + head * p.g_head;
-            if (p.g_bf16) pg = static_cast<const uint16_t*>(p.g)[at];
-            else pg = static_cast<const uint32_t*>(p.g)[at];
+        if (p.g && wave == W - 1) {
+            const int64_t i = (start + dir * (c0 + min(t & 63, m))) * p.g_tok + head * p.g_head;
+            if (p.g_bf16) pg = static_cast<const uint16_t*>(p.g)[i];
+            else pg = static_cast<const uint32_t*>(p.g)[i];
         }
-        const uint32_t xcol = at_.xc < Kd ? at_.xc / VEC : 0;
-        const uint32_t zcol = tile * ZC + at_.zc < Vd ? (tile * ZC + at_.zc) / VEC : 0;
-        const int64_t from = lead(c0, C);
-        auto load = [&](const char* q, int64_t tok, int r, uint32_t col) {
-            r = min(r, m);
-            const uint32_t at = __umul24(static_cast<uint32_t>(reverse ? C - 1 - r : r),
-                                         static_cast<uint32_t>(tok / VEC)) + col;
-            return *reinterpret_cast<const la_u4*>(q + from * (tok * ES) + (at << 4));
-        };
+        const uint32_t xcol = at.xc < Kd ? at.xc * ES : 0;
+        const uint32_t zcol = tile * ZC + at.zc < Vd ? (tile * ZC + at.zc) * ES : 0;
+        if (m >= C - 1) {
+            auto load = [&](Stream& s, int R, int r, uint32_t col) {
+                const uint32_t row = __umul24(static_cast<uint32_t>(reverse ? R - 1 - r : r),
+                                              static_cast<uint32_t>(s.tok >> 4)) << 4;
+                const la_u4 v = *reinterpret_cast<const la_u4*>(s.q + (row + col));
+                s.q += dir * R * s.tok;
+                return v;
+            };
 #pragma unroll
-        for (int i = 0; i < XV; ++i) {
-            if constexpr (!SEG) px[i] = load(xp, x_tok, at_.xr + i * XR, xcol);
-            py[i] = load(yp, y_tok, at_.xr + i * XR, xcol);
+            for (int i = 0; i < XV; ++i) {
+                if constexpr (!SEG) px[i] = load(xs, XR, at.xr, xcol);
+                py[i] = load(ys, XR, at.xr, xcol);
+            }
+#pragma unroll
+            for (int i = 0; i < ZV; ++i) pz[i] = load(zs, ZR, at.zr, zcol);
+        } else {
+            auto load = [&](const Stream& s, int R, int r, uint32_t col) {
+                // from the chunk's first load, rows in walk order
+                const int64_t row = dir * min(r, m) + (reverse ? R - 1 : 0);
+                return *reinterpret_cast<const la_u4*>(s.q + row * s.tok + col);
+            };
+#pragma unroll
+            for (int i = 0; i < XV; ++i) {
+                if constexpr (!SEG) px[i] = load(xs, XR, at.xr + i * XR, xcol);
+                py[i] = load(ys, XR, at.xr + i * XR, xcol);
+            }
+#pragma unroll
+            for (int i = 0; i < ZV; ++i) pz[i] = load(zs, ZR, at.zr + i * ZR, zcol);
         }
-#pragma unroll
-        for (int i = 0; i < ZV; ++i) pz[i] = load(zp, z_tok, at_.zr + i * ZR, zcol);
     };
     auto place = [](int r, int c, int stride) { return M::at(r & ~15, r & 15, c, stride); };
     auto stage = [&](int c0) {
@@ -294,9 +363,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         if (m >= C && Kd == KP && (tile + 1) * ZC <= Vd) {
 #pragma unroll
             for (int i = 0; i < XV; ++i) {
-                const int at = place(xr0 + i * XR, xc, XS);
-                if constexpr (!SEG) *reinterpret_cast<la_u4*>(&Xs[at]) = px[i];
-                *reinterpret_cast<la_u4*>(&Ys[at]) = py[i];
+                if constexpr (!SEG) M::put_x(Xs, xr0 + i * XR, xc, XS, px[i]);
+                *reinterpret_cast<la_u4*>(&Ys[place(xr0 + i * XR, xc, XS)]) = py[i];
             }
 #pragma unroll
             for (int i = 0; i < ZV; ++i)
@@ -305,10 +373,10 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         }
 #pragma unroll
         for (int i = 0; i < XV; ++i) {
-            const int r = xr0 + i * XR, at = place(r, xc, XS);
+            const int r = xr0 + i * XR;
             const uint32_t keep = xok && r < m ? ~0u : 0u;
-            if constexpr (!SEG) *reinterpret_cast<la_u4*>(&Xs[at]) = px[i] & keep;
-            *reinterpret_cast<la_u4*>(&Ys[at]) = py[i] & keep;
+            if constexpr (!SEG) M::put_x(Xs, r, xc, XS, px[i] & keep);
+            *reinterpret_cast<la_u4*>(&Ys[place(r, xc, XS)]) = py[i] & keep;
         }
 #pragma unroll
         for (int i = 0; i < ZV; ++i) {
@@ -319,33 +387,37 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     };
     const float scale = p.scale;
     double walked = 0.0;                  // log2 decay of the chunks so far (SEG)
-    // A chunk's decay exponents (base 2), by the first wave: a lane per token.
+    // A chunk's decay exponents (base 2), by the last wave: a lane per token,
+    // summed over rows of 16 lanes and then across them without leaving the
+    // registers.
     auto decays = [&](int c0, int b) {
+        const int ln = fresh(lane);
         const float g = __uint_as_float(p.g_bf16 ? pg << 16 : pg);
-        const double own_g = lane < C && lane < n - c0
+        const double own_g = p.g && ln < C && ln < n - c0
                                  ? static_cast<double>(la_clamp_g(g)) * kLog2e : 0.0;
         double sum = own_g;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const double up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
-        const double all = __shfl(sum, C - 1);
+        sum += la_lanes<0x111, 0xf>(sum);             // lane - 1 of the row of 16
+        sum += la_lanes<0x112, 0xf>(sum);             // lane - 2
+        sum += la_lanes<0x114, 0xf>(sum);
+        sum += la_lanes<0x118, 0xf>(sum);
+        sum += la_lanes<0x142, 0xa>(sum);             // row 0's last to row 1, 2's to 3
+        if constexpr (C > 32) sum += la_lanes<0x143, 0xc>(sum);  // row 1's last to rows 2, 3
+        const double all = la_lane(sum, C - 1);
         if (reverse) sum -= own_g;
-        if (lane < C) {
+        if (ln < C) {
             const float hi = static_cast<float>(sum);
-            g_hi[b][lane] = hi;
-            g_lo[b][lane] = static_cast<float>(sum - static_cast<double>(hi));
-            g_in[b][lane] = scale * __builtin_amdgcn_exp2f(static_cast<float>(sum));
-            g_out[b][lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - sum));
+            g_hi[b][ln] = hi;
+            g_lo[b][ln] = static_cast<float>(sum - static_cast<double>(hi));
+            g_in[b][ln] = scale * __builtin_amdgcn_exp2f(static_cast<float>(sum));
+            g_out[b][ln] = __builtin_amdgcn_exp2f(static_cast<float>(all - sum));
         }
-        if (lane == 0) g_all[b] = __builtin_amdgcn_exp2f(static_cast<float>(all));
+        if (ln == 0) g_all[b] = __builtin_amdgcn_exp2f(static_cast<float>(all));
         if (SEG) walked += all;
     };
 
     if (n > 0) {
         fetch(0);
-        if (wave == 0) decays(0, 0);
+        if (wave == W - 1) decays(0, 0);
     }
     for (int c0 = 0, b = 0; c0 < n; c0 += C, b ^= 1) {
         stage(c0);
@@ -354,7 +426,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         if (more) fetch(c0 + C);
         const int ln = fresh(lane);
         const int g4 = (ln >> 4) * 4, i16 = ln & 15;
-        const int row_x = M::at(0, i16, g4, XS), col_y = M::col_place(ln, XS);
+        const int row_x = M::x_place(ln, XS), col_y = M::col_place(ln, XS);
         // a wave's own columns start at a multiple of 16 within a tile's rows
         const int col_z = M::step(M::col_place(ln, ZS), wave);
         la_f4 O[SEG ? 1 : IT];
@@ -365,12 +437,12 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
 #pragma unroll
             for (int kt = 0; kt < KT; kt += 2) {
                 Fr s0[N], s1[N];
-                split<T, N>(S[kt], s0);
-                split<T, N>(S[kt + 1], s1);
+                M::template split<N>(S[kt], s0);
+                M::template split<N>(S[kt + 1], s1);
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    const Fr x0 = M::row(&Xs[it * 16 * XS + M::step(row_x, kt)]);
-                    const Fr x1 = M::row(&Xs[it * 16 * XS + M::step(row_x, kt + 1)]);
+                    Fr x0, x1;
+                    M::x_pair(&Xs[it * 16 * XS], row_x, kt, x0, x1);
 #pragma unroll
                     for (int t = 0; t < N; ++t) O[it] = M::mma(s0[t], s1[t], x0, x1, O[it]);
                 }
@@ -382,12 +454,14 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 const int it = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3;
                 const int jt = t - it * (it + 1) / 2;
                 la_f4 acc = {0, 0, 0, 0};
-                const int rx = row_x + it * 16 * XS, ry = row_x + jt * 16 * XS;
+                const int ry = M::at(0, i16, g4, XS) + jt * 16 * XS;
 #pragma unroll
-                for (int kt = 0; kt < KT; kt += 2)
+                for (int kt = 0; kt < KT; kt += 2) {
+                    Fr x0, x1;
+                    M::x_pair(&Xs[it * 16 * XS], row_x, kt, x0, x1);
                     acc = M::mma(M::row(&Ys[M::step(ry, kt)]), M::row(&Ys[M::step(ry, kt + 1)]),
-                                 M::row(&Xs[M::step(rx, kt)]), M::row(&Xs[M::step(rx, kt + 1)]),
-                                 acc);
+                                 x0, x1, acc);
+                }
                 acc *= scale;
                 const int i = it * 16 + i16;
                 const float hi = g_hi[b][i], lo = g_lo[b][i];
@@ -402,11 +476,12 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                     acc[r] = keep ? acc[r] * e : 0.0f;
                 }
                 Fr pf[N];
-                split<T, N>(acc, pf);
+                M::template split<N>(acc, pf);
 #pragma unroll
                 for (int u = 0; u < N; ++u)
                     *reinterpret_cast<Fr*>(&Ps[(u * C + i) * PS + jt * 16 + g4]) = pf[u];
             }
+            if (more && wave == W - 1) decays(c0 + C, b ^ 1);
             __syncthreads();
         }
         // Z by columns: operand of P Z as it is, of the state's sum with its decay
@@ -463,18 +538,18 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 const uint32_t at = __umul24(static_cast<uint32_t>(reverse ? 15 - i16 : i16),
                                              static_cast<uint32_t>(out_tok / 4)) * sizeof(Vec) +
                                     g4 * OES;
+                char* base = out + (lead(c0, 16) * out_tok + head * out_head + zbase) * OES;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    char* const base = out + (lead(c0 + it * 16, 16) * out_tok +
-                                              head * out_head + zbase) * OES;
                     if (c0 + it * 16 + i16 < n && zbase + g4 < Vd)
                         *reinterpret_cast<Vec*>(base + at) = narrow(O[it]);
+                    base += dir * 16 * out_tok * OES;
                 }
             };
             if (out_f32) put([](la_f4 v) { return v; });
             else put([](la_f4 v) { return M::narrow(v); });
         }
-        if (more && wave == 0) decays(c0 + C, b ^ 1);
+        if (SEG && more && wave == W - 1) decays(c0 + C, b ^ 1);
         // ---- S <- exp(G_C) S + Y^T (decayed Z)
         const float all = g_all[b];
 #pragma unroll
@@ -484,8 +559,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + g4]);
             const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + 16 + g4]);
             Fr z0[N], z1[N];
-            split<T, N>(M::widen(zf[jt]) * w0, z0);
-            split<T, N>(M::widen(zf[jt + 1]) * w1, z1);
+            M::template split<N>(M::widen(zf[jt]) * w0, z0);
+            M::template split<N>(M::widen(zf[jt + 1]) * w1, z1);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
@@ -502,8 +577,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                     const la_f4 w1 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + 16 + g4]);
                     Fr z0[3], z1[3];
                     const T* z = &Zs[jt * 16 * ZS + col_z];
-                    split<T, 3>(M::widen(M::col(z, ZS)) * w0, z0);
-                    split<T, 3>(M::widen(M::col(z + 16 * ZS, ZS)) * w1, z1);
+                    M::template split<3>(M::widen(M::col(z, ZS)) * w0, z0);
+                    M::template split<3>(M::widen(M::col(z + 16 * ZS, ZS)) * w1, z1);
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt) {
                         const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
@@ -536,7 +611,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     };
     if (SEG) {
         store_state(w.last, int64_t{seg} * w.last.outer + head * w.last.head);
-        if (tid == 0 && tile == 0 && tot)
+        if (tid == TH - 1 && tile == 0 && tot)
             tot[(int64_t{reverse} * p.segs + seg) * p.nv + head] = static_cast<float>(walked);
         return;
     }
