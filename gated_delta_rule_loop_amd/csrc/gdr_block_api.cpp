@@ -498,6 +498,9 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
             (rc = no_alias(fn, dg, "dg", {d_o, q, k, v, g})))
             return rc;
     }
+    if (d.nv * d.K > kLaMaxTokenStride)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: v's heads times K above %lld", fn,
+                    static_cast<ll>(kLaMaxTokenStride));
     if (d.B == 0) return done();
     const LaPlan pl = la_plan(d.T, d.B, d.nk, d.nv, d.K, d.V, true);
     if ((rc = check_workspace(fn, workspace, pl.end)) ||

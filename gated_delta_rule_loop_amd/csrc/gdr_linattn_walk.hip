@@ -232,19 +232,17 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     const bool at_last = reverse ? sp.s == 0 : sp.s == sp.count - 1;
     if (SEG && at_last) return;           // no later segment needs its sum
     const bool sums = SUMS && w.row_sum != nullptr;
-    char* const out = static_cast<char*>(w.out);
-    const int64_t out_tok = w.out_tok, out_head = w.out_head;
 
     // Walk position r is token start + dir * r.
     const int64_t start = reverse ? int64_t{sp.t0} + n - 1 : sp.t0;
-    const int64_t dir = reverse ? -1 : 1;
+    const int dir = reverse ? -1 : 1;
     if (!SEG && slot == kPadSlot) {       // a padding row: zeros out, no state
         for (int64_t i = tid; i < int64_t{n} * ZC; i += TH) {
             const int z = tile * ZC + static_cast<int>(i % ZC);
-            const int64_t at = (sp.t0 + i / ZC) * out_tok + head * out_head + z;
+            const int64_t at = (sp.t0 + i / ZC) * w.out_tok + head * w.out_head + z;
             if (z < Vd) {
-                if (out_f32) reinterpret_cast<float*>(out)[at] = 0.0f;
-                else reinterpret_cast<T*>(out)[at] = T(0);
+                if (out_f32) static_cast<float*>(w.out)[at] = 0.0f;
+                else static_cast<T*>(w.out)[at] = T(0);
             }
         }
         return;
@@ -301,12 +299,12 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     };
     struct Stream {
         const char* q;                    // the next load's first token in memory
-        int64_t tok;                      // bytes from token to token
+        int32_t tok;                      // bytes from token to token, below 2^26
     };
     auto stream = [&](const LaTensor& t, int R) {
         return Stream{static_cast<const char*>(t.p) +
                           (head / t.div * t.head + (reverse ? start - (R - 1) : start) * t.tok) * ES,
-                      t.tok * ES};
+                      static_cast<int32_t>(t.tok * ES)};
     };
     Stream xs = stream(w.x, XR), ys = stream(w.y, XR), zs = stream(w.z, ZR);
     la_u4 px[SEG ? 1 : XV], py[XV], pz[ZV];
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 const uint32_t row = __umul24(static_cast<uint32_t>(reverse ? R - 1 - r : r),
                                               static_cast<uint32_t>(s.tok >> 4)) << 4;
                 const la_u4 v = *reinterpret_cast<const la_u4*>(s.q + (row + col));
-                s.q += dir * R * s.tok;
+                s.q += int64_t{dir * R} * s.tok;
                 return v;
             };
 #pragma unroll
@@ -385,6 +383,11 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             *reinterpret_cast<la_u4*>(&Zs[place(r, zc, ZS)]) = pz[i] & keep;
         }
     };
+    // The next 16 outputs' first token in memory, at this wave's columns
+    const int oes = out_f32 ? 4 : ES;
+    const int32_t out_tok = static_cast<int32_t>(w.out_tok);
+    char* out = static_cast<char*>(w.out) +
+                ((reverse ? start - 15 : start) * w.out_tok + head * w.out_head + zbase) * oes;
     const float scale = p.scale;
     double walked = 0.0;                  // log2 decay of the chunks so far (SEG)
     // A chunk's decay exponents (base 2), by the last wave: a lane per token,
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         stage(c0);
         __syncthreads();
         const bool more = c0 + C < n;
-        if (more) fetch(c0 + C);
+        // (with the decays' sums, after P: the loads' registers do not fit before)
+        if (!SUMS && more) fetch(c0 + C);
         const int ln = fresh(lane);
         const int g4 = (ln >> 4) * 4, i16 = ln & 15;
         const int row_x = M::x_place(ln, XS), col_y = M::col_place(ln, XS);
@@ -481,8 +485,10 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 for (int u = 0; u < N; ++u)
                     *reinterpret_cast<Fr*>(&Ps[(u * C + i) * PS + jt * 16 + g4]) = pf[u];
             }
-            if (more && wave == W - 1) decays(c0 + C, b ^ 1);
+            if (!SUMS && more && wave == W - 1) decays(c0 + C, b ^ 1);
             __syncthreads();
+            if (SUMS) __builtin_amdgcn_sched_barrier(0);
+            if (SUMS && more) fetch(c0 + C);
         }
         // Z by columns: operand of P Z as it is, of the state's sum with its decay
         Fr zf[IT];
@@ -501,6 +507,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                         O[it] = M::mma(zf[jt], zf[jt + 1], p0, p1, O[it]);
                     }
             if (sums) {
+                __builtin_amdgcn_sched_barrier(0);
                 // partner . out without the token's own pair, then that pair
                 const int64_t from = lead(c0, C);
                 const char* const qp = static_cast<const char*>(w.partner.p) +
@@ -513,6 +520,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 const int z = zbase + g4;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
+                    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
                     const int i = it * 16 + i16;
                     const int r0 = min(i, n - 1 - c0);
                     const uint32_t at = __umul24(reverse ? C - 1 - r0 : r0, q_tok) +
@@ -532,24 +540,25 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                     for (int r = 0; r < 4; ++r) O[it][r] = fmaf(d, zz[r], O[it][r]);
                 }
             }
+            if (SUMS) __builtin_amdgcn_sched_barrier(0);
             auto put = [&](auto narrow) {
                 typedef decltype(narrow(O[0])) Vec;
                 constexpr int OES = sizeof(Vec) / 4;
                 const uint32_t at = __umul24(static_cast<uint32_t>(reverse ? 15 - i16 : i16),
                                              static_cast<uint32_t>(out_tok / 4)) * sizeof(Vec) +
                                     g4 * OES;
-                char* base = out + (lead(c0, 16) * out_tok + head * out_head + zbase) * OES;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     if (c0 + it * 16 + i16 < n && zbase + g4 < Vd)
-                        *reinterpret_cast<Vec*>(base + at) = narrow(O[it]);
-                    base += dir * 16 * out_tok * OES;
+                        *reinterpret_cast<Vec*>(out + at) = narrow(O[it]);
+                    out += int64_t{dir * 16} * (out_tok * OES);
                 }
             };
             if (out_f32) put([](la_f4 v) { return v; });
             else put([](la_f4 v) { return M::narrow(v); });
         }
-        if (SEG && more && wave == W - 1) decays(c0 + C, b ^ 1);
+        if ((SEG || SUMS) && more && wave == W - 1) decays(c0 + C, b ^ 1);
+        if (SUMS) __builtin_amdgcn_sched_barrier(0);
         // ---- S <- exp(G_C) S + Y^T (decayed Z)
         const float all = g_all[b];
 #pragma unroll
