@@ -28,6 +28,8 @@
 // the bf16 output itself, and useless decay gradients.  float32 work uses the float32 matrix
 // instructions throughout.  Decay exponents are summed in float64 and kept as
 // a pair of float32.
+#include <type_traits>
+
 #include "gdr_linattn_dev.h"
 
 #ifndef GDR_WT
@@ -248,38 +250,6 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         return;
     }
 
-    // ---- the state.  All loads are issued together: indices past the state
-    // are clamped into it and their values replaced.
-    la_f4 S[KT];
-    auto load_as = [&](const LaState& s, auto* base, auto&& use) {
-        base += (s.by_segment ? int64_t{seg} : int64_t{slot}) * s.outer + head * s.head;
-        const int zo = min(zbase + i16, Vd - 1) * s.sz;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            la_f4 v;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int kd = kt * 16 + g4 + r;
-                const auto raw = base[min(kd, Kd - 1) * s.sk + zo];
-                float f;
-                if constexpr (sizeof(raw) == 2) f = la_widen(raw);
-                else f = raw;
-                v[r] = kd < Kd && zbase + i16 < Vd ? s.mult * f : 0.0f;
-            }
-            use(kt, v);
-        }
-    };
-    auto load_state = [&](const LaState& s, auto&& use) {
-        if (s.bf16) load_as(s, static_cast<const uint16_t*>(s.p), use);
-        else load_as(s, static_cast<const float*>(s.p), use);
-    };
-    if (!SEG && w.in.p) {
-        load_state(w.in, [&](int kt, la_f4 v) { S[kt] = v; });
-    } else {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] = la_f4{0, 0, 0, 0};
-    }
-
     // ---- a chunk's loads, held in registers until its LDS is free.  A load
     // takes XR (ZR) rows: its first token in memory is a uniform address that
     // moves on by `inc`, a thread's own row and column a 32-bit offset from it.
@@ -418,10 +388,58 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         if (SEG) walked += all;
     };
 
-    if (n > 0) {
-        fetch(0);
-        if (wave == W - 1) decays(0, 0);
+    if (n > 0) fetch(0);
+
+    // ---- the state.  A lane's 4 rows of a tile are neighbours: one vector where
+    // the walk's state is stored transposed.  Places are 32-bit offsets from a
+    // uniform base; all loads are in flight before the first value is used.
+    la_f4 S[KT];
+    const bool has_z = zbase + i16 < Vd;
+    auto load_as = [&](const LaState& s, auto* p0, la_f4 (&v)[KT]) {
+        typedef typename std::remove_const<typename std::remove_pointer<decltype(p0)>::type>::type E;
+        const char* base = reinterpret_cast<const char*>(
+            p0 + (s.by_segment ? int64_t{seg} : int64_t{slot}) * s.outer + head * s.head);
+        const uint32_t off = static_cast<uint32_t>((g4 * s.sk + (zbase + i16) * s.sz) *
+                                                   static_cast<int>(sizeof(E)));
+        const uint32_t row = static_cast<uint32_t>(s.sk * static_cast<int>(sizeof(E)));
+        typedef E E4 __attribute__((ext_vector_type(4)));
+        E4 raw[KT];
+        if (s.sk == 1) {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                raw[kt] = E4{0, 0, 0, 0};
+                if (has_z && kt * 16 + g4 < Kd)
+                    raw[kt] = *reinterpret_cast<const E4*>(base + kt * 16 * row + off);
+            }
+        } else {
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                raw[kt] = E4{0, 0, 0, 0};
+                if (has_z && kt * 16 + g4 < Kd)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        raw[kt][r] = *reinterpret_cast<const E*>(base + (kt * 16 + r) * row + off);
+            }
+        }
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if constexpr (sizeof(E) == 2) v[kt][r] = s.mult * la_widen(raw[kt][r]);
+                else v[kt][r] = s.mult * raw[kt][r];
+            }
+    };
+    auto load_state = [&](const LaState& s, la_f4 (&v)[KT]) {
+        if (s.bf16) load_as(s, static_cast<const uint16_t*>(s.p), v);
+        else load_as(s, static_cast<const float*>(s.p), v);
+    };
+    if (!SEG && w.in.p) {
+        load_state(w.in, S);
+    } else {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) S[kt] = la_f4{0, 0, 0, 0};
     }
+    if (n > 0 && wave == W - 1) decays(0, 0);
     for (int c0 = 0, b = 0; c0 < n; c0 += C, b ^= 1) {
         stage(c0);
         __syncthreads();
@@ -601,18 +619,30 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     }
 
     // ---- what is left
-    auto store_as = [&](const LaState& s, auto* base) {
+    auto store_as = [&](const LaState& s, auto* p0) {
+        typedef typename std::remove_pointer<decltype(p0)>::type E;
+        typedef E E4 __attribute__((ext_vector_type(4)));
+        char* base = reinterpret_cast<char*>(p0);
+        const uint32_t off = static_cast<uint32_t>((g4 * s.sk + (zbase + i16) * s.sz) *
+                                                   static_cast<int>(sizeof(E)));
+        const uint32_t row = static_cast<uint32_t>(s.sk * static_cast<int>(sizeof(E)));
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT; ++kt) {
+            if (!has_z || kt * 16 + g4 >= Kd) continue;
+            E4 v;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int kd = kt * 16 + g4 + r, z = zbase + i16;
-                if (kd < Kd && z < Vd) {
-                    const float v = s.mult * S[kt][r];
-                    if constexpr (sizeof(*base) == 2) base[kd * s.sk + z * s.sz] = la_round(v);
-                    else base[kd * s.sk + z * s.sz] = v;
-                }
+                if constexpr (sizeof(E) == 2) v[r] = la_round(s.mult * S[kt][r]);
+                else v[r] = s.mult * S[kt][r];
             }
+            if (s.sk == 1) {
+                *reinterpret_cast<E4*>(base + kt * 16 * row + off) = v;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<E*>(base + (kt * 16 + r) * row + off) = v[r];
+            }
+        }
     };
     auto store_state = [&](const LaState& s, int64_t at) {
         if (s.bf16) store_as(s, static_cast<uint16_t*>(s.p) + at);
@@ -626,11 +656,14 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     }
     if (SUMS && w.phi) {
         float sum = 0.0f;
-        if (w.phi_in.p)
-            load_state(w.phi_in, [&](int kt, la_f4 v) {
+        if (w.phi_in.p) {
+            la_f4 back[KT];
+            load_state(w.phi_in, back);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sum = fmaf(S[kt][r], v[r], sum);
-            });
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sum = fmaf(S[kt][r], back[kt][r], sum);
+        }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
         if (lane == 0)
