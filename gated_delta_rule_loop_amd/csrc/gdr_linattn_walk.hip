@@ -230,9 +230,13 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     const int g4 = (lane >> 4) * 4, i16 = lane & 15;
     const int zbase = tile * ZC + wave * 16;        // this wave's columns
     const uint32_t slot = p.slot_idx ? p.slot_idx[sp.row] : static_cast<uint32_t>(sp.row);
-    const bool third = w.third != 0, reverse = w.reverse != 0, out_f32 = w.out_f32 != 0;
-    const bool at_last = reverse ? sp.s == 0 : sp.s == sp.count - 1;
-    if (SEG && at_last) return;           // no later segment needs its sum
+    const bool third = w.third != 0, out_f32 = w.out_f32 != 0;
+    const bool at_last = w.reverse ? sp.s == 0 : sp.s == sp.count - 1;
+    // A segment's sum is taken from its far end: the state needs no decay on the
+    // way (the factor of a chunk's tokens takes what was walked), and the walk
+    // that follows starts with what was read last.
+    const bool reverse = SEG ? !w.reverse : w.reverse != 0;
+    if (SEG && at_last) return;           // no segment after it in the walk needs its sum
     const bool sums = SUMS && w.row_sum != nullptr;
 
     // Walk position r is token start + dir * r.
@@ -382,7 +386,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             g_hi[b][ln] = hi;
             g_lo[b][ln] = static_cast<float>(sum - static_cast<double>(hi));
             g_in[b][ln] = scale * __builtin_amdgcn_exp2f(static_cast<float>(sum));
-            g_out[b][ln] = __builtin_amdgcn_exp2f(static_cast<float>(all - sum));
+            g_out[b][ln] =
+                __builtin_amdgcn_exp2f(static_cast<float>(SEG ? walked + sum : all - sum));
         }
         if (ln == 0) g_all[b] = __builtin_amdgcn_exp2f(static_cast<float>(all));
         if (SEG) walked += all;
@@ -456,18 +461,35 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             // scale exp(G_i) (S^T X^T): rows are columns of the state, columns tokens
 #pragma unroll
             for (int it = 0; it < IT; ++it) O[it] = la_f4{0, 0, 0, 0};
+            // Two token tiles at a time, the next two's operands on their way: a
+            // wave that waits for each read before its products takes 2 to 3 times
+            // as long.
+            Fr x[2][2][2];                // [of two steps][tile][half]
+            auto read_x = [&](int step) {
+                const int kt = step / (IT / 2) * 2, it = step % (IT / 2) * 2;
 #pragma unroll
-            for (int kt = 0; kt < KT; kt += 2) {
-                Fr s0[N], s1[N];
-                M::template split<N>(S[kt], s0);
-                M::template split<N>(S[kt + 1], s1);
+                for (int j = 0; j < 2; ++j)
+                    M::x_pair(&Xs[(it + j) * 16 * XS], row_x, kt, x[step & 1][j][0],
+                              x[step & 1][j][1]);
+            };
+            constexpr int STEPS = KT / 2 * (IT / 2);
+            Fr s0[N], s1[N];
+            read_x(0);
 #pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    Fr x0, x1;
-                    M::x_pair(&Xs[it * 16 * XS], row_x, kt, x0, x1);
-#pragma unroll
-                    for (int t = 0; t < N; ++t) O[it] = M::mma(s0[t], s1[t], x0, x1, O[it]);
+            for (int step = 0; step < STEPS; ++step) {
+                const int kt = step / (IT / 2) * 2, it = step % (IT / 2) * 2;
+                if (it == 0) {
+                    M::template split<N>(S[kt], s0);
+                    M::template split<N>(S[kt + 1], s1);
                 }
+                if (step + 1 < STEPS) read_x(step + 1);
+#pragma unroll
+                for (int t = 0; t < N; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        O[it + j] = M::mma(s0[t], s1[t], x[step & 1][j][0], x[step & 1][j][1],
+                                           O[it + j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int it = 0; it < IT; ++it) O[it] *= g_in[b][it * 16 + i16];
@@ -578,9 +600,11 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         if ((SEG || SUMS) && more && wave == W - 1) decays(c0 + C, b ^ 1);
         if (SUMS) __builtin_amdgcn_sched_barrier(0);
         // ---- S <- exp(G_C) S + Y^T (decayed Z)
-        const float all = g_all[b];
+        if constexpr (!SEG) {
+            const float all = g_all[b];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) S[kt] *= all;
+            for (int kt = 0; kt < KT; ++kt) S[kt] *= all;
+        }
 #pragma unroll
         for (int jt = 0; jt < IT; jt += 2) {
             const la_f4 w0 = *reinterpret_cast<const la_f4*>(&g_out[b][jt * 16 + g4]);
@@ -588,12 +612,26 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             Fr z0[N], z1[N];
             M::template split<N>(M::widen(zf[jt]) * w0, z0);
             M::template split<N>(M::widen(zf[jt + 1]) * w1, z1);
+            Fr y[2][2][2];                // [of two steps][row tile][half]
+            auto read_y = [&](int kt) {
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-                const Fr y0 = M::col(&Ys[jt * 16 * XS + M::step(col_y, kt)], XS);
-                const Fr y1 = M::col(&Ys[(jt + 1) * 16 * XS + M::step(col_y, kt)], XS);
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int u = 0; u < N; ++u) S[kt] = M::mma(y0, y1, z0[u], z1[u], S[kt]);
+                    for (int h = 0; h < 2; ++h)
+                        y[kt >> 1 & 1][j][h] = M::col(
+                            &Ys[(jt + h) * 16 * XS + M::step(col_y, kt + j)], XS);
+            };
+            read_y(0);
+#pragma unroll
+            for (int kt = 0; kt < KT; kt += 2) {
+                if (kt + 2 < KT) read_y(kt + 2);
+#pragma unroll
+                for (int u = 0; u < N; ++u)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        S[kt + j] = M::mma(y[kt >> 1 & 1][j][0], y[kt >> 1 & 1][j][1], z0[u],
+                                           z1[u], S[kt + j]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
         if constexpr (N > 1) {
@@ -651,7 +689,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     if (SEG) {
         store_state(w.last, int64_t{seg} * w.last.outer + head * w.last.head);
         if (tid == TH - 1 && tile == 0 && tot)
-            tot[(int64_t{reverse} * p.segs + seg) * p.nv + head] = static_cast<float>(walked);
+            tot[(int64_t{w.reverse} * p.segs + seg) * p.nv + head] = static_cast<float>(walked);
         return;
     }
     if (SUMS && w.phi) {
