@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -72,11 +73,12 @@ def lib():
         i64 = ctypes.c_int64
         L.gdr_check_indices.argtypes = [i64, vp, i64, vp, i64, vp, i64, i64, vp]
         L.gdr_set_debug_checks.argtypes = [ctypes.c_int]
-        L.gdr_linear_attention_fwd.argtypes = [P] * 6 + [f32] + [P] * 5 + [vp]
-        L.gdr_linear_attention_step.argtypes = [P] * 7 + [f32, vp]
-        L.gdr_linear_attention_bwd.argtypes = [P] * 6 + [f32] + [P] * 8 + [vp]
-        L.gdr_block_norm.argtypes = [P] * 7 + [i64, f32, f32, u32, vp]
-        L.gdr_block_norm_bwd.argtypes = [P] * 12 + [i64, f32, f32, u32, P, vp]
+        # these take their descriptors by address (_describe_all)
+        L.gdr_linear_attention_fwd.argtypes = [vp] * 6 + [f32] + [vp] * 6
+        L.gdr_linear_attention_step.argtypes = [vp] * 7 + [f32, vp]
+        L.gdr_linear_attention_bwd.argtypes = [vp] * 6 + [f32] + [vp] * 9
+        L.gdr_block_norm.argtypes = [vp] * 7 + [i64, f32, f32, u32, vp]
+        L.gdr_block_norm_bwd.argtypes = [vp] * 12 + [i64, f32, f32, u32, vp, vp]
         L.gdr_linear_attention_workspace.argtypes = [i64, i64, i32, i32, i32, i32, ctypes.c_int]
         L.gdr_block_norm_workspace.argtypes = [i64, i64]
         for name in ("gdr_linear_attention_workspace", "gdr_block_norm_workspace"):
@@ -111,6 +113,40 @@ def describe(t, *, allow_host=False):
         d.shape[i] = s
         d.stride[i] = st
     return d
+
+
+# gdr_tensor as struct.pack writes it, by rank.
+_PACK = [struct.Struct(f"Pii{n}q{8 * (MAX_DIMS - n)}x{n}q{8 * (MAX_DIMS - n)}x").pack_into
+         for n in range(MAX_DIMS + 1)]
+_DESC_BYTES = ctypes.sizeof(GdrTensor)
+
+
+def _describe_all(tensors):
+    """(addresses of the tensors' gdr_tensors, None where a tensor is None, the
+    buffer that holds them): describe() for a whole call, without a ctypes
+    object for each tensor (a call's host time is a third of describe()'s)."""
+    buf = bytearray(_DESC_BYTES * len(tensors))
+    base = ctypes.addressof(ctypes.c_char.from_buffer(buf))
+    refs, at = [], 0
+    for t in tensors:
+        if t is None:
+            refs.append(None)
+        else:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"expected a torch.Tensor, got {type(t)}")
+            if not t.is_cuda:
+                raise ValueError("gdr kernels take device tensors")
+            code = _DTYPES.get(t.dtype)
+            if code is None:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            shape = t.shape
+            n = len(shape)
+            if n > MAX_DIMS:
+                raise ValueError("rank above 5")
+            _PACK[n](buf, at, t.data_ptr(), code, n, *shape, *t.stride())
+            refs.append(base + at)
+        at += _DESC_BYTES
+    return refs, buf
 
 
 def _ref(d):
@@ -265,6 +301,23 @@ def gdr_set_debug_checks(enable):
     return bool(lib().gdr_set_debug_checks(1 if enable else 0))
 
 
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream, t):
+    """The stream's handle: the caller's, or torch's current one on t's device
+    (asked for without building a Stream object where torch can)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_handle is not None:
+        return _current_handle(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _scale_value(scale):
+    return -1.0 if scale is None else float(scale)  # not positive or NaN: the default
+
+
 def _scratch(floats, like, stream):
     """float32 workspace for a call on `stream` (torch's current one when None)."""
     if floats <= 0:
@@ -273,6 +326,14 @@ def _scratch(floats, like, stream):
     if stream is not None:  # allocated on the current stream, used on the caller's
         ws.record_stream(stream)
     return ws
+
+
+def _new(like, shape=None, dtype=None, stream=None):
+    """An output allocated here: on the current stream, written on the caller's."""
+    t = like.new_empty(like.shape if shape is None else shape, dtype=dtype or like.dtype)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def gdr_linear_attention_workspace(tokens, rows, num_key_heads, num_value_heads, key_head_dim,
@@ -286,8 +347,9 @@ def gdr_linear_attention_workspace(tokens, rows, num_key_heads, num_value_heads,
 def _attention_scratch(q, v, offsets, backward, workspace, stream):
     if workspace is not None:
         return workspace
-    n = gdr_linear_attention_workspace(q.shape[0], offsets.shape[0] - 1, q.shape[1], v.shape[1],
-                                       q.shape[2], v.shape[2], backward)
+    T, nk, K = q.shape
+    _, nv, V = v.shape
+    n = lib().gdr_linear_attention_workspace(T, offsets.shape[0] - 1, nk, nv, K, V, backward)
     return _scratch(n, q, stream)
 
 
@@ -303,16 +365,16 @@ def gdr_linear_attention_fwd(q, k, v, g, input_row_offsets, *, state=None, slot_
     (allocated here when output_final_state is set), else None.  o and the
     workspace are allocated here with torch when not passed in."""
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = _new(v, stream=stream)
     if state is None and output_final_state and final_state is None:
         dt = initial_state.dtype if initial_state is not None else torch.float32
-        final_state = torch.empty((input_row_offsets.shape[0] - 1, v.shape[1], q.shape[2],
-                                   v.shape[2]), dtype=dt, device=v.device)
-    ws = _attention_scratch(q, v, input_row_offsets, False, workspace, stream)
-    ds = [describe(x) for x in (o, q, k, v, g, input_row_offsets)]
-    more = [describe(x) for x in (initial_state, final_state, state, slot_idx, ws)]
-    rc = lib().gdr_linear_attention_fwd(*[_ref(d) for d in ds], _scale(scale),
-                                        *[_ref(d) for d in more], _stream(stream))
+        final_state = _new(v, (input_row_offsets.shape[0] - 1, v.shape[1], q.shape[2],
+                               v.shape[2]), dt, stream)
+    ws = _attention_scratch(q, v, input_row_offsets, 0, workspace, stream)
+    r, _buf = _describe_all((o, q, k, v, g, input_row_offsets, initial_state, final_state, state,
+                             slot_idx, ws))
+    rc = lib().gdr_linear_attention_fwd(*r[:6], _scale_value(scale), *r[6:],
+                                        _stream_of(stream, q))
     _check("gdr_linear_attention_fwd", rc)
     return o, (state if state is not None else final_state)
 
@@ -322,9 +384,9 @@ def gdr_linear_attention_step(q, k, v, g, state, slot_idx=None, *, scale=None, o
     """One token for each row (q, k [B, nk, K]; v [B, nv, V]; g [B, nv] or
     None), with the row's state updated in place in its slot.  Returns o."""
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    ds = [describe(x) for x in (o, q, k, v, g, state, slot_idx)]
-    rc = lib().gdr_linear_attention_step(*[_ref(d) for d in ds], _scale(scale), _stream(stream))
+        o = _new(v, stream=stream)
+    r, _buf = _describe_all((o, q, k, v, g, state, slot_idx))
+    rc = lib().gdr_linear_attention_step(*r, _scale_value(scale), _stream_of(stream, q))
     _check("gdr_linear_attention_step", rc)
     return o
 
@@ -339,25 +401,23 @@ def gdr_linear_attention_bwd(do, q, k, v, g, input_row_offsets, *, initial_state
     need_dinitial_state is set).  dg has one entry per token and head; a decay
     that tokens share gets their sum.  Outputs and the workspace are allocated
     here with torch when not passed in."""
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
-    dq = new(q) if dq is None else dq
-    dk = new(k) if dk is None else dk
-    dv = new(v) if dv is None else dv
+    dq = _new(q, stream=stream) if dq is None else dq
+    dk = _new(k, stream=stream) if dk is None else dk
+    dv = _new(v, stream=stream) if dv is None else dv
     if g is not None and need_dg and dg is None:
-        dg = new(g)
+        dg = _new(g, stream=stream)
     if need_dinitial_state is None:
         need_dinitial_state = initial_state is not None
     if need_dinitial_state and dinitial_state is None:
         like = initial_state if initial_state is not None else dfinal_state
         dt = like.dtype if like is not None else torch.float32
-        dinitial_state = torch.empty((input_row_offsets.shape[0] - 1, v.shape[1], q.shape[2],
-                                      v.shape[2]), dtype=dt, device=v.device)
-    ws = _attention_scratch(q, v, input_row_offsets, True, workspace, stream)
-    ds = [describe(x) for x in (do, q, k, v, g, input_row_offsets)]
-    more = [describe(x) for x in (initial_state, dfinal_state, dq, dk, dv, dg, dinitial_state,
-                                  ws)]
-    rc = lib().gdr_linear_attention_bwd(*[_ref(d) for d in ds], _scale(scale),
-                                        *[_ref(d) for d in more], _stream(stream))
+        dinitial_state = _new(v, (input_row_offsets.shape[0] - 1, v.shape[1], q.shape[2],
+                                  v.shape[2]), dt, stream)
+    ws = _attention_scratch(q, v, input_row_offsets, 1, workspace, stream)
+    r, _buf = _describe_all((do, q, k, v, g, input_row_offsets, initial_state, dfinal_state, dq,
+                             dk, dv, dg, dinitial_state, ws))
+    rc = lib().gdr_linear_attention_bwd(*r[:6], _scale_value(scale), *r[6:],
+                                        _stream_of(stream, q))
     _check("gdr_linear_attention_bwd", rc)
     return dq, dk, dv, dg, dinitial_state
 
@@ -374,12 +434,12 @@ def gdr_block_norm(y, *, post_weight=None, group=0, gate=None, activation=None, 
     (h, n), n None without pre_weight; both are allocated here with torch when
     not passed in."""
     if h is None:
-        h = torch.empty(y.shape, dtype=y.dtype, device=y.device)
+        h = _new(y, stream=stream)
     if pre_weight is not None and n is None:
-        n = torch.empty(y.shape, dtype=y.dtype, device=y.device)
-    ds = [describe(x) for x in (h, n, y, residual, gate, post_weight, pre_weight)]
-    rc = lib().gdr_block_norm(*[_ref(d) for d in ds], int(group), float(residual_scale),
-                              float(eps), _ACTIVATIONS[activation], _stream(stream))
+        n = _new(y, stream=stream)
+    r, _buf = _describe_all((h, n, y, residual, gate, post_weight, pre_weight))
+    rc = lib().gdr_block_norm(*r, group, residual_scale, eps, _ACTIVATIONS[activation],
+                              _stream_of(stream, y))
     _check("gdr_block_norm", rc)
     return h, n
 
@@ -398,25 +458,23 @@ def gdr_block_norm_bwd(dh, dn, y, h, *, post_weight=None, group=0, gate=None, ac
     pre_weight only.  Returns (dresidual, dgate, dy, dpost_weight,
     dpre_weight), None for what the forward did not have.  Without pre_weight
     dresidual is dh itself."""
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
     dx = dresidual
     if residual and dx is None and pre_weight is not None:
-        dx = new(y)
-    dy = new(y) if dy is None else dy
-    dgate = new(gate) if gate is not None and dgate is None else dgate
+        dx = _new(y, stream=stream)
+    dy = _new(y, stream=stream) if dy is None else dy
+    dgate = _new(gate, stream=stream) if gate is not None and dgate is None else dgate
     if post_weight is not None and dpost_weight is None:
-        dpost_weight = new(post_weight)
+        dpost_weight = _new(post_weight, stream=stream)
     if pre_weight is not None and dpre_weight is None:
-        dpre_weight = new(pre_weight)
+        dpre_weight = _new(pre_weight, stream=stream)
     ws = workspace
     if ws is None and y.dim() == 2:
-        ws = _scratch(gdr_block_norm_workspace(*y.shape), y, stream)
-    ds = [describe(x) for x in (dx, dy, dgate, dpost_weight, dpre_weight, dh, dn, y,
-                                h if pre_weight is not None else None, gate, post_weight,
-                                pre_weight)]
-    rc = lib().gdr_block_norm_bwd(*[_ref(d) for d in ds], int(group), float(residual_scale),
-                                  float(eps), _ACTIVATIONS[activation], _ref(describe(ws)),
-                                  _stream(stream))
+        ws = _scratch(lib().gdr_block_norm_workspace(*y.shape), y, stream)
+    r, _buf = _describe_all((dx, dy, dgate, dpost_weight, dpre_weight, dh, dn, y,
+                             h if pre_weight is not None else None, gate, post_weight, pre_weight,
+                             ws))
+    rc = lib().gdr_block_norm_bwd(*r[:12], group, residual_scale, eps, _ACTIVATIONS[activation],
+                                  r[12], _stream_of(stream, y))
     _check("gdr_block_norm_bwd", rc)
     return (dx if dx is not None else dh) if residual else None, dgate, dy, dpost_weight, \
         dpre_weight

@@ -6,6 +6,9 @@
 // once and every output written once; the arithmetic and the sums of squares
 // are float32.  Bound by HBM.
 #include "gdr_norm.h"
+
+#include <algorithm>
+
 #include "gdr_linattn_dev.h"
 
 namespace gdr {
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
 // b, b + parts, ...; it sums its rows' weight gradients in registers and writes
 // them once, and norm_reduce_kernel adds the parts in order.
 template <typename T, int NV, int GM, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormParams p) {
+__global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p) {
     extern __shared__ __attribute__((aligned(16))) float lds[];
     float* red = lds;                     // [16]
     float* per_unit = lds + 16;           // [units] kAny, [D] to fold a shared weight
@@ -336,25 +339,39 @@ __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormParams p) {
     }
 }
 
-// Sums of up to three arrays of parts over the parts: 64 columns a workgroup,
-// 16 threads down the parts of each column.
+// Sums of up to three arrays of parts over the parts: 16 columns a workgroup,
+// 64 threads down the parts of each column, whose sums are added in order.
 struct NormReduces { NormReduce r[3]; };
-__global__ void __launch_bounds__(1024) norm_reduce_kernel(const NormReduces a) {
-    __shared__ float lds[16][64];
+constexpr int kReduceCols = 16, kReduceWalk = 64;
+__global__ void __launch_bounds__(kReduceCols * kReduceWalk)
+    norm_reduce_kernel(const NormReduces a) {
+    __shared__ float lds[kReduceWalk][kReduceCols];
     const NormReduce& r = a.r[blockIdx.y];
-    const int col = threadIdx.x & 63, walk = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + col;
-    if (static_cast<int>(blockIdx.x) * 64 >= r.n) return;
+    const int col = threadIdx.x % kReduceCols, walk = threadIdx.x / kReduceCols;
+    const int c = blockIdx.x * kReduceCols + col;
+    if (static_cast<int>(blockIdx.x) * kReduceCols >= r.n) return;
     float s = 0.0f;
-    if (c < r.n)
-        for (int k = walk; k < r.parts; k += 16) s += r.part[int64_t{k} * r.n + c];
+    if (c < r.n) {
+        const float* q = r.part + c;
+        int k = walk;
+        for (; k + 3 * kReduceWalk < r.parts; k += 4 * kReduceWalk) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = q[int64_t{k + i * kReduceWalk} * r.n];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s += v[i];
+        }
+        for (; k < r.parts; k += kReduceWalk) s += q[int64_t{k} * r.n];
+    }
     lds[walk][col] = s;
     __syncthreads();
-    if (walk == 0 && c < r.n) {
+    if (walk < 4) {
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) sum += lds[k][col];
-        la_store(r.out, c, r.out_bf16, sum);
+        for (int k = 0; k < kReduceWalk / 4; ++k) sum += lds[walk * (kReduceWalk / 4) + k][col];
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (walk == 0 && c < r.n) la_store(r.out, c, r.out_bf16, sum);
     }
 }
 
@@ -365,6 +382,9 @@ int row_threads(int D, int nv) {
     while (t * nv < units && t < 1024) t *= 2;
     return t;
 }
+
+// Units of 8 values a thread, where a row fits 1024 threads that way.
+constexpr int kFwdUnits = 2, kBwdUnits = 1;
 
 int group_mode(const NormParams& p) {
     if (!p.w1.p) return kNoNorm;
@@ -395,18 +415,22 @@ hipError_t run_mode(const NormParams& p, int threads, hipStream_t s) {
 
 template <typename T, bool BWD>
 hipError_t run(const NormParams& p, hipStream_t s) {
-    const int threads = row_threads(p.D, 2);
-    if (threads <= 256) return run_mode<T, 2, 256, BWD>(p, threads, s);
-    if (threads <= 512) return run_mode<T, 2, 512, BWD>(p, threads, s);
-    return run_mode<T, 2, 1024, BWD>(p, threads, s);
+    constexpr int units = BWD ? kBwdUnits : kFwdUnits;
+    const int threads = row_threads(p.D, units);
+    if (threads * units * 8 < p.D) return run_mode<T, 2, 1024, BWD>(p, 1024, s);
+    if (threads <= 256) return run_mode<T, units, 256, BWD>(p, threads, s);
+    if (threads <= 512) return run_mode<T, units, 512, BWD>(p, threads, s);
+    return run_mode<T, units, 1024, BWD>(p, threads, s);
 }
 
 }  // namespace
 
 int norm_parts(int64_t T, int D) {
-    // four workgroups a compute unit at 256 threads, as many threads in all at other sizes
-    const int64_t most = 1024 * 256 / (row_threads(D, 2) < 256 ? 256 : row_threads(D, 2));
-    return static_cast<int>(T < most ? T : most);
+    // as many workgroups as the chip holds at 16 waves a compute unit (fewer than
+    // that need more rows in flight), and a few rows each: a part costs a write
+    // and a read of a row for each weight
+    const int64_t most = std::min<int64_t>(1024, 256 * 16 * 64 / row_threads(D, kBwdUnits));
+    return static_cast<int>(std::min(T, std::min(most, std::max<int64_t>(256, T / 4))));
 }
 
 hipError_t launch_norm(const NormParams& p, bool work_bf16, hipStream_t s) {
@@ -422,7 +446,8 @@ hipError_t launch_norm_reduce(const NormReduce* r, int count, hipStream_t s) {
         a.r[i] = r[i];
         n = r[i].n > n ? r[i].n : n;
     }
-    norm_reduce_kernel<<<dim3((n + 63) / 64, count), 1024, 0, s>>>(a);
+    norm_reduce_kernel<<<dim3((n + kReduceCols - 1) / kReduceCols, count),
+                         kReduceCols * kReduceWalk, 0, s>>>(a);
     return hipGetLastError();
 }
 
