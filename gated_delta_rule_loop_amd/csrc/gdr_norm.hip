@@ -47,35 +47,51 @@ __device__ __forceinline__ void load8(const NormVec& w, int i, float (&v)[8]) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// Sum over the workgroup, the same bits in every thread.  `red` holds one
-// float per wave; two barriers.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Sums over the workgroup, the same bits in every thread, with one barrier
+// each: `red` holds a float per wave in each of kSlots slots used in turn, so
+// that a slot's last readers are barriers away from its next writers.
+constexpr int kSlots = 4;
+struct BlockSums {
+    float* red;
+    int slot = 0;
+    __device__ explicit BlockSums(float* r) : red(r) {}
+    template <int N> __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    const int waves = blockDim.x >> 6;
-    if (waves == 1) return v;
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float sum = 0.0f;
-    for (int i = 0; i < waves; ++i) sum += red[i];
-    __syncthreads();
-    return sum;
-}
+        for (int d = 1; d < 64; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
+        const int waves = blockDim.x >> 6;
+        if (waves == 1) return;
+        float* const r = red + slot * 16 * 2;
+        slot = (slot + 1) % kSlots;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) r[i * 16 + (threadIdx.x >> 6)] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float sum = 0.0f;
+            for (int k = 0; k < waves; ++k) sum += r[i * 16 + k];
+            v[i] = sum;
+        }
+    }
+};
+constexpr int kRedFloats = kSlots * 2 * 16;
 
 // How the values of a group share a sum (group / 8 units of 8 values each).
 enum GroupMode { kNoNorm, kWholeRow, kLanes, kAny };
 
 // Sums of v[i] (one value per unit tid + i * threads) over each unit's group.
 template <int NV, int GM>
-__device__ __forceinline__ void group_sum(float (&v)[NV], int gu, int units, float* red,
+__device__ __forceinline__ void group_sum(float (&v)[NV], int gu, int units, BlockSums& block,
                                           float* per_unit) {
     if constexpr (GM == kWholeRow) {
-        float s = 0.0f;
+        float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < NV; ++i) s += v[i];
-        s = block_sum(s, red);
+        for (int i = 0; i < NV; ++i) s[0] += v[i];
+        block(s);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = s;
+        for (int i = 0; i < NV; ++i) v[i] = s[0];
     } else if constexpr (GM == kLanes) {  // gu is a power of two up to 64
         for (int d = 1; d < gu; d <<= 1)
 #pragma unroll
@@ -102,8 +118,8 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], int gu, int units, flo
 template <typename T, int NV, int GM, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    float* red = lds;                     // [16]
-    float* per_unit = lds + 16;           // [units], kAny only
+    BlockSums block(lds);
+    float* per_unit = lds + kRedFloats;   // [units], kAny only
     const int64_t t = blockIdx.x;
     const int units = p.D >> 3, gu = p.group >> 3;
     const T* y = static_cast<const T*>(p.y) + t * p.y_row;
@@ -125,11 +141,11 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
             for (int e = 0; e < 8; ++e) r[i] = fmaf(yv[i][e], yv[i][e], r[i]);
     }
     if constexpr (GM != kNoNorm) {
-        group_sum<NV, GM>(r, gu, units, red, per_unit);
+        group_sum<NV, GM>(r, gu, units, block, per_unit);
 #pragma unroll
         for (int i = 0; i < NV; ++i) r[i] = 1.0f / sqrtf(r[i] / static_cast<float>(p.group) + p.eps);
     }
-    float sq = 0.0f;
+    float sq[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -149,14 +165,15 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
                 }
                 if (p.x) u += xv[i][e];
                 yv[i][e] = u;
-                sq = fmaf(u, u, sq);
+                sq[0] = fmaf(u, u, sq[0]);
             }
             store8(static_cast<T*>(p.h) + t * p.h_row + c, yv[i]);
         }
     }
     if (!p.w2.p) return;
     // n is the norm of h before h's rounding
-    const float rh = 1.0f / sqrtf(block_sum(sq, red) / static_cast<float>(p.D) + p.eps);
+    block(sq);
+    const float rh = 1.0f / sqrtf(sq[0] / static_cast<float>(p.D) + p.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -178,8 +195,8 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormParams p) {
 template <typename T, int NV, int GM, int THREADS>
 __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p) {
     extern __shared__ __attribute__((aligned(16))) float lds[];
-    float* red = lds;                     // [16]
-    float* per_unit = lds + 16;           // [units] kAny, [D] to fold a shared weight
+    BlockSums block(lds);
+    float* per_unit = lds + kRedFloats;   // [units] kAny, [D] to fold a shared weight
     const int units = p.D >> 3, gu = p.group >> 3;
     float a1[NV][8], a2[NV][8], ag[NV][8];
 #pragma unroll
@@ -206,7 +223,8 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
             }
         }
         if (p.w2.p) {
-            float hv[NV][8], tv[NV][8], sq = 0.0f, dot = 0.0f;
+            // with a norm over whole rows its squares are summed along
+            float hv[NV][8], tv[NV][8], sq[2] = {0.0f, 0.0f}, dot[1] = {0.0f};
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -216,10 +234,15 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
                     load8(static_cast<const T*>(p.h) + t * p.h_row + c, hv[i]);
                     load8(static_cast<const T*>(p.dn) + t * p.dn_row + c, tv[i]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) sq = fmaf(hv[i][e], hv[i][e], sq);
+                    for (int e = 0; e < 8; ++e) sq[0] = fmaf(hv[i][e], hv[i][e], sq[0]);
                 }
+                sq[1] += r[i];
             }
-            const float rh = 1.0f / sqrtf(block_sum(sq, red) / static_cast<float>(p.D) + p.eps);
+            block(sq);
+            if constexpr (GM == kWholeRow)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) r[i] = sq[1];
+            const float rh = 1.0f / sqrtf(sq[0] / static_cast<float>(p.D) + p.eps);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -231,11 +254,12 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
                         hv[i][e] *= rh;
                         a2[i][e] = fmaf(tv[i][e], hv[i][e], a2[i][e]);
                         tv[i][e] *= w[e];
-                        dot = fmaf(tv[i][e], hv[i][e], dot);
+                        dot[0] = fmaf(tv[i][e], hv[i][e], dot[0]);
                     }
                 }
             }
-            const float mean = block_sum(dot, red) / static_cast<float>(p.D);
+            block(dot);
+            const float mean = dot[0] / static_cast<float>(p.D);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -254,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
             }
         }
         if constexpr (GM != kNoNorm) {
-            group_sum<NV, GM>(r, gu, units, red, per_unit);
+            if (GM != kWholeRow || !p.w2.p) group_sum<NV, GM>(r, gu, units, block, per_unit);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 r[i] = 1.0f / sqrtf(r[i] / static_cast<float>(p.group) + p.eps);
@@ -298,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
                 if (p.dgate) store8(static_cast<T*>(p.dgate) + t * p.dgate_row + c, gv[i]);
             }
         }
-        if constexpr (GM != kNoNorm) group_sum<NV, GM>(dot, gu, units, red, per_unit);
+        if constexpr (GM != kNoNorm) group_sum<NV, GM>(dot, gu, units, block, per_unit);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -396,9 +420,9 @@ int group_mode(const NormParams& p) {
 template <typename T, int NV, int THREADS, bool BWD>
 hipError_t run_mode(const NormParams& p, int threads, hipStream_t s) {
     const int gm = group_mode(p);
-    uint32_t lds = 16 * sizeof(float);
+    uint32_t lds = kRedFloats * sizeof(float);
     if (gm == kAny) lds += p.D / 8 * sizeof(float);
-    if (BWD && p.pw1 && p.w1_len != p.D) lds = static_cast<uint32_t>((16 + p.D) * sizeof(float));
+    if (BWD && p.pw1 && p.w1_len != p.D) lds = static_cast<uint32_t>((kRedFloats + p.D) * sizeof(float));
     const dim3 grid(static_cast<uint32_t>(BWD ? p.parts : p.T));
 #define GDR_NORM_RUN(GM)                                                        \
     do {                                                                        \
@@ -426,11 +450,11 @@ hipError_t run(const NormParams& p, hipStream_t s) {
 }  // namespace
 
 int norm_parts(int64_t T, int D) {
-    // as many workgroups as the chip holds at 16 waves a compute unit (fewer than
-    // that need more rows in flight), and a few rows each: a part costs a write
-    // and a read of a row for each weight
+    // as many workgroups as the chip holds at 16 waves a compute unit, with rows
+    // shared evenly
     const int64_t most = std::min<int64_t>(1024, 256 * 16 * 64 / row_threads(D, kBwdUnits));
-    return static_cast<int>(std::min(T, std::min(most, std::max<int64_t>(256, T / 4))));
+    const int64_t rows = (T + most - 1) / most;  // of the fullest workgroup
+    return static_cast<int>((T + rows - 1) / rows);
 }
 
 hipError_t launch_norm(const NormParams& p, bool work_bf16, hipStream_t s) {
