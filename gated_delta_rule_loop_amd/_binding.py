@@ -330,7 +330,11 @@ def _scratch(floats, like, stream):
 
 def _new(like, shape=None, dtype=None, stream=None):
     """An output allocated here: on the current stream, written on the caller's."""
-    t = like.new_empty(like.shape if shape is None else shape, dtype=dtype or like.dtype)
+    if shape is None and like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = torch.empty(like.shape if shape is None else shape, dtype=dtype or like.dtype,
+                        device=like.device)
     if stream is not None:
         t.record_stream(stream)
     return t

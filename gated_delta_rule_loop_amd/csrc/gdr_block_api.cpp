@@ -423,8 +423,8 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
         ps.max_tiles = w.tiles;
         ps.w[0] = sum;
         e = launch_la_segments(ps, b16, ws + pl.tot, s);
-        if (e == hipSuccess)
-            e = launch_la_scan(la_scan(p, d, ws + pl.s_fwd, ws + pl.tot, false, in), s);
+        const LaScan scan = la_scan(p, d, ws + pl.s_fwd, ws + pl.tot, false, in);
+        if (e == hipSuccess) e = launch_la_scans(&scan, 1, s);
         w.in = sum.last;
     }
     if (e == hipSuccess) e = run_walks(p, &w, 1, b16, s);
@@ -540,12 +540,10 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         ps.w[1].third = wv.third;
         ps.max_tiles = ps.w[0].tiles;
         e = launch_la_segments(ps, b16, tot, s);
-        if (e == hipSuccess)
-            e = launch_la_scan(la_scan(p, d, sf, tot, false,
-                                       la_state(initial_state, d.V, false, 1.0f)), s);
-        if (e == hipSuccess)
-            e = launch_la_scan(la_scan(p, d, sr, tot, true,
-                                       la_state(dfinal_state, d.V, false, 1.0f / sc)), s);
+        const LaScan scans[2] = {
+            la_scan(p, d, sf, tot, false, la_state(initial_state, d.V, false, 1.0f)),
+            la_scan(p, d, sr, tot, true, la_state(dfinal_state, d.V, false, 1.0f / sc))};
+        if (e == hipSuccess) e = launch_la_scans(scans, 2, s);
         wq.in = la_segment_state(sf, d.nv, d.K, d.V, true);
         wv.in = la_segment_state(sr, d.nv, d.K, d.V, false);
         wk.in = la_segment_state(sr, d.nv, d.K, d.V, true);
@@ -597,9 +595,8 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         c.offsets = p.offsets;
         c.rq = ws + pl.rq;
         c.rk = ws + pl.rk;
-        c.rq_parts = c.rk_parts = wq.tiles * la_waves(wq.Vd);
         c.phi = wq.phi;
-        c.phi_parts = wq.tiles * la_waves(wq.Vd);
+        c.parts = wq.tiles * la_waves(wq.Vd);
         c.dg = dg->data;
         c.dg_tok = dg->stride[0];
         c.dg_head = dg->stride[1];

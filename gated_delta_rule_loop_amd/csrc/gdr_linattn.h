@@ -88,9 +88,9 @@ struct LaScan {
 struct LaDecayGrad {
     int32_t B, nv, T, seg_len, segs;
     const uint32_t* offsets;
-    const float* rq; int32_t rq_parts;  // [parts, nv, T]
-    const float* rk; int32_t rk_parts;
-    const float* phi; int32_t phi_parts; // [segs, nv, parts] or nullptr
+    const float *rq, *rk;   // [parts, nv, T]
+    const float* phi;       // [segs, nv, parts] or nullptr
+    int32_t parts;          // a multiple of 4
     void* dg; int64_t dg_tok, dg_head; int32_t dg_bf16;
 };
 
@@ -119,7 +119,7 @@ inline int la_waves(int Vd) { return Vd <= 64 ? 4 : 8; }
 
 hipError_t launch_la_walks(const LaParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_la_segments(const LaParams& p, bool work_bf16, float* tot, hipStream_t s);
-hipError_t launch_la_scan(const LaScan& p, hipStream_t s);
+hipError_t launch_la_scans(const LaScan* c, int count, hipStream_t s);
 hipError_t launch_la_decay_grad(const LaDecayGrad& p, hipStream_t s);
 hipError_t launch_la_head_sum(const LaHeadSum& p, bool work_bf16, hipStream_t s);
 hipError_t launch_la_step(const LaStep& p, bool work_bf16, hipStream_t s);

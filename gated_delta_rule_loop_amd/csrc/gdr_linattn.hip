@@ -136,8 +136,11 @@ hipError_t run_step(const LaStep& p, hipStream_t s) {
 // ------------------------------------------------------------------- scan ---
 
 // A thread carries 4 elements of a (row, head) state over the row's segments:
-// each segment's sum is replaced by the state that its walk starts from.
-__global__ void __launch_bounds__(256) scan_kernel(const LaScan p) {
+// each segment's sum is replaced by the state that its walk starts from.  The
+// sums are loaded a step ahead.  blockIdx.z: the scans of one launch.
+struct LaScans { LaScan c[2]; };
+__global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
+    const LaScan& p = both.c[blockIdx.z];
     const int head = blockIdx.y % p.nv, row = blockIdx.y / p.nv;
     const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
     // the row's first segment
@@ -145,6 +148,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const LaScan p) {
     for (int b = threadIdx.x & 63; b < row; b += 64)
         first += la_row_segs(static_cast<int>(p.offsets[b + 1] - p.offsets[b]), p.seg_len);
     for (int d = 1; d < 64; d <<= 1) first += __shfl_xor(first, d);
+    first = __builtin_amdgcn_readfirstlane(first);
     const int count = la_row_segs(static_cast<int>(p.offsets[row + 1] - p.offsets[row]), p.seg_len);
     if (i >= p.n) return;
     const uint32_t slot = p.slot_idx ? p.slot_idx[row] : static_cast<uint32_t>(row);
@@ -155,20 +159,27 @@ __global__ void __launch_bounds__(256) scan_kernel(const LaScan p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) run[e] = p.in.mult * la_load(p.in.p, base + e, p.in.bf16);
     }
-    const int64_t step = int64_t{p.nv} * p.n;
-    float* s = p.state + (int64_t{first} * p.nv + head) * p.n + i;
-    const float* tot = p.tot + (int64_t{p.reverse} * p.segs + first) * p.nv + head;
+    const int64_t step = (p.reverse ? -1 : 1) * int64_t{p.nv} * p.n;
+    const int from = first + (p.reverse ? count - 1 : 0);
+    float* q = p.state + (int64_t{from} * p.nv + head) * p.n + i;
+    const float* tot = p.tot + (int64_t{p.reverse} * p.segs + from) * p.nv + head;
+    const int tot_step = p.reverse ? -p.nv : p.nv;
+    la_f4 own = {0, 0, 0, 0};
+    float a = 0.0f;
+    auto fetch = [&]() {
+        own = *reinterpret_cast<const la_f4*>(q);
+        a = *tot;
+    };
+    if (count > 1) fetch();
     for (int j = 0; j < count; ++j) {
-        const int at = p.reverse ? count - 1 - j : j;
-        la_f4* q = reinterpret_cast<la_f4*>(s + at * step);
-        if (j + 1 < count) {
-            const la_f4 own = *q;
-            const float a = exp2f(tot[int64_t{at} * p.nv]);
-            *q = run;
-            run = run * a + own;
-        } else {
-            *q = run;
-        }
+        la_f4* const to = reinterpret_cast<la_f4*>(q);
+        const la_f4 sum = own;
+        const float decay = exp2f(a);
+        q += step;
+        tot += tot_step;
+        if (j + 2 < count) fetch();
+        *to = run;
+        run = run * decay + sum;
     }
 }
 
@@ -185,9 +196,12 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const LaDecayGrad p) {
     if (!la_locate(p.offsets, p.B, p.seg_len, seg, sp)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     double carry = 0.0;
-    if (p.phi)
-        for (int i = 0; i < p.phi_parts; ++i)
-            carry += p.phi[(int64_t{seg} * p.nv + head) * p.phi_parts + i];
+    if (p.phi) {
+        const float* f = p.phi + (int64_t{seg} * p.nv + head) * p.parts;
+        for (int i = 0; i < p.parts; i += 4)
+            carry += (static_cast<double>(f[i]) + f[i + 1]) +
+                     (static_cast<double>(f[i + 2]) + f[i + 3]);
+    }
     const int64_t part = int64_t{p.nv} * p.T;
     for (int r0 = 0; r0 < sp.n; r0 += 256) {  // r counts from the segment's end
         const int r = r0 + tid;
@@ -195,8 +209,16 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const LaDecayGrad p) {
         double v = 0.0;
         if (r < sp.n) {
             const int64_t at = int64_t{head} * p.T + t;
-            for (int i = 0; i < p.rq_parts; ++i) v += p.rq[i * part + at];
-            for (int i = 0; i < p.rk_parts; ++i) v -= p.rk[i * part + at];
+            for (int i = 0; i < p.parts; i += 4) {  // a multiple of 4, in flight together
+                float a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    a[e] = p.rq[(i + e) * part + at];
+                    b[e] = p.rk[(i + e) * part + at];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v += static_cast<double>(a[e]) - b[e];
+            }
         }
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -252,9 +274,12 @@ hipError_t launch_la_step(const LaStep& p, bool work_bf16, hipStream_t s) {
     return st16 ? run_step<float, uint16_t>(p, s) : run_step<float, float>(p, s);
 }
 
-hipError_t launch_la_scan(const LaScan& p, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>((p.n / 4 + 255) / 256), static_cast<uint32_t>(p.B * p.nv));
-    scan_kernel<<<grid, 256, 0, s>>>(p);
+hipError_t launch_la_scans(const LaScan* c, int count, hipStream_t s) {
+    LaScans both{};
+    for (int i = 0; i < count; ++i) both.c[i] = c[i];
+    const dim3 grid(static_cast<uint32_t>((c->n / 4 + 255) / 256),
+                    static_cast<uint32_t>(c->B * c->nv), static_cast<uint32_t>(count));
+    scan_kernel<<<grid, 256, 0, s>>>(both);
     return hipGetLastError();
 }
 

@@ -198,11 +198,17 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
     BlockSums block(lds);
     float* per_unit = lds + kRedFloats;   // [units] kAny, [D] to fold a shared weight
     const int units = p.D >> 3, gu = p.group >> 3;
-    float a1[NV][8], a2[NV][8], ag[NV][8];
+    float a1[NV][8], a2[NV][8], ag[NV][8], w1[NV][8], w2[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) a1[i][e] = a2[i][e] = ag[i][e] = 0.0f;
+        if (c < p.D) {
+            if (GM != kNoNorm) load8(p.w1, p.w1_len == p.D ? c : c % p.w1_len, w1[i]);
+            if (p.w2.p) load8(p.w2, c, w2[i]);
+        }
+    }
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         float H[NV][8], yv[NV][8], gv[NV][8], r[NV];
 #pragma unroll
@@ -247,13 +253,11 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
             for (int i = 0; i < NV; ++i) {
                 const int c = (threadIdx.x + i * blockDim.x) * 8;
                 if (c < p.D) {
-                    float w[8];
-                    load8(p.w2, c, w);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         hv[i][e] *= rh;
                         a2[i][e] = fmaf(tv[i][e], hv[i][e], a2[i][e]);
-                        tv[i][e] *= w[e];
+                        tv[i][e] *= w2[i][e];
                         dot[0] = fmaf(tv[i][e], hv[i][e], dot[0]);
                     }
                 }
@@ -289,14 +293,10 @@ __global__ void __launch_bounds__(THREADS, 4) norm_bwd_kernel(const NormParams p
             const int c = (threadIdx.x + i * blockDim.x) * 8;
             dot[i] = 0.0f;
             if (c < p.D) {
-                float w[8];
-                if constexpr (GM != kNoNorm) {
-                    load8(p.w1, p.w1_len == p.D ? c : c % p.w1_len, w);
-                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float hat = GM == kNoNorm ? yv[i][e] : yv[i][e] * r[i];
-                    const float wt = GM == kNoNorm ? 1.0f : w[e];
+                    const float wt = GM == kNoNorm ? 1.0f : w1[i][e];
                     float dp = p.c * H[i][e];
                     if (p.gate_mode) {
                         const float z = gv[i][e];
