@@ -105,6 +105,8 @@ LaState la_segment_state(float* p, int64_t nv, int64_t K, int64_t V, bool flip) 
     return s;
 }
 
+constexpr int64_t kLaUncut = 192;         // tokens of a call up to which no row is cut
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // How a call is cut into segments and what its workspace holds (float32
@@ -120,15 +122,20 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     const int64_t q_waves = la_waves(static_cast<int>(K));
     p.v_tiles = ceil_div(V, 16 * la_waves(static_cast<int>(V)));
     p.q_tiles = ceil_div(K, 16 * q_waves);
-    // Rows are walked token by token, so few (row, head) pairs leave most of
-    // the 256 compute units idle: rows are cut into segments, whose own sums a
-    // first pass takes, until about two workgroups a unit are walking.
+    // Rows are walked chunk by chunk, so few (row, head) pairs leave most of the
+    // 256 compute units idle: rows are cut into segments, whose own sums a first
+    // pass takes and a scan turns into states, until about two workgroups a unit
+    // are walking (64 segments at most: the scan goes through a row's in turn).
+    // Measured at 16 value heads, K = V = 128, us uncut and in segments of 64
+    // tokens: bf16 forward of 200 tokens 24 and 26, of 300 (by 256) 38 and 27,
+    // float32 46 and 35, 82 and 37; the two more launches cost up to 5 us where
+    // they gain nothing.
     const int64_t per_seg = nv * (backward ? p.v_tiles + 2 * p.q_tiles : p.v_tiles);
-    const int64_t want = ceil_div(512, per_seg);
+    const int64_t want = std::min<int64_t>(64, ceil_div(512, per_seg));
     p.segs = B;
-    if (B < want) {
+    if (B < want && T > kLaUncut) {
         const int64_t full = std::max<int64_t>(1, want - B / 2);  // rows end in part segments
-        const int64_t len = std::max<int64_t>(256, ceil_div(ceil_div(T, full), 64) * 64);
+        const int64_t len = std::max<int64_t>(64, ceil_div(ceil_div(T, full), 64) * 64);
         if (len < T) {
             p.seg_len = len;
             p.segs = T / len + B;

@@ -137,7 +137,7 @@ hipError_t run_step(const LaStep& p, hipStream_t s) {
 
 // A thread carries 4 elements of a (row, head) state over the row's segments:
 // each segment's sum is replaced by the state that its walk starts from.  The
-// sums are loaded a step ahead.  blockIdx.z: the scans of one launch.
+// sums are loaded four steps ahead.  blockIdx.z: the scans of one launch.
 struct LaScans { LaScan c[2]; };
 __global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
     const LaScan& p = both.c[blockIdx.z];
@@ -164,22 +164,27 @@ __global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
     float* q = p.state + (int64_t{from} * p.nv + head) * p.n + i;
     const float* tot = p.tot + (int64_t{p.reverse} * p.segs + from) * p.nv + head;
     const int tot_step = p.reverse ? -p.nv : p.nv;
-    la_f4 own = {0, 0, 0, 0};
-    float a = 0.0f;
-    auto fetch = [&]() {
-        own = *reinterpret_cast<const la_f4*>(q);
-        a = *tot;
+    constexpr int AHEAD = 4;
+    la_f4 own[AHEAD];
+    float a[AHEAD];
+    auto fetch = [&](int j, int e) {      // of the last segment nothing is needed
+        const int c = min(j, count - 2);
+        own[e] = *reinterpret_cast<const la_f4*>(q + c * step);
+        a[e] = tot[c * tot_step];
     };
-    if (count > 1) fetch();
-    for (int j = 0; j < count; ++j) {
-        la_f4* const to = reinterpret_cast<la_f4*>(q);
-        const la_f4 sum = own;
-        const float decay = exp2f(a);
-        q += step;
-        tot += tot_step;
-        if (j + 2 < count) fetch();
-        *to = run;
-        run = run * decay + sum;
+    if (count > 1)
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) fetch(e, e);
+    for (int j = 0; j < count; j += AHEAD) {
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            if (j + e >= count) break;
+            *reinterpret_cast<la_f4*>(q + (j + e) * step) = run;
+            if (j + e + 1 < count) {
+                run = run * exp2f(a[e]) + own[e];
+                if (j + e + AHEAD < count - 1) fetch(j + e + AHEAD, e);
+            }
+        }
     }
 }
 
