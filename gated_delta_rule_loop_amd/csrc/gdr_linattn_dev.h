@@ -51,6 +51,15 @@ __device__ __forceinline__ double la_lane(double v, int lane) {
     return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
 
+// Sum over the four lanes that share lane % 16.
+__device__ __forceinline__ float la_sum_rows(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t s = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(s, s, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // Segments of a row of n tokens (one at least: it carries the row's state).
 __device__ __forceinline__ int la_row_segs(int n, int seg_len) {
     return n <= seg_len ? 1 : (n + seg_len - 1) / seg_len;

@@ -449,13 +449,29 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         stage(c0);
         __syncthreads();
         const bool more = c0 + C < n;
-        // (with the decays' sums, after P: the loads' registers do not fit before)
-        if (!SUMS && more) fetch(c0 + C);
         const int ln = fresh(lane);
         const int g4 = (ln >> 4) * 4, i16 = ln & 15;
         const int row_x = M::x_place(ln, XS), col_y = M::col_place(ln, XS);
         // a wave's own columns start at a multiple of 16 within a tile's rows
         const int col_z = M::step(M::col_place(ln, ZS), wave);
+        // the partner's values at this wave's outputs, before the next chunk's
+        // loads: what is loaded in order is waited for in order
+        Fr partner[SUMS ? IT : 1];
+        if (sums) {
+            const int64_t from = lead(c0, C);
+            const char* const qp = static_cast<const char*>(w.partner.p) +
+                                   (head / w.partner.div * w.partner.head +
+                                    from * w.partner.tok) * ES;
+            const uint32_t q_tok = static_cast<uint32_t>(w.partner.tok / 4);
+            const uint32_t z = static_cast<uint32_t>(min(zbase + g4, Vd - 4)) / 4;
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+                const int r = min(it * 16 + i16, n - 1 - c0);
+                const uint32_t at = __umul24(reverse ? C - 1 - r : r, q_tok) + z;
+                partner[it] = *reinterpret_cast<const Fr*>(qp + at * static_cast<uint32_t>(4 * ES));
+            }
+        }
+        if (more) fetch(c0 + C);
         la_f4 O[SEG ? 1 : IT];
         if constexpr (!SEG) {
             // scale exp(G_i) (S^T X^T): rows are columns of the state, columns tokens
@@ -525,10 +541,9 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 for (int u = 0; u < N; ++u)
                     *reinterpret_cast<Fr*>(&Ps[(u * C + i) * PS + jt * 16 + g4]) = pf[u];
             }
-            if (!SUMS && more && wave == W - 1) decays(c0 + C, b ^ 1);
+            if (more && wave == W - 1) decays(c0 + C, b ^ 1);
             __syncthreads();
             if (SUMS) __builtin_amdgcn_sched_barrier(0);
-            if (SUMS && more) fetch(c0 + C);
         }
         // Z by columns: operand of P Z as it is, of the state's sum with its decay
         Fr zf[IT];
@@ -547,32 +562,19 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                         O[it] = M::mma(zf[jt], zf[jt + 1], p0, p1, O[it]);
                     }
             if (sums) {
-                __builtin_amdgcn_sched_barrier(0);
                 // partner . out without the token's own pair, then that pair
-                const int64_t from = lead(c0, C);
-                const char* const qp = static_cast<const char*>(w.partner.p) +
-                                       (head / w.partner.div * w.partner.head +
-                                        from * w.partner.tok) * ES;
                 const int row_z = M::step(M::at(0, i16, g4, ZS), wave);
-                const uint32_t q_tok = static_cast<uint32_t>(w.partner.tok / 4);
                 float* const rs = w.row_sum + (int64_t{tile} * W + wave) * p.nv * p.T +
-                                  int64_t{head} * p.T + from;
-                const int z = zbase + g4;
+                                  int64_t{head} * p.T + lead(c0, C);
+                const bool has = zbase + g4 < Vd;
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
-                    __builtin_amdgcn_sched_barrier(0);  // one tile's operands at a time
                     const int i = it * 16 + i16;
-                    const int r0 = min(i, n - 1 - c0);
-                    const uint32_t at = __umul24(reverse ? C - 1 - r0 : r0, q_tok) +
-                                        static_cast<uint32_t>(min(z, Vd - 4)) / 4;
-                    const la_f4 a = M::widen(*reinterpret_cast<const Fr*>(
-                        qp + at * static_cast<uint32_t>(4 * ES)));
+                    const la_f4 a = M::widen(partner[it]);
                     float sum = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) sum = fmaf(a[r], O[it][r], sum);
-                    sum = z < Vd ? sum : 0.0f;
-                    sum += __shfl_xor(sum, 16);
-                    sum += __shfl_xor(sum, 32);
+                    sum = la_sum_rows(has ? sum : 0.0f);
                     if (ln < 16 && c0 + i < n) rs[reverse ? C - 1 - i : i] = sum;
                     const float d = own[i];
                     const la_f4 zz = M::widen(M::row(&Zs[it * 16 * ZS + row_z]));
@@ -580,7 +582,6 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                     for (int r = 0; r < 4; ++r) O[it][r] = fmaf(d, zz[r], O[it][r]);
                 }
             }
-            if (SUMS) __builtin_amdgcn_sched_barrier(0);
             auto put = [&](auto narrow) {
                 typedef decltype(narrow(O[0])) Vec;
                 constexpr int OES = sizeof(Vec) / 4;
@@ -597,8 +598,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             if (out_f32) put([](la_f4 v) { return v; });
             else put([](la_f4 v) { return M::narrow(v); });
         }
-        if ((SEG || SUMS) && more && wave == W - 1) decays(c0 + C, b ^ 1);
-        if (SUMS) __builtin_amdgcn_sched_barrier(0);
+        if (SEG && more && wave == W - 1) decays(c0 + C, b ^ 1);
         // ---- S <- exp(G_C) S + Y^T (decayed Z)
         if constexpr (!SEG) {
             const float all = g_all[b];
@@ -732,7 +732,9 @@ hipError_t dispatch(const LaParams& p, float* tot, hipStream_t s) {
         return run<256, 4, 32, MODE>(p, tot, s);
     }
     if (Kd <= 64) return run<64, 8, C, MODE>(p, tot, s);
-    if (Kd <= 128) return run<128, 8, C, MODE>(p, tot, s);
+    // with the decays' sums a chunk of 64 does not fit the registers of four waves
+    // a SIMD (gradient of 8192 tokens, 32 heads, K = V = 128: 502 us, 484 by 32)
+    if (Kd <= 128) return run<128, 8, MODE == kWalkSums ? 32 : C, MODE>(p, tot, s);
     return run<256, 8, 32, MODE>(p, tot, s);
 }
 

@@ -761,3 +761,18 @@ def test_norm_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(want, every))
+
+
+@pytest.mark.gpu
+def test_example_runs_the_operators_together():
+    """examples/linear_attention_block.py: prompt, single tokens and a training
+    step.  Two float32 layers whose rows are cut differently: differences of a
+    few hundred roundings, 100 u(float32) (K + 64) at most."""
+    import importlib.util
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "linear_attention_block.py")
+    spec = importlib.util.spec_from_file_location("linear_attention_block", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, finite = mod.main(["--prompt", "150", "--tokens", "3"])
+    assert worst <= 100 * U32 * (64 + 64) and finite
