@@ -714,8 +714,8 @@ int check_norm(const char* fn, const gdr_tensor* y, const gdr_tensor* gate,
             p.gate = gate->data;
             p.gate_row = gate->stride[0];
         }
-    } else if (p.act) {
-        return fail(GDR_ERR_INVALID_ARG, "%s: an activation needs gate", fn);
+    } else {
+        p.act = 0;  // an activation of nothing
     }
     if (present(pre_weight)) {
         if ((rc = check_vec(fn, "pre_weight", pre_weight, D, work))) return rc;

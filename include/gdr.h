@@ -386,7 +386,8 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
  *   pre_weight        [D] f32 or work, or absent
  *   h                 [T, D] work (out); may be residual or y themselves
  *   n                 [T, D] work (out), given exactly when pre_weight is
- *   flags             GDR_FLAG_GATE_SIGMOID or GDR_FLAG_GATE_SILU, or 0
+ *   flags             GDR_FLAG_GATE_SIGMOID or GDR_FLAG_GATE_SILU, or 0; they
+ *                     say nothing without gate
  */
 int gdr_block_norm(const gdr_tensor* h, const gdr_tensor* n, const gdr_tensor* y,
                    const gdr_tensor* residual, const gdr_tensor* gate,

@@ -202,7 +202,7 @@ def _norm_args(over):
     (dict(w1=None), -1, "groups need post_weight"),
     (dict(w1=D([32])), -1, "post_weight dim 0"),
     (dict(w1=D([16], BF16)), -2, "post_weight must be"),
-    (dict(gate=None), -1, "needs gate"),
+    (dict(gate=D([4, 64])), -1, "gate dim 0"),
     (dict(gate=D([32])), -1, "gate dim 0"),
     (dict(flags=12), -1, "one activation"),
     (dict(flags=16), -1, "unknown flags"),
@@ -728,6 +728,20 @@ def test_norm_backward(case):
         sums = T + D // 8 if v.dim() == 1 else 0
         close(name, v, want[name], want["a" + name], f + sums * U32)
         assert torch.equal(v, v2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_an_activation_without_a_gate_says_nothing(act):
+    y, x, a, n = norm_inputs(NORM[8])
+    h, m = gdr.gdr_block_norm(y, residual=x, **a)
+    h2, m2 = gdr.gdr_block_norm(y, residual=x, **{**a, "activation": act})
+    assert torch.equal(h, h2) and torch.equal(m, m2)
+    dh, dn = n(*y.shape).to(y.dtype).cuda(), n(*y.shape).to(y.dtype).cuda()
+    got = gdr.gdr_block_norm_bwd(dh, dn, y, h, **a)
+    again = gdr.gdr_block_norm_bwd(dh, dn, y, h, **{**a, "activation": act})
+    for p, q in zip(got, again):
+        assert (p is None and q is None) or torch.equal(p, q)
 
 
 @pytest.mark.gpu
