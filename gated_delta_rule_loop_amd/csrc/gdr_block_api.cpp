@@ -106,6 +106,7 @@ LaState la_segment_state(float* p, int64_t nv, int64_t K, int64_t V, bool flip) 
 }
 
 constexpr int64_t kLaUncut = 192;         // tokens of a call up to which no row is cut
+constexpr int64_t kLaSumTokens = 512;     // longest segment of a gradient
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -114,7 +115,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct LaPlan {
     int64_t seg_len, segs;
     int64_t q_tiles, v_tiles;             // workgroups over K (dq, dk) and over V (fwd, dv)
-    int64_t s_fwd, s_rev, tot, rq, rk, phi, pq, pk, end;
+    int64_t s_fwd, s_rev, tot, rq, rk, phi, phi0, pq, pk, end;
 };
 
 LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t V, bool backward) {
@@ -133,13 +134,16 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     const int64_t per_seg = nv * (backward ? p.v_tiles + 2 * p.q_tiles : p.v_tiles);
     const int64_t want = std::min<int64_t>(64, ceil_div(512, per_seg));
     p.segs = B;
+    int64_t len = T;
     if (B < want && T > kLaUncut) {
         const int64_t full = std::max<int64_t>(1, want - B / 2);  // rows end in part segments
-        const int64_t len = std::max<int64_t>(64, ceil_div(ceil_div(T, full), 64) * 64);
-        if (len < T) {
-            p.seg_len = len;
-            p.segs = T / len + B;
-        }
+        len = std::max<int64_t>(64, ceil_div(ceil_div(T, full), 64) * 64);
+    }
+    // the decays' gradient is summed over a segment, with errors as its root
+    if (backward) len = std::min(len, kLaSumTokens);
+    if (len < T) {
+        p.seg_len = len;
+        p.segs = T / len + B;
     }
     int64_t at = 0;
     auto take = [&](int64_t n) {
@@ -156,6 +160,7 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
         p.rq = take(p.q_tiles * q_waves * nv * T);
         p.rk = take(p.q_tiles * q_waves * nv * T);
         p.phi = take(p.segs * nv * p.q_tiles * q_waves);
+        p.phi0 = take(p.segs * nv * p.v_tiles * la_waves(static_cast<int>(V)));
         if (nv != nk) {
             p.pq = take(T * nv * K);
             p.pk = take(T * nv * K);
@@ -581,6 +586,11 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
             wq.phi = ws + pl.phi;
             wq.phi_in = wk.in;
         }
+        if (present(initial_state)) {     // and into their starts
+            wv.phi = ws + pl.phi0;
+            wv.phi_in = la_state(initial_state, d.V, false, 1.0f);
+            wv.phi_rows = 1;
+        }
     }
     const LaWalk all[3] = {wq, wv, wk};
     if (e == hipSuccess) {
@@ -604,6 +614,8 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         c.rk = ws + pl.rk;
         c.phi = wq.phi;
         c.parts = wq.tiles * la_waves(wq.Vd);
+        c.phi0 = wv.phi;
+        c.parts0 = wv.tiles * la_waves(wv.Vd);
         c.dg = dg->data;
         c.dg_tok = dg->stride[0];
         c.dg_head = dg->stride[1];

@@ -53,6 +53,7 @@ struct LaWalk {
     float* row_sum;
     float* phi;
     LaState phi_in;
+    int32_t phi_rows;       // phi only where the walk leaves its row
 };
 
 constexpr int kLaMaxWalks = 3;
@@ -89,8 +90,9 @@ struct LaDecayGrad {
     int32_t B, nv, T, seg_len, segs;
     const uint32_t* offsets;
     const float *rq, *rk;   // [parts, nv, T]
-    const float* phi;       // [segs, nv, parts] or nullptr
-    int32_t parts;          // a multiple of 4
+    const float* phi;       // [segs, nv, parts] at the segments' ends, or nullptr (zeros)
+    const float* phi0;      // [segs, nv, parts0] where rows start, or nullptr (zeros)
+    int32_t parts, parts0;  // multiples of 4
     void* dg; int64_t dg_tok, dg_head; int32_t dg_bf16;
 };
 

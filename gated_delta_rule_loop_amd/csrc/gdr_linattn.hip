@@ -190,41 +190,64 @@ __global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
 
 // ---------------------------------------------------------- decay gradient ---
 
-// dg_j = sum_{i >= j} (q_i . dq_i - k_i . dk_i) + <S, dL/dS> at the segment's
-// end, the tokens' own pairs left out of both products.  One workgroup per
-// (segment, head) sums from the segment's end, 256 tokens at a time, in
-// float64: the terms telescope, so what is left is a small difference.
+// dg_j = sum_{i >= j} (q_i . dq_i - k_i . dk_i) + phi(end), the tokens' own pairs
+// left out of both products, phi = <S, dL/dS> at a segment's end.  One workgroup
+// per (segment, head) sums from the segment's end, 256 tokens at a time, in
+// float64: the terms telescope, so what is left is a small difference of sums
+// whose rounding errors add up like a random walk.  The sum over the whole
+// segment has to be phi(start) - phi(end), both known; what it misses is taken
+// back from every dg_j in proportion to the terms it holds, which leaves 0.6 of
+// the error (float32, 256 tokens: 8.9e-7 of the gradient without).
+__device__ __forceinline__ double phi_at(const float* phi, int64_t i, int parts) {
+    const float* f = phi + i * parts;
+    double sum = 0.0;
+    for (int k = 0; k < parts; k += 4)
+        sum += (static_cast<double>(f[k]) + f[k + 1]) + (static_cast<double>(f[k + 2]) + f[k + 3]);
+    return sum;
+}
+
 __global__ void __launch_bounds__(256) decay_grad_kernel(const LaDecayGrad p) {
     __shared__ double wsum[4];
     const int head = blockIdx.x % p.nv, seg = blockIdx.x / p.nv;
     LaSpan sp;
     if (!la_locate(p.offsets, p.B, p.seg_len, seg, sp)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    double carry = 0.0;
-    if (p.phi) {
-        const float* f = p.phi + (int64_t{seg} * p.nv + head) * p.parts;
-        for (int i = 0; i < p.parts; i += 4)
-            carry += (static_cast<double>(f[i]) + f[i + 1]) +
-                     (static_cast<double>(f[i + 2]) + f[i + 3]);
-    }
-    const int64_t part = int64_t{p.nv} * p.T;
-    for (int r0 = 0; r0 < sp.n; r0 += 256) {  // r counts from the segment's end
-        const int r = r0 + tid;
-        const int64_t t = int64_t{sp.t0} + sp.n - 1 - r;
+    const int64_t at = int64_t{seg} * p.nv + head, part = int64_t{p.nv} * p.T;
+    const double end = p.phi ? phi_at(p.phi, at, p.parts) : 0.0;
+    double begin = 0.0;
+    if (sp.s > 0) begin = phi_at(p.phi, at - p.nv, p.parts);
+    else if (p.phi0) begin = phi_at(p.phi0, at, p.parts0);
+    // the term of the r-th token from the segment's end
+    auto term = [&](int r) {
         double v = 0.0;
         if (r < sp.n) {
-            const int64_t at = int64_t{head} * p.T + t;
-            for (int i = 0; i < p.parts; i += 4) {  // a multiple of 4, in flight together
+            const int64_t i = int64_t{head} * p.T + sp.t0 + sp.n - 1 - r;
+            for (int k = 0; k < p.parts; k += 4) {  // in flight together
                 float a[4], b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    a[e] = p.rq[(i + e) * part + at];
-                    b[e] = p.rk[(i + e) * part + at];
+                    a[e] = p.rq[(k + e) * part + i];
+                    b[e] = p.rk[(k + e) * part + i];
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v += static_cast<double>(a[e]) - b[e];
             }
         }
+        return v;
+    };
+    double first = term(tid), all = first;
+    for (int r = 256 + tid; r < sp.n; r += 256) all += term(r);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d);
+    if (lane == 0) wsum[wave] = all;
+    __syncthreads();
+    all = (wsum[0] + wsum[1]) + (wsum[2] + wsum[3]);
+    __syncthreads();
+    const double missed = sp.n > 0 ? (begin - end - all) / sp.n : 0.0;  // by each term
+    double carry = end;
+    for (int r0 = 0; r0 < sp.n; r0 += 256) {  // r counts from the segment's end
+        const int r = r0 + tid;
+        double v = r0 ? term(r) : first;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
             const double up = __shfl_up(v, d);
@@ -232,15 +255,14 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const LaDecayGrad p) {
         }
         if (lane == 63) wsum[wave] = v;
         __syncthreads();
-        double before = carry, all = 0.0;
+        double before = carry;
         for (int i = 0; i < 4; ++i) {
             if (i < wave) before += wsum[i];
-            all += wsum[i];
+            carry += wsum[i];
         }
         if (r < sp.n)
-            la_store(p.dg, t * p.dg_tok + head * p.dg_head, p.dg_bf16,
-                     static_cast<float>(before + v));
-        carry += all;
+            la_store(p.dg, (int64_t{sp.t0} + sp.n - 1 - r) * p.dg_tok + head * p.dg_head, p.dg_bf16,
+                     static_cast<float>(before + v + missed * (r + 1)));
         __syncthreads();
     }
 }

@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
             tot[(int64_t{w.reverse} * p.segs + seg) * p.nv + head] = static_cast<float>(walked);
         return;
     }
-    if (SUMS && w.phi) {
+    if (SUMS && w.phi && (!w.phi_rows || at_last)) {
         float sum = 0.0f;
         if (w.phi_in.p) {
             la_f4 back[KT];
@@ -742,7 +742,7 @@ hipError_t dispatch(const LaParams& p, float* tot, hipStream_t s) {
 
 hipError_t GDR_LA_WALK(const LaParams& p, hipStream_t s) {
     bool sums = false;
-    for (int i = 0; i < p.nwalks; ++i) sums = sums || p.w[i].row_sum != nullptr;
+    for (int i = 0; i < p.nwalks; ++i) sums = sums || p.w[i].row_sum || p.w[i].phi;
     return sums ? dispatch<kWalkSums>(p, nullptr, s) : dispatch<kWalk>(p, nullptr, s);
 }
 hipError_t GDR_LA_SEG(const LaParams& p, float* tot, hipStream_t s) {
