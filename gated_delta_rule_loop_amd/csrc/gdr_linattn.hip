@@ -42,6 +42,27 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// A state is read and written once a call: its lines are streamed past the
+// caches (16 bytes a lane, whole lines a wave).
+template <typename E> __device__ __forceinline__ void stream_in(const E* p, float (&v)[8]) {
+    constexpr int N = sizeof(E) / 2;
+    __attribute__((aligned(16))) E raw[8];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        reinterpret_cast<la_u4*>(raw)[i] =
+            __builtin_nontemporal_load(reinterpret_cast<const la_u4*>(p) + i);
+    load8(raw, v);
+}
+template <typename E> __device__ __forceinline__ void stream_out(E* p, const float (&v)[8]) {
+    constexpr int N = sizeof(E) / 2;
+    __attribute__((aligned(16))) E raw[8];
+    store8(raw, v);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        __builtin_nontemporal_store(reinterpret_cast<const la_u4*>(raw)[i],
+                                    reinterpret_cast<la_u4*>(p) + i);
+}
+
 template <typename T, typename ST, int THREADS>
 __global__ void __launch_bounds__(THREADS) step_kernel(const LaStep p) {
     extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -75,7 +96,7 @@ __global__ void __launch_bounds__(THREADS) step_kernel(const LaStep p) {
         const ST* s = static_cast<const ST*>(p.in.p) + int64_t{slot} * p.in.outer +
                       head * p.in.head + rg * p.V + cg * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load8(s + i * K8 * p.V, S[i]);
+        for (int i = 0; i < 8; ++i) stream_in(s + i * K8 * p.V, S[i]);
     }
     const T* q = static_cast<const T*>(p.q) + (head / p.G) * p.q_head;
     const T* k = static_cast<const T*>(p.k) + (head / p.G) * p.k_head;
@@ -117,7 +138,7 @@ __global__ void __launch_bounds__(THREADS) step_kernel(const LaStep p) {
         ST* s = static_cast<ST*>(p.last.p) + int64_t{slot} * p.last.outer + head * p.last.head +
                 rg * p.V + cg * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) store8(s + i * K8 * p.V, S[i]);
+        for (int i = 0; i < 8; ++i) stream_out(s + i * K8 * p.V, S[i]);
     }
 }
 
