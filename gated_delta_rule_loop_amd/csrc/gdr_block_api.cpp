@@ -292,6 +292,7 @@ LaScan la_scan(const LaParams& p, const LaDims& d, float* state, const float* to
     c.nv = p.nv;
     c.T = p.T;
     c.seg_len = p.seg_len;
+    c.walk_from = p.walk_from;
     c.segs = p.segs;
     c.offsets = p.offsets;
     c.slot_idx = p.slot_idx;
@@ -323,6 +324,7 @@ hipError_t run_step(const LaDims& d, const gdr_tensor* o, const gdr_tensor* q, c
     p.out = o->data; p.o_tok = o->stride[0]; p.o_head = o->stride[1];
     p.in = in;
     p.last = last;
+    p.most = kLaStepTokens;
     p.scale = scale;
     return launch_la_step(p, d.work == GDR_DTYPE_BF16, s);
 }
@@ -400,10 +402,9 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
     const LaState in = la_state(pool ? state : initial_state, d.V, false, 1.0f);
     const LaState last = la_state(pool ? state : final_state, d.V, false, 1.0f);
     if ((rc = check_grid(fn, d.B * d.nv))) return rc;
-    const bool few = d.T <= kLaStepTokens * d.B;
     const LaPlan pl = la_plan(d.T, d.B, d.nk, d.nv, d.K, d.V, false);
-    if (!few && ((rc = check_workspace(fn, workspace, pl.end)) ||
-                 (rc = check_grid(fn, pl.segs * d.nv * pl.v_tiles))))
+    if ((rc = check_workspace(fn, workspace, pl.end)) ||
+        (rc = check_grid(fn, pl.segs * d.nv * pl.v_tiles)))
         return rc;
     IndexCheck ic;
     ic.offsets = input_row_offsets;
@@ -413,11 +414,17 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
         ic.num_slots = state->shape[0];
     }
     if ((rc = run_debug_check(fn, d.B, ic, stream))) return rc;
-    if (few)
-        return hip_status(fn, run_step(d, o, q, k, v, g, input_row_offsets, slot_idx, in, last, sc,
-                                       s));
     const int64_t G = d.nv / d.nk;
     LaParams p = la_params(d, pl, input_row_offsets, slot_idx, g, sc);
+    hipError_t e = hipSuccess;
+    if (d.B >= kLaStepRows) {
+        e = run_step(d, o, q, k, v, g, input_row_offsets, slot_idx, in, last, sc, s);
+        const int64_t rows = std::min(d.B, d.T / (kLaStepTokens + 1));  // that are longer
+        if (e != hipSuccess || rows == 0) return hip_status(fn, e);
+        p.walk_from = kLaStepTokens + 1;
+        p.segs = static_cast<int32_t>(rows + (pl.seg_len ? d.T / pl.seg_len : 0));
+        if (!pl.seg_len) p.seg_len = p.T;
+    }
     LaWalk w = la_walk(la_tensor(q, G), la_tensor(k, G), la_tensor(v, 1), d.K, d.V, false);
     w.out = o->data;
     w.out_tok = d.T > 1 ? o->stride[0] : 0;
@@ -425,8 +432,7 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
     w.in = in;
     w.last = last;
     w.third = last.p && !last.bf16;
-    hipError_t e = hipSuccess;
-    if (pl.seg_len) {
+    if (pl.seg_len && e == hipSuccess) {
         float* ws = static_cast<float*>(workspace->data);
         LaWalk sum = w;
         sum.last = la_segment_state(ws + pl.s_fwd, d.nv, d.K, d.V, false);

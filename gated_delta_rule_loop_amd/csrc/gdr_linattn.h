@@ -57,11 +57,21 @@ struct LaWalk {
 };
 
 constexpr int kLaMaxWalks = 3;
-constexpr int kLaStepTokens = 4;  // tokens a row, on average, up to which rows go token by token
+// Where a call has many rows, those of a few tokens go token by token and only the
+// others are walked, each row by its own length (a batch of single tokens and a
+// prompt is common).  A short row is mostly its state, which the token-by-token
+// form streams in whole lines; the walk's layout reads it in pieces.  Measured at
+// 32 value heads, K = V = 128, us token by token and walked: 64 rows of 1, 8 and 16
+// tokens bf16 29 and 57, 57 and 60, 89 and 55, float32 54 and 89, 91 and 91, 117 and
+// 95; 256 rows of 8 bf16 196 and 268; 4 rows of 1 token 14.4 and 15.7.  A prompt of
+// 190 tokens beside 63 single ones: 57 us, 332 where the call went token by token,
+// 59 where it was walked; one of 512 beside 255: 158, 968 and 272.
+constexpr int kLaStepTokens = 8, kLaStepRows = 16;
 
 struct LaParams {
     int32_t B, nv, T;
     int32_t seg_len;        // tokens per segment; 0: one segment per row
+    int32_t walk_from;      // rows of fewer tokens are not walked (then seg_len > 0)
     int32_t segs;           // segments launched (rows, or their upper bound)
     int32_t nwalks, max_tiles;
     const uint32_t* offsets;
@@ -75,7 +85,7 @@ struct LaParams {
 
 // Segment sums -> the state that each segment's walk starts from, in place.
 struct LaScan {
-    int32_t B, nv, T, seg_len, segs;
+    int32_t B, nv, T, seg_len, walk_from, segs;
     const uint32_t* offsets;
     const uint32_t* slot_idx;
     int32_t n;              // elements per state
@@ -114,6 +124,7 @@ struct LaStep {
     void* out; int64_t o_tok, o_head;
     LaState in, last;
     float scale;
+    int32_t most;              // with offsets: rows of more tokens are left out
 };
 
 // Waves of a walk's workgroup, of 16 columns of the state each.

@@ -60,9 +60,10 @@ __device__ __forceinline__ float la_sum_rows(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// Segments of a row of n tokens (one at least: it carries the row's state).
-__device__ __forceinline__ int la_row_segs(int n, int seg_len) {
-    return n <= seg_len ? 1 : (n + seg_len - 1) / seg_len;
+// Segments of a row of n tokens (one at least: it carries the row's state); none
+// of a row below `from` tokens, which is not walked.
+__device__ __forceinline__ int la_row_segs(int n, int seg_len, int from) {
+    return n < from ? 0 : n <= seg_len ? 1 : (n + seg_len - 1) / seg_len;
 }
 
 struct LaSpan {
@@ -73,8 +74,8 @@ struct LaSpan {
 
 // Which tokens segment `seg` spans; false past the last one.  Each wave scans
 // the rows' segment counts, 64 rows at a time.
-__device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_len, int seg,
-                                          LaSpan& o) {
+__device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_len, int from,
+                                          int seg, LaSpan& o) {
     if (seg_len == 0) {
         if (seg >= B) return false;
         o.row = seg;
@@ -93,7 +94,7 @@ __device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_le
         if (b < B) {
             a = static_cast<int>(off[b]);
             n = static_cast<int>(off[b + 1]) - a;
-            c = la_row_segs(n, seg_len);
+            c = la_row_segs(n, seg_len, from);
         }
         int sum = c;
         for (int d = 1; d < 64; d <<= 1) {

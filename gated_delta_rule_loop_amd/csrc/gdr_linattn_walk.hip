@@ -28,6 +28,14 @@
 // the bf16 output itself, and useless decay gradients.  float32 work uses the float32 matrix
 // instructions throughout.  Decay exponents are summed in float64 and kept as
 // a pair of float32.
+//
+// Measured, 32 value heads, K = V = 128.  bf16, 32768 tokens in 16 segments: 375 us
+// (317 with one term everywhere), 260 of them the walk (544 MB: q, k, v once a
+// value head's share through the caches, the outputs), 110 the segments' sums.  Of the
+// walk's cycles the VALU issues in 53%, the LDS is busy in 49% and the matrix
+// instructions in 30%, at 16 waves a compute unit.  float32, 8336 tokens: 277 us, the
+// matrix instructions at half their rate.  Eight waves of 16 columns instead of
+// four of 32: 408 against 424 us, for twice the waves a SIMD.
 #include <type_traits>
 
 #include "gdr_linattn_dev.h"
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     const LaWalk& w = p.w[wi];
     if (tile >= w.tiles) return;
     LaSpan sp;
-    if (!la_locate(p.offsets, p.B, p.seg_len, seg, sp)) return;
+    if (!la_locate(p.offsets, p.B, p.seg_len, p.walk_from, seg, sp)) return;
     auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     sp = LaSpan{uniform(sp.row), uniform(sp.s), uniform(sp.count), uniform(sp.t0), uniform(sp.n),
                 uniform(sp.first)};

@@ -379,6 +379,40 @@ def test_forward(case, packed):
             assert torch.equal(pool[s], before[s])
 
 
+# Sixteen rows and more: those of up to eight tokens and the longer ones take
+# different ways, whatever stands beside them.
+MANY = [
+    ([1] * 15 + [40] + [8, 9, 0, 1], 1, 2, 64, 64, "bf16", "bf16", "token"),
+    ([1] * 16 + [700] + [3] * 4 + [150, 0, 7, 10], 1, 2, 64, 96, "f32", "f32", "token"),
+    ([2] * 18 + [600, 64, 65, 1], 2, 2, 128, 128, "bf16", "f32", "head"),
+    ([1] * 17, 2, 6, 64, 40, "f32", "bf16", "token"),
+    ([20] * 16, 1, 1, 128, 128, "bf16", "bf16", "none"),
+    ([0] * 20, 1, 2, 8, 16, "f32", "f32", "token"),
+    ([0] * 70 + [300] + [1] * 70 + [9, 8], 1, 3, 16, 24, "bf16", "bf16", "token"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "%d-rows-%s" % (len(c[0]), c[1:]))
+def test_forward_of_many_rows(case):
+    test_forward(case, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("initial", [True, False])
+def test_dense_states_of_many_rows(initial):
+    lens = [1] * 14 + [33, 0, 8, 9, 700, 0, 2]
+    q, k, v, g, off, offs, gen = inputs(lens, 1, 2, 64, 64, torch.float32, seed=15)
+    s0 = (0.3 * torch.randn((len(lens), 2, 64, 64), generator=gen)).cuda()
+    start = s0 if initial else torch.zeros_like(s0)
+    pool = start.clone()
+    o1, end = gdr.gdr_linear_attention_fwd(q, k, v, g, offs, initial_state=s0 if initial else None,
+                                           output_final_state=True)
+    o2, _ = gdr.gdr_linear_attention_fwd(q, k, v, g, offs, state=pool)
+    assert torch.equal(o1, o2) and torch.equal(end, pool)
+    assert torch.equal(end[15], start[15]) and torch.equal(end[19], start[19])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("work", ["bf16", "f32"])
 def test_forward_dense_states_equal_the_pool(work):
