@@ -105,7 +105,8 @@ LaState la_segment_state(float* p, int64_t nv, int64_t K, int64_t V, bool flip) 
     return s;
 }
 
-constexpr int64_t kLaUncut = 192;         // tokens of a call up to which no row is cut
+constexpr int64_t kLaUncut = 192;         // tokens of a call up to which no row is cut,
+constexpr int64_t kLaUncutMany = 1024;    // and of a forward with rows enough to fill the chip
 constexpr int64_t kLaSumTokens = 512;     // longest segment of a gradient
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -114,6 +115,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // elements; every part starts at a multiple of 64).
 struct LaPlan {
     int64_t seg_len, segs;
+    int64_t cuts, cut_rows;               // segments that have states of their own; their rows
     int64_t q_tiles, v_tiles;             // workgroups over K (dq, dk) and over V (fwd, dv)
     int64_t s_fwd, s_rev, tot, rq, rk, phi, phi0, pq, pk, end;
 };
@@ -135,8 +137,10 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     const int64_t want = std::min<int64_t>(64, ceil_div(512, per_seg));
     p.segs = B;
     int64_t len = T;
-    if (B < want && T > kLaUncut) {
-        const int64_t full = std::max<int64_t>(1, want - B / 2);  // rows end in part segments
+    // With rows enough only those are cut that are longer than twice their share.
+    if (B < want ? T > kLaUncut : !backward && T > kLaUncutMany) {
+        // rows end in part segments
+        const int64_t full = std::max<int64_t>(1, want - std::min(B, want) / 2);
         len = std::max<int64_t>(64, ceil_div(ceil_div(T, full), 64) * 64);
     }
     // the decays' gradient is summed over a segment, with errors as its root
@@ -144,6 +148,8 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     if (len < T) {
         p.seg_len = len;
         p.segs = T / len + B;
+        p.cut_rows = backward ? B : std::min(B, T / (len + 1));
+        p.cuts = backward ? p.segs : T / len + p.cut_rows;
     }
     int64_t at = 0;
     auto take = [&](int64_t n) {
@@ -152,9 +158,9 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
         return here;
     };
     if (p.seg_len) {
-        p.s_fwd = take(p.segs * nv * K * V);
-        if (backward) p.s_rev = take(p.segs * nv * K * V);
-        p.tot = take(2 * p.segs * nv);
+        p.s_fwd = take(p.cuts * nv * K * V);
+        if (backward) p.s_rev = take(p.cuts * nv * K * V);
+        p.tot = take(2 * p.cuts * nv);
     }
     if (backward) {
         p.rq = take(p.q_tiles * q_waves * nv * T);
@@ -285,10 +291,11 @@ hipError_t run_walks(LaParams p, const LaWalk* w, int n, bool b16, hipStream_t s
 // Walks of one class run the same kernel.
 int size_class(int Kd, int Vd) { return (Kd <= 64 ? 0 : Kd <= 128 ? 1 : 2) * 16 + la_waves(Vd); }
 
-LaScan la_scan(const LaParams& p, const LaDims& d, float* state, const float* tot, bool reverse,
-               const LaState& in) {
+LaScan la_scan(const LaParams& p, const LaDims& d, int64_t rows, float* state, const float* tot,
+               bool reverse, const LaState& in) {
     LaScan c{};
     c.B = p.B;
+    c.rows = static_cast<int32_t>(rows);
     c.nv = p.nv;
     c.T = p.T;
     c.seg_len = p.seg_len;
@@ -436,14 +443,18 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
         float* ws = static_cast<float*>(workspace->data);
         LaWalk sum = w;
         sum.last = la_segment_state(ws + pl.s_fwd, d.nv, d.K, d.V, false);
-        LaParams ps = p;
+        LaParams ps = p;                  // of the rows that are cut
+        ps.walk_from = static_cast<int32_t>(pl.seg_len) + 1;
+        ps.segs = static_cast<int32_t>(pl.cuts);
         ps.nwalks = 1;
         ps.max_tiles = w.tiles;
         ps.w[0] = sum;
         e = launch_la_segments(ps, b16, ws + pl.tot, s);
-        const LaScan scan = la_scan(p, d, ws + pl.s_fwd, ws + pl.tot, false, in);
+        const LaScan scan = la_scan(ps, d, pl.cut_rows, ws + pl.s_fwd, ws + pl.tot, false, in);
         if (e == hipSuccess) e = launch_la_scans(&scan, 1, s);
+        w.in_row = in;
         w.in = sum.last;
+        w.by_cut = 1;
     }
     if (e == hipSuccess) e = run_walks(p, &w, 1, b16, s);
     return hip_status(fn, e);
@@ -559,8 +570,8 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         ps.max_tiles = ps.w[0].tiles;
         e = launch_la_segments(ps, b16, tot, s);
         const LaScan scans[2] = {
-            la_scan(p, d, sf, tot, false, la_state(initial_state, d.V, false, 1.0f)),
-            la_scan(p, d, sr, tot, true, la_state(dfinal_state, d.V, false, 1.0f / sc))};
+            la_scan(p, d, pl.cut_rows, sf, tot, false, la_state(initial_state, d.V, false, 1.0f)),
+            la_scan(p, d, pl.cut_rows, sr, tot, true, la_state(dfinal_state, d.V, false, 1.0f / sc))};
         if (e == hipSuccess) e = launch_la_scans(scans, 2, s);
         wq.in = la_segment_state(sf, d.nv, d.K, d.V, true);
         wv.in = la_segment_state(sr, d.nv, d.K, d.V, false);

@@ -46,6 +46,10 @@ struct LaWalk {
     int32_t out_f32;        // float32 output whatever the work type
     int32_t third;          // a third bf16 term in the state's sums (float32 states)
     LaState in, last;
+    // by_cut: a row of one segment starts from in_row; `in` holds states by the
+    // number of a segment among those of rows that have several.
+    LaState in_row;
+    int32_t by_cut;
     // Sums for the decays' gradient (row_sum != nullptr): row_sum[part, head,
     // token] += partner . out without the token's own pair, and phi[segment,
     // head, part] = scale <state at the walk's end, phi_in>.
@@ -86,6 +90,7 @@ struct LaParams {
 // Segment sums -> the state that each segment's walk starts from, in place.
 struct LaScan {
     int32_t B, nv, T, seg_len, walk_from, segs;
+    int32_t rows;           // rows of walk_from tokens and more, or their upper bound
     const uint32_t* offsets;
     const uint32_t* slot_idx;
     int32_t n;              // elements per state

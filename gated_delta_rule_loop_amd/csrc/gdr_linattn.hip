@@ -162,14 +162,20 @@ hipError_t run_step(const LaStep& p, hipStream_t s) {
 
 // A thread carries 4 elements of a (row, head) state over the row's segments:
 // each segment's sum is replaced by the state that its walk starts from.  The
-// sums are loaded four steps ahead.  blockIdx.z: the scans of one launch.
+// sums are loaded four steps ahead.  blockIdx.y: the scans of one launch.
 // Bound by the latency of a row's segments in turn: the 16 of 32768 tokens at 32
 // heads, K = V = 128: 14 us for 67 MB.
 struct LaScans { LaScan c[2]; };
 __global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
-    const LaScan& p = both.c[blockIdx.z];
-    const int head = blockIdx.y % p.nv, row = blockIdx.y / p.nv;
-    const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+    const LaScan& p = both.c[blockIdx.y];
+    const int blocks = (p.n / 4 + 255) / 256;    // of a state
+    const int which = blockIdx.x / blocks;
+    const int head = which % p.nv;
+    LaSpan sp;                            // of the rows that are walked, as one segment each
+    if (!la_locate(p.offsets, p.B, p.walk_from ? 0x7FFFFFFF : 0, p.walk_from, which / p.nv, sp))
+        return;
+    const int row = __builtin_amdgcn_readfirstlane(sp.row);
+    const int i = ((blockIdx.x % blocks) * 256 + threadIdx.x) * 4;
     // the row's first segment
     int first = 0;
     for (int b = threadIdx.x & 63; b < row; b += 64)
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
     first = __builtin_amdgcn_readfirstlane(first);
     const int count = la_row_segs(static_cast<int>(p.offsets[row + 1] - p.offsets[row]),
                                   p.seg_len, p.walk_from);
-    if (i >= p.n || count == 0) return;
+    if (i >= p.n) return;
     const uint32_t slot = p.slot_idx ? p.slot_idx[row] : static_cast<uint32_t>(row);
     if (slot == kPadSlot) return;
     la_f4 run = {0, 0, 0, 0};
@@ -335,8 +341,8 @@ hipError_t launch_la_step(const LaStep& p, bool work_bf16, hipStream_t s) {
 hipError_t launch_la_scans(const LaScan* c, int count, hipStream_t s) {
     LaScans both{};
     for (int i = 0; i < count; ++i) both.c[i] = c[i];
-    const dim3 grid(static_cast<uint32_t>((c->n / 4 + 255) / 256),
-                    static_cast<uint32_t>(c->B * c->nv), static_cast<uint32_t>(count));
+    const dim3 grid(static_cast<uint32_t>((c->n / 4 + 255) / 256) * c->rows * c->nv,
+                    static_cast<uint32_t>(count));
     scan_kernel<<<grid, 256, 0, s>>>(both);
     return hipGetLastError();
 }

@@ -70,6 +70,7 @@ struct LaSpan {
     int row, s, count;   // the segment's row, its number there, the row's segments
     int t0, n;           // its tokens
     int first;           // the row's first segment
+    int cut;             // ... and among the segments of rows that have several
 };
 
 // Which tokens segment `seg` spans; false past the last one.  Each wave scans
@@ -84,10 +85,11 @@ __device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_le
         o.t0 = static_cast<int>(off[seg]);
         o.n = static_cast<int>(off[seg + 1]) - o.t0;
         o.first = seg;
+        o.cut = 0;
         return true;
     }
     const int lane = threadIdx.x & 63;
-    int base = 0;
+    int base = 0, cut_base = 0;
     for (int b0 = 0; b0 < B; b0 += 64) {
         const int b = b0 + lane;
         int a = 0, n = 0, c = 0;
@@ -96,10 +98,14 @@ __device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_le
             n = static_cast<int>(off[b + 1]) - a;
             c = la_row_segs(n, seg_len, from);
         }
-        int sum = c;
+        const int cuts = c > 1 ? c : 0;
+        int sum = c, cut_sum = cuts;
         for (int d = 1; d < 64; d <<= 1) {
-            const int up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
+            const int up = __shfl_up(sum, d), cut_up = __shfl_up(cut_sum, d);
+            if (lane >= d) {
+                sum += up;
+                cut_sum += cut_up;
+            }
         }
         const uint64_t past = __ballot(base + sum > seg);
         if (past) {
@@ -108,6 +114,7 @@ __device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_le
             o.row = b0 + at;
             o.count = of(c);
             o.first = base + of(sum) - o.count;
+            o.cut = cut_base + of(cut_sum) - of(cuts);
             o.s = seg - o.first;
             const int ra = of(a), rn = of(n);
             o.t0 = ra + o.s * seg_len;
@@ -116,6 +123,7 @@ __device__ __forceinline__ bool la_locate(const uint32_t* off, int B, int seg_le
             return true;
         }
         base += __builtin_amdgcn_readlane(sum, 63);
+        cut_base += __builtin_amdgcn_readlane(cut_sum, 63);
     }
     return false;
 }

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     if (!la_locate(p.offsets, p.B, p.seg_len, p.walk_from, seg, sp)) return;
     auto uniform = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
     sp = LaSpan{uniform(sp.row), uniform(sp.s), uniform(sp.count), uniform(sp.t0), uniform(sp.n),
-                uniform(sp.first)};
+                uniform(sp.first), uniform(sp.cut)};
     const int Kd = w.Kd, Vd = w.Vd, n = sp.n;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -239,6 +239,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     const int zbase = tile * ZC + wave * 16;        // this wave's columns
     const uint32_t slot = p.slot_idx ? p.slot_idx[sp.row] : static_cast<uint32_t>(sp.row);
     const bool third = w.third != 0, out_f32 = w.out_f32 != 0;
+    const LaState& in = w.by_cut && sp.count == 1 ? w.in_row : w.in;
+    const int state_seg = w.by_cut ? sp.cut + sp.s : seg;
     const bool at_last = w.reverse ? sp.s == 0 : sp.s == sp.count - 1;
     // A segment's sum is taken from its far end: the state needs no decay on the
     // way (the factor of a chunk's tokens takes what was walked), and the walk
@@ -411,7 +413,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
     auto load_as = [&](const LaState& s, auto* p0, la_f4 (&v)[KT]) {
         typedef typename std::remove_const<typename std::remove_pointer<decltype(p0)>::type>::type E;
         const char* base = reinterpret_cast<const char*>(
-            p0 + (s.by_segment ? int64_t{seg} : int64_t{slot}) * s.outer + head * s.head);
+            p0 + int64_t{s.by_segment ? static_cast<uint32_t>(state_seg) : slot} * s.outer +
+            head * s.head);
         const uint32_t off = static_cast<uint32_t>((g4 * s.sk + (zbase + i16) * s.sz) *
                                                    static_cast<int>(sizeof(E)));
         const uint32_t row = static_cast<uint32_t>(s.sk * static_cast<int>(sizeof(E)));
@@ -446,8 +449,8 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
         if (s.bf16) load_as(s, static_cast<const uint16_t*>(s.p), v);
         else load_as(s, static_cast<const float*>(s.p), v);
     };
-    if (!SEG && w.in.p) {
-        load_state(w.in, S);
+    if (!SEG && in.p) {
+        load_state(in, S);
     } else {
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) S[kt] = la_f4{0, 0, 0, 0};
@@ -717,7 +720,7 @@ __global__ void __launch_bounds__(64 * W, KP > 128 || W == 4 ? 2 : 4) walk_kerne
                 scale * sum;
     }
     // a row without tokens leaves its pool slot alone
-    if (w.last.p && at_last && (n > 0 || w.last.p != w.in.p))
+    if (w.last.p && at_last && (n > 0 || w.last.p != in.p))
         store_state(w.last, int64_t{slot} * w.last.outer + head * w.last.head);
 }
 

@@ -389,6 +389,10 @@ MANY = [
     ([20] * 16, 1, 1, 128, 128, "bf16", "bf16", "none"),
     ([0] * 20, 1, 2, 8, 16, "f32", "f32", "token"),
     ([0] * 70 + [300] + [1] * 70 + [9, 8], 1, 3, 16, 24, "bf16", "bf16", "token"),
+    # heads enough to fill the chip: only what is longer than its share is cut
+    ([1] * 14 + [1300, 5, 0, 900, 64, 130], 2, 32, 16, 24, "bf16", "bf16", "token"),
+    ([1] * 70 + [321, 5, 0, 1200, 9] + [3] * 70 + [320], 2, 32, 16, 24, "f32", "f32", "zeros"),
+    ([70] * 16, 4, 32, 8, 16, "f32", "bf16", "head"),
 ]
 
 
@@ -542,6 +546,24 @@ def test_backward(case):
         close("ds0", d0, want["ds0"], A["ds0"], f)
     else:
         assert d0 is None
+
+
+@pytest.mark.gpu
+def test_backward_of_more_rows_and_heads_than_a_grid_dimension_holds():
+    """Every row gets what it gets in a call of its own rows alone, the last ones too."""
+    lens = [1] * 2097 + [600, 0, 3]
+    q, k, v, g, off, offs, gen = inputs(lens, 16, 32, 8, 8, torch.float32, seed=16)
+    s0 = (0.3 * torch.randn((len(lens), 32, 8, 8), generator=gen)).cuda()
+    do = torch.randn(v.shape, generator=gen).cuda()
+    whole = gdr.gdr_linear_attention_bwd(do, q, k, v, g, offs, initial_state=s0,
+                                         dfinal_state=s0)
+    at = off[2090]
+    part = [x[at:] for x in (do, q, k, v, g)]
+    few = gdr.gdr_linear_attention_bwd(*part, offs[2090:] - at, initial_state=s0[2090:],
+                                       dfinal_state=s0[2090:])
+    for i, (x, y) in enumerate(zip(whole, few)):
+        y = y.double().cpu()
+        near(i, x[2090:] if i == 4 else x[at:], y, 1e-5)
 
 
 @pytest.mark.gpu
