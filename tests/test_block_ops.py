@@ -393,6 +393,7 @@ MANY = [
     ([1] * 14 + [1300, 5, 0, 900, 64, 130], 2, 32, 16, 24, "bf16", "bf16", "token"),
     ([1] * 70 + [321, 5, 0, 1200, 9] + [3] * 70 + [320], 2, 32, 16, 24, "f32", "f32", "zeros"),
     ([70] * 16, 4, 32, 8, 16, "f32", "bf16", "head"),
+    ([64] * 15 + [65, 66, 130, 1], 2, 32, 16, 24, "f32", "f32", "token"),
 ]
 
 
