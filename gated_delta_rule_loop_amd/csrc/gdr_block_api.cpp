@@ -648,6 +648,8 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
         h.nk = static_cast<int32_t>(d.nk);
         h.G = static_cast<int32_t>(G);
         h.K = static_cast<int32_t>(d.K);
+        h.B = p.B;
+        h.offsets = p.offsets;
         const gdr_tensor* outs[2] = {dq, dk};
         const int64_t from[2] = {pl.pq, pl.pk};
         for (int i = 0; i < 2 && e == hipSuccess; ++i) {

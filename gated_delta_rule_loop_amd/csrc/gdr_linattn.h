@@ -112,7 +112,8 @@ struct LaDecayGrad {
 };
 
 struct LaHeadSum {          // out[t, hk, :] = sum over the group of part[t, hv, :]
-    int32_t T, nk, G, K;
+    int32_t T, nk, G, K, B;
+    const uint32_t* offsets;   // tokens outside [offsets[0], offsets[B]) have no parts
     const float* part;      // [T, nk * G, K]
     void* out; int64_t out_tok, out_head;
 };

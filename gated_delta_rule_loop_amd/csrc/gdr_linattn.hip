@@ -306,19 +306,21 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const LaDecayGrad p) {
 // --------------------------------------------------------------- head sums ---
 
 // Gradients of key heads that G value heads share: the heads' float32 parts
-// added in order and rounded once.  1507 tokens, 4 key heads of 64: 4.3 us, the
-// launch's own time.
+// added in order and rounded once.  Tokens of no row are left alone: the walks
+// wrote no parts for them.  1507 tokens, 4 key heads of 64: 4.3 us, the launch's
+// own time.
 template <typename T>
 __global__ void __launch_bounds__(256) head_sum_kernel(const LaHeadSum p) {
     const int K4 = p.K >> 2;
     const int64_t i = int64_t{blockIdx.x} * 256 + threadIdx.x;
     if (i >= int64_t{p.T} * p.nk * K4) return;
     const int c = static_cast<int>(i % K4) * 4;
-    const int64_t th = i / K4;
+    const int64_t th = i / K4, t = th / p.nk;
+    if (t < int64_t{p.offsets[0]} || t >= int64_t{p.offsets[p.B]}) return;
     const float* s = p.part + th * p.G * p.K + c;
     la_f4 sum = {0, 0, 0, 0};
     for (int m = 0; m < p.G; ++m) sum += *reinterpret_cast<const la_f4*>(s + int64_t{m} * p.K);
-    T* o = static_cast<T*>(p.out) + th / p.nk * p.out_tok + th % p.nk * p.out_head + c;
+    T* o = static_cast<T*>(p.out) + t * p.out_tok + th % p.nk * p.out_head + c;
     if constexpr (sizeof(T) == 2) {
         la_b4 b;
 #pragma unroll
