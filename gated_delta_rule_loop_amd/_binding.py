@@ -8,6 +8,7 @@ missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -318,25 +319,32 @@ def _scale_value(scale):
     return -1.0 if scale is None else float(scale)  # not positive or NaN: the default
 
 
+def _memory_of(stream):
+    """Allocations inside come from `stream`'s own memory: a block that another
+    stream has freed may still be in use there, and nothing makes `stream` wait
+    for it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _scratch(floats, like, stream):
     """float32 workspace for a call on `stream` (torch's current one when None)."""
     if floats <= 0:
         return None
-    ws = torch.empty(floats, dtype=torch.float32, device=like.device)
-    if stream is not None:  # allocated on the current stream, used on the caller's
-        ws.record_stream(stream)
-    return ws
+    with _memory_of(stream):
+        return torch.empty(floats, dtype=torch.float32, device=like.device)
 
 
 def _new(like, shape=None, dtype=None, stream=None):
-    """An output allocated here: on the current stream, written on the caller's."""
-    if shape is None and like.is_contiguous():
-        t = torch.empty_like(like)
-    else:
-        t = torch.empty(like.shape if shape is None else shape, dtype=dtype or like.dtype,
-                        device=like.device)
+    """An output allocated here, written on `stream` and handed to a program that
+    may read it on its current one."""
+    with _memory_of(stream):
+        if shape is None and like.is_contiguous():
+            t = torch.empty_like(like)
+        else:
+            t = torch.empty(like.shape if shape is None else shape, dtype=dtype or like.dtype,
+                            device=like.device)
     if stream is not None:
-        t.record_stream(stream)
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 

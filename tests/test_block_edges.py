@@ -1,9 +1,12 @@
 """Linear attention and the fused norms where their calls border on something
 else.  Error bounds as in test_block_ops.py."""
+import contextlib
+
 import pytest
 import torch
 
 import gated_delta_rule_loop_amd as gdr
+from gated_delta_rule_loop_amd import _binding as B
 from tests import block_ref as ref
 from tests.test_block_ops import BWD, DT, U32, bwd_inputs, inputs, near
 
@@ -56,3 +59,83 @@ def test_decay_gradient_after_a_few_large_tokens(lens, work, at):
     want = ref.attention_grads(do, q, k, v, g, off, None, None, 64 ** -0.5)["dg"]
     n = max(lens)
     near("dg", dg[late], want[late], (40 * U32 + (2.0 ** -16 if work == "bf16" else 0)) * n ** 0.5)
+
+
+# ----------------------------------------------------- the caller's stream ---
+
+def test_buffers_made_for_a_stream_come_from_its_memory(monkeypatch):
+    """The allocator hands a block out again in the order of the stream that freed
+    it: what a call on another stream writes has to be allocated on that one.  An
+    output is also held for the program's current stream."""
+    current, made, held = ["main"], [], []
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, current[0] = current[0], stream
+        yield
+        current[0] = before
+
+    def counted(f):
+        def g(*a, **kw):
+            made.append(current[0])
+            return f(*a, **kw)
+        return g
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[0])
+    for name in ("empty", "empty_like"):
+        monkeypatch.setattr(torch, name, counted(getattr(torch, name)))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.append(s))
+    x = torch.ones(4, 6)
+    B._scratch(10, x, "side")
+    assert made == ["side"]
+    for like, shape in ((x, None), (x.t(), None), (x, (3, 2))):
+        made.clear(), held.clear()
+        assert B._new(like, shape, stream="side").shape == (shape or like.shape)
+        assert made == ["side"] and held == ["main"]
+    made.clear(), held.clear()
+    B._scratch(10, x, None)
+    B._new(x)
+    assert made == ["main"] * 2 and not held and current == ["main"]
+
+
+def busy_then_fill(floats, value):
+    """A block that the current stream has freed and will yet write, after about a
+    millisecond of other work; its address."""
+    a = torch.ones(4096, 4096, device="cuda")
+    x = torch.empty(floats, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(4):
+        a = a @ a * 1e-4
+    x.fill_(value)
+    return x.data_ptr()
+
+
+@pytest.mark.gpu
+def test_calls_on_a_stream_do_not_wait_for_the_current_one():
+    """Inputs ready, nothing else ordered between the streams: results are those of
+    the current stream, whatever it is still writing into memory it has freed."""
+    do, q, k, v, g, off, offs, s0, ds = bwd_inputs(BWD[11])
+    y = torch.randn(64, 256, generator=torch.Generator().manual_seed(1)).cuda()
+    w = torch.ones(256, device="cuda")
+    s = slice(off[0], off[-1])
+    calls = {
+        "fwd": lambda st: gdr.gdr_linear_attention_fwd(
+            q, k, v, g, offs, initial_state=s0, output_final_state=True, stream=st),
+        "bwd": lambda st: gdr.gdr_linear_attention_bwd(
+            do, q, k, v, g, offs, initial_state=s0, dfinal_state=ds, stream=st),
+        "norm": lambda st: gdr.gdr_block_norm(y, residual=y, pre_weight=w, stream=st),
+        "norm bwd": lambda st: gdr.gdr_block_norm_bwd(y, y, y, y, pre_weight=w, stream=st),
+    }
+    inside = lambda t: t[s] if t.shape[0] == q.shape[0] else t  # noqa: E731
+    side = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = [inside(t).clone() for t in call(None) if t is not None]
+        sizes = {t.numel() * t.element_size() // 4 for t in call(None) if t is not None}
+        torch.cuda.synchronize()
+        freed = [busy_then_fill(n, float("nan")) for n in sizes]
+        got = [t for t in call(side) if t is not None]
+        assert not {t.data_ptr() for t in got} & set(freed), name
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, inside(b)), name
