@@ -221,12 +221,11 @@ def gdr_fused_recurrent_update(q, k, v, g=None, beta=None, scale=None, initial_s
     v's dtype) and a dense final state are allocated here with torch when not
     passed in."""
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = _new(v, stream=stream)
     if state is None and output_final_state and final_state is None:
         N = q.shape[0] if cu_seqlens is None else cu_seqlens.shape[0] - 1
         dt = initial_state.dtype if initial_state is not None else torch.float32
-        final_state = torch.empty((N, v.shape[2], q.shape[3], v.shape[3]), dtype=dt,
-                                  device=v.device)
+        final_state = _new(v, (N, v.shape[2], q.shape[3], v.shape[3]), dt, stream)
     args = [describe(x) for x in (q, k, v, g, beta)]
     init_d, fin_d = describe(initial_state), describe(final_state)
     rest = [describe(x) for x in (cu_seqlens, state, state_indices, intermediate_states)]
@@ -256,7 +255,7 @@ def gdr_causal_conv1d(x, weight, input_row_offsets, *, bias=None, conv_state=Non
     torch, x's dtype and shape, when not passed in); conv_state is updated in
     place."""
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x, stream=stream)
     ds = [describe(t) for t in (out, x, weight, bias, conv_state, slot_idx, input_row_offsets)]
     rc = lib().gdr_causal_conv1d(*[_ref(d) for d in ds], GDR_FLAG_CONV_SILU if silu else 0,
                                  _stream(stream))

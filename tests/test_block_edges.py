@@ -63,6 +63,24 @@ def test_decay_gradient_after_a_few_large_tokens(lens, work, at):
 
 # ----------------------------------------------------- the caller's stream ---
 
+@pytest.mark.parametrize("call", ["conv", "update"])
+def test_entry_points_allocate_on_the_callers_stream(call, monkeypatch):
+    """The Python functions hand their stream on to what they allocate."""
+    class Stop(Exception):
+        pass
+
+    def new(like, shape=None, dtype=None, stream=None):
+        raise Stop(stream)
+
+    monkeypatch.setattr(B, "_new", new)
+    x = torch.ones(4, 2, 2, 8)
+    with pytest.raises(Stop, match="side"):
+        if call == "conv":
+            gdr.gdr_causal_conv1d(x[0, 0], x[0, 0], None, stream="side")
+        else:
+            gdr.gdr_fused_recurrent_update(x, x, x, stream="side")
+
+
 def test_buffers_made_for_a_stream_come_from_its_memory(monkeypatch):
     """The allocator hands a block out again in the order of the stream that freed
     it: what a call on another stream writes has to be allocated on that one.  An
@@ -118,6 +136,10 @@ def test_calls_on_a_stream_do_not_wait_for_the_current_one():
     do, q, k, v, g, off, offs, s0, ds = bwd_inputs(BWD[11])
     y = torch.randn(64, 256, generator=torch.Generator().manual_seed(1)).cuda()
     w = torch.ones(256, device="cuda")
+    conv, rows = torch.full((256, 4), 0.25, device="cuda"), torch.tensor([0, 64]).int().cuda()
+    u = torch.randn(2, 8, 2, 32, generator=torch.Generator().manual_seed(2)).cuda()
+    ug, u0 = -u[..., 0].abs().contiguous(), torch.ones(2, 2, 32, 32, device="cuda")
+    beta = ug.sigmoid()
     s = slice(off[0], off[-1])
     calls = {
         "fwd": lambda st: gdr.gdr_linear_attention_fwd(
@@ -126,6 +148,9 @@ def test_calls_on_a_stream_do_not_wait_for_the_current_one():
             do, q, k, v, g, offs, initial_state=s0, dfinal_state=ds, stream=st),
         "norm": lambda st: gdr.gdr_block_norm(y, residual=y, pre_weight=w, stream=st),
         "norm bwd": lambda st: gdr.gdr_block_norm_bwd(y, y, y, y, pre_weight=w, stream=st),
+        "conv": lambda st: (gdr.gdr_causal_conv1d(y, conv, rows, stream=st),),
+        "update": lambda st: gdr.gdr_fused_recurrent_update(
+            u, u, u, ug, beta, initial_state=u0, output_final_state=True, stream=st),
     }
     inside = lambda t: t[s] if t.shape[0] == q.shape[0] else t  # noqa: E731
     side = torch.cuda.Stream()
