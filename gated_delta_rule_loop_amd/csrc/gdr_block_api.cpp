@@ -17,14 +17,17 @@ typedef long long ll;
 
 constexpr int64_t kLaMaxTokenStride = (int64_t{1} << 24) - 1;
 
-// [tokens, heads, dim] operand: unit innermost stride, 16-byte rows.
+// [tokens, heads, dim] operand: unit innermost stride, 16-byte rows.  `walked`:
+// the walks read it, which address a chunk's tokens from one 64-bit base by
+// unsigned 32-bit offsets.
 int check_heads(const char* fn, const char* name, const gdr_tensor* t, int64_t T, int64_t heads,
-                int64_t dim, int32_t work) {
+                int64_t dim, int32_t work, bool walked) {
     const int64_t shape[3] = {T, heads, dim};
     int rc = check_tensor(fn, name, t, 3, shape, true, true, false);
     if (rc || (rc = check_work_dtype(fn, name, t, work))) return rc;
     if ((rc = check_layout(fn, name, t, vec_mult(work)))) return rc;
-    // the kernels address a chunk's tokens from one 64-bit base by 32-bit offsets
+    if (T > 1 && heads > 0 && walked && t->stride[0] < 0)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a negative token stride", fn, name);
     if (T > 1 && heads > 0 && std::llabs(t->stride[0]) > kLaMaxTokenStride)
         return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a token stride above %lld elements", fn, name,
                     static_cast<ll>(kLaMaxTokenStride));
@@ -54,7 +57,7 @@ int check_distinct(const char* fn, const char* name, const gdr_tensor* t) {
 
 int check_out_heads(const char* fn, const char* name, const gdr_tensor* t, int64_t T,
                     int64_t heads, int64_t dim, int32_t work) {
-    int rc = check_heads(fn, name, t, T, heads, dim, work);
+    int rc = check_heads(fn, name, t, T, heads, dim, work, false);
     return rc ? rc : check_distinct(fn, name, t);
 }
 
@@ -204,7 +207,7 @@ struct LaDims {
 };
 
 int check_la(const char* fn, const gdr_tensor* q, const gdr_tensor* k, const gdr_tensor* v,
-             const gdr_tensor* g, LaDims& d) {
+             const gdr_tensor* g, bool walked, LaDims& d) {
     int rc = check_tensor(fn, "q", q, 3, nullptr, true, true, false);
     if (rc || (rc = check_tensor(fn, "v", v, 3, nullptr, true, true, false))) return rc;
     d.T = q->shape[0];
@@ -220,9 +223,9 @@ int check_la(const char* fn, const gdr_tensor* q, const gdr_tensor* k, const gdr
         d.V > GDR_MAX_HEAD_DIM)
         return fail(GDR_ERR_UNSUPPORTED, "%s: head dims K=%lld V=%lld (multiples of 8 up to %d)",
                     fn, static_cast<ll>(d.K), static_cast<ll>(d.V), GDR_MAX_HEAD_DIM);
-    if ((rc = check_heads(fn, "q", q, d.T, d.nk, d.K, d.work)) ||
-        (rc = check_heads(fn, "k", k, d.T, d.nk, d.K, d.work)) ||
-        (rc = check_heads(fn, "v", v, d.T, d.nv, d.V, d.work)))
+    if ((rc = check_heads(fn, "q", q, d.T, d.nk, d.K, d.work, walked)) ||
+        (rc = check_heads(fn, "k", k, d.T, d.nk, d.K, d.work, walked)) ||
+        (rc = check_heads(fn, "v", v, d.T, d.nv, d.V, d.work, walked)))
         return rc;
     const int64_t gs[2] = {d.T, d.nv};
     if (present(g) && (rc = check_tensor(fn, "g", g, 2, gs, true, true, false))) return rc;
@@ -378,7 +381,7 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
     const char* fn = "gdr_linear_attention_fwd";
     LaDims d{};
     int rc;
-    if ((rc = check_la(fn, q, k, v, g, d)) || (rc = check_offsets(fn, input_row_offsets, d)) ||
+    if ((rc = check_la(fn, q, k, v, g, true, d)) || (rc = check_offsets(fn, input_row_offsets, d)) ||
         (rc = check_out_heads(fn, "o", o, d.T, d.nv, d.V, d.work)) ||
         (rc = no_alias(fn, o, "o", {q, k, v, g})))
         return rc;
@@ -469,7 +472,7 @@ int gdr_linear_attention_step(const gdr_tensor* o, const gdr_tensor* q, const gd
     const char* fn = "gdr_linear_attention_step";
     LaDims d{};
     int rc;
-    if ((rc = check_la(fn, q, k, v, g, d)) ||
+    if ((rc = check_la(fn, q, k, v, g, false, d)) ||
         (rc = check_out_heads(fn, "o", o, d.T, d.nv, d.V, d.work)) ||
         (rc = no_alias(fn, o, "o", {q, k, v, g})) ||
         (rc = check_la_state(fn, "state", state, -1, d.nv, d.K, d.V, true)))
@@ -503,8 +506,8 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
     const char* fn = "gdr_linear_attention_bwd";
     LaDims d{};
     int rc;
-    if ((rc = check_la(fn, q, k, v, g, d)) || (rc = check_offsets(fn, input_row_offsets, d)) ||
-        (rc = check_heads(fn, "do", d_o, d.T, d.nv, d.V, d.work)) ||
+    if ((rc = check_la(fn, q, k, v, g, true, d)) || (rc = check_offsets(fn, input_row_offsets, d)) ||
+        (rc = check_heads(fn, "do", d_o, d.T, d.nv, d.V, d.work, true)) ||
         (rc = check_out_heads(fn, "dq", dq, d.T, d.nk, d.K, d.work)) ||
         (rc = check_out_heads(fn, "dk", dk, d.T, d.nk, d.K, d.work)) ||
         (rc = check_out_heads(fn, "dv", dv, d.T, d.nv, d.V, d.work)) ||

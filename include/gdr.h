@@ -290,9 +290,11 @@ int gdr_causal_conv1d(const gdr_tensor* out, const gdr_tensor* x, const gdr_tens
  *   q, k              [T, nk, K] work dtype: f32 or bf16 (float32 sums either
  *                     way); K a multiple of 8 up to GDR_MAX_HEAD_DIM
  *   v, o              [T, nv, V] work; nv a multiple of nk; V like K.  Heads
- *                     and tokens take any strides that keep 16-byte rows (a
- *                     token stride below 2^24 elements), so channel
- *                     ranges of a packed projection can be given as they are.
+ *                     and tokens take any strides that keep 16-byte rows, so
+ *                     channel ranges of a packed projection can be given as
+ *                     they are; token strides are below 2^24 elements in
+ *                     magnitude, and not negative except in
+ *                     gdr_linear_attention_step.
  *   g                 [T, nv] f32 or bf16 log decay, any strides (a fixed
  *                     decay per head: stride 0 over the tokens); -inf is a
  *                     decay of 0; absent: no decay

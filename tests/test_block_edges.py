@@ -8,7 +8,7 @@ import torch
 import gated_delta_rule_loop_amd as gdr
 from gated_delta_rule_loop_amd import _binding as B
 from tests import block_ref as ref
-from tests.test_block_ops import BWD, DT, U32, bwd_inputs, inputs, near
+from tests.test_block_ops import BWD, D, DT, FAKE, I32, U32, _call, _fwd, bwd_inputs, inputs, near
 
 
 # ------------------------------------------------- tokens outside the rows ---
@@ -164,3 +164,26 @@ def test_calls_on_a_stream_do_not_wait_for_the_current_one():
         torch.cuda.synchronize()
         for a, b in zip(want, got):
             assert torch.equal(a, inside(b)), name
+
+
+# -------------------------------------------------- strides and launch sizes ---
+
+@pytest.mark.parametrize("name,shape", [("q", [2000, 2, 64]), ("k", [2000, 2, 64]),
+                                        ("v", [2000, 4, 32])])
+def test_forward_refuses_tokens_in_falling_order_of_address(name, shape):
+    back = D(shape, stride=[-shape[1] * shape[2], shape[2], 1], data=FAKE * 64)
+    assert _call("gdr_linear_attention_fwd", _fwd(**{name: back, "ws": None})) == -2
+    assert f"{name} has a negative token stride" in B.gdr_last_error_message()
+
+
+@pytest.mark.parametrize("name", ["do", "q", "k", "v"])
+def test_backward_refuses_tokens_in_falling_order_of_address(name):
+    a = dict(do=D([100, 4, 32]), q=D([100, 2, 64]), k=D([100, 2, 64]), v=D([100, 4, 32]),
+             g=D([100, 4]), off=D([3], I32), scale=-1.0, s0=None, ds=None,
+             dq=D([100, 2, 64], data=FAKE * 2), dk=D([100, 2, 64], data=FAKE * 3),
+             dv=D([100, 4, 32], data=FAKE * 4), dg=D([100, 4], data=FAKE * 6), d0=None,
+             ws=None, stream=None)
+    shape = list(a[name].shape[:3])
+    a[name] = D(shape, stride=[-shape[1] * shape[2], shape[2], 1], data=FAKE * 64)
+    assert _call("gdr_linear_attention_bwd", list(a.values())) == -2
+    assert f"{name} has a negative token stride" in B.gdr_last_error_message()
