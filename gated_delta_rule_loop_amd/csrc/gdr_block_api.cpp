@@ -242,10 +242,17 @@ int check_offsets(const char* fn, const gdr_tensor* off, LaDims& d) {
     return check_index_vec(fn, "input_row_offsets", off, d.B + 1);
 }
 
-int check_grid(const char* fn, int64_t blocks) {
-    if (blocks > INT32_MAX)
+// A launch holds fewer than 2^32 threads in a dimension.  Every launch of a call is
+// checked before the first, which may already change states.
+int check_grid(const char* fn, int64_t blocks, int64_t threads) {
+    if (blocks > UINT32_MAX / threads)
         return fail(GDR_ERR_INVALID_ARG, "%s: batch too large for one launch", fn);
     return GDR_OK;
+}
+
+int check_scan(const char* fn, const LaDims& d, int64_t rows) {
+    return check_grid(fn, la_scan_blocks(static_cast<int>(d.K * d.V)) * rows * d.nv,
+                      kLaScanThreads);
 }
 
 void set_decay(const gdr_tensor* g, const void*& p, int64_t& tok, int64_t& head, int32_t& bf16) {
@@ -414,10 +421,17 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
     const float sc = resolve_scale(scale, d.K);
     const LaState in = la_state(pool ? state : initial_state, d.V, false, 1.0f);
     const LaState last = la_state(pool ? state : final_state, d.V, false, 1.0f);
-    if ((rc = check_grid(fn, d.B * d.nv))) return rc;
     const LaPlan pl = la_plan(d.T, d.B, d.nk, d.nv, d.K, d.V, false);
+    // with rows enough those of few tokens go token by token, and these are walked
+    const bool split = d.B >= kLaStepRows;
+    const int64_t rows = split ? std::min(d.B, d.T / (kLaStepTokens + 1)) : d.B;
+    const int64_t segs = !split ? pl.segs : rows + (pl.seg_len ? d.T / pl.seg_len : 0);
+    const int64_t wide = 64 * la_waves(static_cast<int>(d.V));
     if ((rc = check_workspace(fn, workspace, pl.end)) ||
-        (rc = check_grid(fn, pl.segs * d.nv * pl.v_tiles)))
+        (split && (rc = check_grid(fn, d.B * d.nv, la_step_threads(d.K, d.V)))) ||
+        (rows && (rc = check_grid(fn, segs * d.nv * pl.v_tiles, wide))) ||
+        (pl.seg_len && ((rc = check_grid(fn, pl.cuts * d.nv * pl.v_tiles, wide)) ||
+                        (rc = check_scan(fn, d, pl.cut_rows)))))
         return rc;
     IndexCheck ic;
     ic.offsets = input_row_offsets;
@@ -430,12 +444,11 @@ int gdr_linear_attention_fwd(const gdr_tensor* o, const gdr_tensor* q, const gdr
     const int64_t G = d.nv / d.nk;
     LaParams p = la_params(d, pl, input_row_offsets, slot_idx, g, sc);
     hipError_t e = hipSuccess;
-    if (d.B >= kLaStepRows) {
+    if (split) {
         e = run_step(d, o, q, k, v, g, input_row_offsets, slot_idx, in, last, sc, s);
-        const int64_t rows = std::min(d.B, d.T / (kLaStepTokens + 1));  // that are longer
         if (e != hipSuccess || rows == 0) return hip_status(fn, e);
         p.walk_from = kLaStepTokens + 1;
-        p.segs = static_cast<int32_t>(rows + (pl.seg_len ? d.T / pl.seg_len : 0));
+        p.segs = static_cast<int32_t>(segs);
         if (!pl.seg_len) p.seg_len = p.T;
     }
     LaWalk w = la_walk(la_tensor(q, G), la_tensor(k, G), la_tensor(v, 1), d.K, d.V, false);
@@ -484,7 +497,7 @@ int gdr_linear_attention_step(const gdr_tensor* o, const gdr_tensor* q, const gd
         return fail(GDR_ERR_INVALID_ARG, "%s: state has fewer slots than rows", fn);
     }
     if (d.B == 0) return done();
-    if ((rc = check_grid(fn, d.B * d.nv))) return rc;
+    if ((rc = check_grid(fn, d.B * d.nv, la_step_threads(d.K, d.V)))) return rc;
     IndexCheck ic;
     if (present(slot_idx)) {
         ic.slots = slot_idx;
@@ -538,8 +551,17 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
                     static_cast<ll>(kLaMaxTokenStride));
     if (d.B == 0) return done();
     const LaPlan pl = la_plan(d.T, d.B, d.nk, d.nv, d.K, d.V, true);
+    const int K = static_cast<int>(d.K), V = static_cast<int>(d.V);
+    const bool one = size_class(V, K) == size_class(K, V);  // launch of the three walks
+    const int64_t rows = pl.segs * d.nv, wide_k = 64 * la_waves(K), wide_v = 64 * la_waves(V);
     if ((rc = check_workspace(fn, workspace, pl.end)) ||
-        (rc = check_grid(fn, pl.segs * d.nv * 3 * std::max(pl.q_tiles, pl.v_tiles))))
+        (one ? (rc = check_grid(fn, rows * 3 * std::max(pl.q_tiles, pl.v_tiles), wide_v))
+             : (rc = check_grid(fn, rows * 2 * pl.q_tiles, wide_k)) ||
+                   (rc = check_grid(fn, rows * pl.v_tiles, wide_v))) ||
+        (pl.seg_len && ((rc = check_grid(fn, pl.cuts * d.nv * 2 * pl.v_tiles, wide_v)) ||
+                        (rc = check_scan(fn, d, pl.cut_rows)))) ||
+        (present(dg) && (rc = check_grid(fn, rows, 256))) ||
+        (d.nv != d.nk && (rc = check_grid(fn, ceil_div(d.T * d.nk * (d.K / 4), 256), 256))))
         return rc;
     IndexCheck ic;
     ic.offsets = input_row_offsets;
@@ -617,7 +639,7 @@ int gdr_linear_attention_bwd(const gdr_tensor* d_o, const gdr_tensor* q, const g
     }
     const LaWalk all[3] = {wq, wv, wk};
     if (e == hipSuccess) {
-        if (size_class(wq.Kd, wq.Vd) == size_class(wv.Kd, wv.Vd)) {
+        if (one) {
             e = run_walks(p, all, 3, b16, s);
         } else {
             const LaWalk two[2] = {wq, wk};
@@ -812,6 +834,7 @@ int gdr_block_norm(const gdr_tensor* h, const gdr_tensor* n, const gdr_tensor* y
     p.h = h->data;
     p.h_row = h->stride[0];
     if (none) return done();
+    if ((rc = check_grid(fn, p.T, norm_threads(p)))) return rc;
     return hip_status(fn, launch_norm(p, work == GDR_DTYPE_BF16, static_cast<hipStream_t>(stream)));
 }
 

@@ -136,6 +136,15 @@ struct LaStep {
 // Waves of a walk's workgroup, of 16 columns of the state each.
 inline int la_waves(int Vd) { return Vd <= 64 ? 4 : 8; }
 
+// Threads of a step's workgroup: 8 x 8 elements of the state each.
+inline int64_t la_step_threads(int64_t K, int64_t V) { return ((K / 8) * (V / 8) + 63) / 64 * 64; }
+
+// Workgroups of a scan over one state of n elements, 4 a thread.
+constexpr int kLaScanThreads = 256;
+__host__ __device__ inline int la_scan_blocks(int n) {
+    return (n / 4 + kLaScanThreads - 1) / kLaScanThreads;
+}
+
 hipError_t launch_la_walks(const LaParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_la_segments(const LaParams& p, bool work_bf16, float* tot, hipStream_t s);
 hipError_t launch_la_scans(const LaScan* c, int count, hipStream_t s);

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(THREADS) step_kernel(const LaStep p) {
 
 template <typename T, typename ST>
 hipError_t run_step(const LaStep& p, hipStream_t s) {
-    const int threads = ((p.K / 8) * (p.V / 8) + 63) / 64 * 64;
+    const int threads = static_cast<int>(la_step_threads(p.K, p.V));
     const uint32_t lds = static_cast<uint32_t>((2 * p.K + (p.K / 8) * p.V) * sizeof(float));
     const dim3 grid(static_cast<uint32_t>(p.B) * p.nv);
     if (threads <= 256)
@@ -166,16 +166,16 @@ hipError_t run_step(const LaStep& p, hipStream_t s) {
 // Bound by the latency of a row's segments in turn: the 16 of 32768 tokens at 32
 // heads, K = V = 128: 14 us for 67 MB.
 struct LaScans { LaScan c[2]; };
-__global__ void __launch_bounds__(256) scan_kernel(const LaScans both) {
+__global__ void __launch_bounds__(kLaScanThreads) scan_kernel(const LaScans both) {
     const LaScan& p = both.c[blockIdx.y];
-    const int blocks = (p.n / 4 + 255) / 256;    // of a state
+    const int blocks = la_scan_blocks(p.n);      // of a state
     const int which = blockIdx.x / blocks;
     const int head = which % p.nv;
     LaSpan sp;                            // of the rows that are walked, as one segment each
     if (!la_locate(p.offsets, p.B, p.walk_from ? 0x7FFFFFFF : 0, p.walk_from, which / p.nv, sp))
         return;
     const int row = __builtin_amdgcn_readfirstlane(sp.row);
-    const int i = ((blockIdx.x % blocks) * 256 + threadIdx.x) * 4;
+    const int i = ((blockIdx.x % blocks) * kLaScanThreads + threadIdx.x) * 4;
     // the row's first segment
     int first = 0;
     for (int b = threadIdx.x & 63; b < row; b += 64)
@@ -370,9 +370,9 @@ hipError_t launch_la_step(const LaStep& p, bool work_bf16, hipStream_t s) {
 hipError_t launch_la_scans(const LaScan* c, int count, hipStream_t s) {
     LaScans both{};
     for (int i = 0; i < count; ++i) both.c[i] = c[i];
-    const dim3 grid(static_cast<uint32_t>((c->n / 4 + 255) / 256) * c->rows * c->nv,
+    const dim3 grid(static_cast<uint32_t>(la_scan_blocks(c->n)) * c->rows * c->nv,
                     static_cast<uint32_t>(count));
-    scan_kernel<<<grid, 256, 0, s>>>(both);
+    scan_kernel<<<grid, kLaScanThreads, 0, s>>>(both);
     return hipGetLastError();
 }
 

@@ -44,6 +44,9 @@ constexpr int kNormMaxDim = 16384;
 // Workgroups that share the backward's rows.
 int norm_parts(int64_t T, int D);
 
+// Threads of a forward's workgroup; one workgroup a row.
+int norm_threads(const NormParams& p);
+
 hipError_t launch_norm(const NormParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_norm_bwd(const NormParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_norm_reduce(const NormReduce* r, int count, hipStream_t s);

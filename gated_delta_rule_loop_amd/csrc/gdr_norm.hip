@@ -463,6 +463,8 @@ int norm_parts(int64_t T, int D) {
     return static_cast<int>((T + rows - 1) / rows);
 }
 
+int norm_threads(const NormParams& p) { return row_threads(p.D, fwd_units(p)); }
+
 hipError_t launch_norm(const NormParams& p, bool work_bf16, hipStream_t s) {
     if (fwd_units(p) == 1)
         return work_bf16 ? run<uint16_t, false, 1>(p, s) : run<float, false, 1>(p, s);

@@ -187,3 +187,43 @@ def test_backward_refuses_tokens_in_falling_order_of_address(name):
     a[name] = D(shape, stride=[-shape[1] * shape[2], shape[2], 1], data=FAKE * 64)
     assert _call("gdr_linear_attention_bwd", list(a.values())) == -2
     assert f"{name} has a negative token stride" in B.gdr_last_error_message()
+
+
+def refused_as_too_large(fn, args):
+    assert _call(fn, args) == -1
+    assert "too large for one launch" in B.gdr_last_error_message()
+
+
+@pytest.mark.parametrize("T,R", [(4, 2 ** 26), (9 * 2 ** 25, 2 ** 25)], ids=["step", "walk"])
+def test_forward_refuses_what_one_launch_cannot_hold(T, R):
+    """Before the first launch: the short rows' states do not move when the long
+    rows cannot be walked."""
+    x = D([T, 1, 8])
+    refused_as_too_large("gdr_linear_attention_fwd", _fwd(
+        o=D([T, 1, 8], data=FAKE * 2), q=x, k=x, v=x, g=None, off=D([R + 1], I32),
+        state=D([R, 1, 8, 8]), slot=None, ws=D([2 ** 40])))
+
+
+def test_step_refuses_what_one_launch_cannot_hold():
+    x = D([2 ** 26, 1, 8])
+    refused_as_too_large("gdr_linear_attention_step", [
+        D([2 ** 26, 1, 8], data=FAKE * 2), x, x, x, None, D([2 ** 26, 1, 8, 8]), None, -1.0, None])
+
+
+@pytest.mark.parametrize("T,nk,nv,K,R,dg", [
+    (2 ** 23, 1, 1, 64, 2 ** 23, False),        # three walks of 256 threads a row
+    (2 ** 22, 1, 1, 256, 2 ** 22, True),        # scans: 64 workgroups a state
+    (2 ** 30, 1, 2, 16, 1, False),              # sums over heads: a thread for 4 values
+], ids=["walks", "scans", "sums"])
+def test_backward_refuses_what_one_launch_cannot_hold(T, nk, nv, K, R, dg):
+    q, v = D([T, nk, K]), D([T, nv, K])
+    refused_as_too_large("gdr_linear_attention_bwd", [
+        v, q, q, v, D([T, nv]), D([R + 1], I32), -1.0, None, None, D([T, nk, K], data=FAKE * 2),
+        D([T, nk, K], data=FAKE * 3), D([T, nv, K], data=FAKE * 4),
+        D([T, nv], data=FAKE * 6) if dg else None, None, D([2 ** 50]), None])
+
+
+def test_norm_refuses_what_one_launch_cannot_hold():
+    x = D([2 ** 26, 64])
+    refused_as_too_large("gdr_block_norm", [
+        D([2 ** 26, 64], data=FAKE * 2), None, x, None, None, None, None, 0, 1.0, 1e-6, 0, None])
