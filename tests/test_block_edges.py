@@ -8,7 +8,8 @@ import torch
 import gated_delta_rule_loop_amd as gdr
 from gated_delta_rule_loop_amd import _binding as B
 from tests import block_ref as ref
-from tests.test_block_ops import BWD, D, DT, FAKE, I32, U32, _call, _fwd, bwd_inputs, inputs, near
+from tests.test_block_ops import (BWD, D, DT, FAKE, I32, U32, _call, _fwd, bounds, bwd_inputs,
+                                  close, inputs, near)
 
 
 # ------------------------------------------------- tokens outside the rows ---
@@ -227,3 +228,81 @@ def test_norm_refuses_what_one_launch_cannot_hold():
     x = D([2 ** 26, 64])
     refused_as_too_large("gdr_block_norm", [
         D([2 ** 26, 64], data=FAKE * 2), None, x, None, None, None, None, 0, 1.0, 1e-6, 0, None])
+
+
+# --------------------------------------------------------- what a test can see ---
+
+@pytest.mark.gpu
+def test_gradient_of_a_shared_decay_against_differences():
+    """The float64 reference's own central differences (2^-17: cubic terms and
+    rounding below 1e-6 of the slope).  The kernel's sum over N tokens is off by
+    sqrt(N) times test_backward's bound of the whole at most, below a thousandth."""
+    case = ([90, 20], 1, 2, 32, 32, "f32", True, "head")
+    do, q, k, v, g, off, offs, s0, ds = bwd_inputs(case)
+    s = slice(off[0], off[-1])
+    dg = gdr.gdr_linear_attention_bwd(do, q, k, v, g, offs, initial_state=s0, dfinal_state=ds)[3]
+    got = dg[s].double().sum(0).cpu()
+    do, ds, rates = do.cpu().double()[s], ds.cpu().double(), g[0].cpu().double()
+
+    def loss(rates):
+        o, end = ref.attention(q, k, v, rates.expand(q.shape[0], 2), off, s0, 32 ** -0.5)
+        return float((o[s] * do).sum() + (end * ds).sum())
+
+    most = 110 ** 0.5 * 40 * 90 ** 0.5 * U32 * float(dg[s].double().norm())
+    for h in range(2):
+        step = torch.zeros(2, dtype=torch.float64)
+        step[h] = 2.0 ** -17
+        want = (loss(rates + step) - loss(rates - step)) / 2.0 ** -16
+        assert most < 1e-3 * abs(want)
+        assert abs(float(got[h]) - want) <= most, (h, float(got[h]), want, most)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[150], [700, 300], [1] * 15 + [700]], ids=["uncut", "cut", "many"])
+@pytest.mark.parametrize("initial", [False, True])
+def test_float32_states_of_bf16_work_hold_float32(lens, initial):
+    """A float32 state takes three bf16 terms of each decayed value, in the segments'
+    own sums too.  Its error in the 2-norm: about 200 additions that count (64 tokens
+    of a chunk, three terms) as a random walk, 14 u / sqrt(3), the exponents' 4 u and
+    the terms' 2^-24: below 2^-20.  Two terms would leave 2^-18.9."""
+    q, k, v, g, off, offs, gen = inputs(lens, 2, 4, 64, 64, torch.bfloat16, seed=23)
+    s0 = (0.3 * torch.randn((len(lens), 4, 64, 64), generator=gen)).cuda() if initial else None
+    _, end = gdr.gdr_linear_attention_fwd(q, k, v, g, offs, initial_state=s0,
+                                          output_final_state=True)
+    want = ref.attention(q, k, v, g, off, s0, 0.125)[1]
+    for r, n in enumerate(lens):
+        near(f"state of {n}", end[r], want[r], 2.0 ** -20)
+
+
+def spread(gen, *xs):
+    """Tokens of sizes from a hundredth to a hundred times the others'."""
+    for x in xs:
+        f = 10 ** (4 * torch.rand(x.shape[0], 1, 1, generator=gen) - 2)
+        x *= f.to(x.dtype).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("work", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[180], [600, 3, 70]], ids=["uncut", "cut"])
+def test_tokens_of_very_different_sizes(lens, work):
+    """Every output and gradient within the elementwise bounds of test_block_ops.py,
+    which follow the sizes of the terms."""
+    case = (lens, 1, 2, 64, 64, work, True, "token")
+    do, q, k, v, g, off, offs, s0, ds = bwd_inputs(case)
+    spread(torch.Generator().manual_seed(24), do, q, k, v)
+    s, n, sc = slice(off[0], off[-1]), max(lens), 0.4
+    o, end = gdr.gdr_linear_attention_fwd(q, k, v, g, offs, initial_state=s0, scale=sc,
+                                          output_final_state=True)
+    got = gdr.gdr_linear_attention_bwd(do, q, k, v, g, offs, initial_state=s0, dfinal_state=ds,
+                                       scale=sc)
+    mag = lambda *xs: [x.detach().cpu().double().abs() for x in xs]  # noqa: E731
+    want, wend = ref.attention(q, k, v, g, off, s0, sc)
+    A, Aend = ref.attention(*mag(q, k, v), g.cpu(), off, *mag(s0), sc)
+    f = bounds(DT[work], 64, n) + 2 * U32
+    close("o", o[s], want[s], A[s], f)
+    close("state", end, wend, Aend, f)
+    want = ref.attention_grads(do, q, k, v, g, off, s0, ds, sc)
+    A = ref.attention_grads(*mag(do, q, k, v), g.cpu(), off, *mag(s0, ds), sc, sign=1.0)
+    for name, x in zip(("dq", "dk", "dv", "dg"), got):
+        close(name, x[s], want[name][s], A[name][s], f + (64 * U32 if name == "dg" else 0))
+    close("ds0", got[4], want["ds0"], A["ds0"], f)
