@@ -374,7 +374,8 @@ def gdr_linear_attention_fwd(q, k, v, g, input_row_offsets, *, state=None, slot_
     decay per head) or None.  Returns (o, final state): the pool itself,
     updated in place at slot_idx, when `state` is given, else final_state
     (allocated here when output_final_state is set), else None.  o and the
-    workspace are allocated here with torch when not passed in."""
+    workspace are allocated here with torch when not passed in.  Tokens outside
+    the rows are not written: in an o allocated here they hold anything."""
     if o is None:
         o = _new(v, stream=stream)
     if state is None and output_final_state and final_state is None:
@@ -411,7 +412,8 @@ def gdr_linear_attention_bwd(do, q, k, v, g, input_row_offsets, *, initial_state
     dinitial_state None unless there is an initial_state (or
     need_dinitial_state is set).  dg has one entry per token and head; a decay
     that tokens share gets their sum.  Outputs and the workspace are allocated
-    here with torch when not passed in."""
+    here with torch when not passed in; tokens outside the rows are not written
+    (in outputs allocated here they hold anything)."""
     dq = _new(q, stream=stream) if dq is None else dq
     dk = _new(k, stream=stream) if dk is None else dk
     dv = _new(v, stream=stream) if dv is None else dv

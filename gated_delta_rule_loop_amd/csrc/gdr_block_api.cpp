@@ -131,7 +131,8 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     // Rows are walked chunk by chunk, so few (row, head) pairs leave most of the
     // 256 compute units idle: rows are cut into segments, whose own sums a first
     // pass takes and a scan turns into states, until about two workgroups a unit
-    // are walking (64 segments at most: the scan goes through a row's in turn).
+    // are walking (64 segments at most, as the scan goes through a row's in turn; a
+    // gradient's are 512 tokens long at most, however many that makes).
     // Measured at 16 value heads, K = V = 128, us uncut and in segments of 64
     // tokens: bf16 forward of 200 tokens 24 and 26, of 300 (by 256) 38 and 27,
     // float32 46 and 35, 82 and 37; the two more launches cost up to 5 us where

@@ -29,13 +29,15 @@
 // instructions throughout.  Decay exponents are summed in float64 and kept as
 // a pair of float32.
 //
-// Measured, 32 value heads, K = V = 128.  bf16, 32768 tokens in 16 segments: 375 us
-// (317 with one term everywhere), 260 of them the walk (544 MB: q, k, v once a
-// value head's share through the caches, the outputs), 110 the segments' sums.  Of the
-// walk's cycles the VALU issues in 53%, the LDS is busy in 49% and the matrix
-// instructions in 30%, at 16 waves a compute unit.  float32, 8336 tokens: 277 us, the
-// matrix instructions at half their rate.  Eight waves of 16 columns instead of
-// four of 32: 408 against 424 us, for twice the waves a SIMD.
+// Measured, 32 value heads, K = V = 128.  bf16, 32768 tokens in 16 segments: 367 us a
+// call (with one term everywhere 317, of 378 then).  By the kernel trace, which slows
+// the calls down, the walk takes 304 us on average and 255 at best (544 MB: q, k, v
+// once a value head's share through the caches, the outputs), the segments' sums 122
+// and 108, the scan 15.  Of the walk's cycles the VALU issues in 53%, the LDS is busy
+// in 49%, a third of that in bank conflicts, and the matrix instructions in 30%, at 16
+// waves a compute unit.  float32, 8336 tokens: 276 us, the matrix instructions at half
+// their rate.  Eight waves of 16 columns instead of four of 32: 408 against 424 us, for
+// twice the waves a SIMD.
 #include <type_traits>
 
 #include "gdr_linattn_dev.h"
@@ -56,8 +58,8 @@ template <> struct Mat<uint16_t> {
     enum { kTerms = 2, kVec = 8, kPad = 0 };  // kVec: elements per 16 bytes
     // Place of (row r0 + r, column c), r0 a multiple of 16, in a tile of rows
     // of S elements (64 at least).  The 16-byte slots of a row are permuted by
-    // the row's number, so that the lanes of a transposing read (16 at a time:
-    // 4 rows, 32 bytes each) do not meet in a bank.
+    // the row's number, to spread the lanes of a transposing read (16 at a time:
+    // 4 rows, 32 bytes each) over the banks.
     static __device__ __forceinline__ int at(int r0, int r, int c, int S) {
         // rows of 64 lie two to a round of the banks: the row's parity tells them apart
         const int h = S == 64 ? ((r >> 1 & 3) << 1 | r >> 3) : ((r & 7) << 1 | (r >> 3 & 1));
@@ -100,8 +102,8 @@ template <> struct Mat<uint16_t> {
     }
     // X is only read along its rows, 32 values a time: their order in LDS is that
     // of the state's registers (4 g + e, then 16 + 4 g + e), so that a lane reads
-    // them as 16 bytes.  Its slots are permuted so that 8 lanes of such a read
-    // do not meet in a bank.
+    // them as 16 bytes.  Its slots are permuted to spread 8 lanes of such a read
+    // over the banks.
     static __device__ __forceinline__ void put_x(uint16_t* p, int r, int c, int S, la_u4 v) {
         const int q = c >> 3 & 3;
         const int a = r * S + ((((c >> 5) * 4 + (q & 1) * 2) ^ (r & 7)) << 3) + (q >> 1) * 4;
