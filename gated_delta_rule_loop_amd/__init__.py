@@ -11,6 +11,9 @@ from ._binding import (  # noqa: F401
     gdr_block_norm_bwd,
     gdr_block_norm_workspace,
     gdr_causal_conv1d,
+    gdr_causal_conv1d_bwd,
+    gdr_causal_conv1d_fold,
+    gdr_causal_conv1d_workspace,
     gdr_check_indices,
     gdr_fused_recurrent_update,
     gdr_fwd_output_shape,
@@ -23,8 +26,15 @@ from ._binding import (  # noqa: F401
     gdr_recurrence_verify_ring,
     gdr_set_debug_checks,
     gdr_ring_record_elements,
+    gdr_selective_scan_bwd,
+    gdr_selective_scan_fold,
+    gdr_selective_scan_fwd,
+    gdr_selective_scan_step,
+    gdr_selective_scan_workspace,
     gdr_snapshot_rollback,
     gdr_state_fold,
+    gdr_verify_drafts,
+    gdr_verify_drafts_workspace,
     gdr_version,
     lib,
 )

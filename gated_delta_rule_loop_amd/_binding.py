@@ -25,6 +25,8 @@ GDR_FLAG_L2NORM_QK = 1
 GDR_FLAG_CONV_SILU = 2
 GDR_FLAG_GATE_SIGMOID = 4
 GDR_FLAG_GATE_SILU = 8
+GDR_FLAG_KEEP_STATE = 16
+GDR_FLAG_DT_SOFTPLUS = 32
 MAX_DIMS = 5
 
 _DTYPES = {torch.float32: GDR_DTYPE_F32, torch.bfloat16: GDR_DTYPE_BF16,
@@ -49,8 +51,13 @@ EXPORTS = ("gdr_recurrence_fwd", "gdr_recurrence_verify_ring", "gdr_state_fold",
            "gdr_fused_recurrent_update", "gdr_snapshot_rollback", "gdr_causal_conv1d",
            "gdr_fwd_output_shape", "gdr_check_indices", "gdr_set_debug_checks",
            "gdr_linear_attention_fwd", "gdr_linear_attention_step", "gdr_linear_attention_bwd",
-           "gdr_block_norm", "gdr_block_norm_bwd", "gdr_linear_attention_workspace",
-           "gdr_block_norm_workspace", "gdr_ring_record_elements", "gdr_last_error_message", "gdr_version")
+           "gdr_block_norm", "gdr_block_norm_bwd", "gdr_selective_scan_fwd",
+           "gdr_selective_scan_step", "gdr_selective_scan_fold", "gdr_selective_scan_bwd",
+           "gdr_causal_conv1d_fold", "gdr_causal_conv1d_bwd", "gdr_verify_drafts",
+           "gdr_linear_attention_workspace", "gdr_block_norm_workspace",
+           "gdr_selective_scan_workspace", "gdr_causal_conv1d_workspace",
+           "gdr_verify_drafts_workspace", "gdr_ring_record_elements", "gdr_last_error_message",
+           "gdr_version")
 
 
 def lib():
@@ -82,13 +89,24 @@ def lib():
         L.gdr_block_norm_bwd.argtypes = [vp] * 12 + [i64, f32, f32, u32, vp, vp]
         L.gdr_linear_attention_workspace.argtypes = [i64, i64, i32, i32, i32, i32, ctypes.c_int]
         L.gdr_block_norm_workspace.argtypes = [i64, i64]
-        for name in ("gdr_linear_attention_workspace", "gdr_block_norm_workspace"):
-            getattr(L, name).restype = i64
+        L.gdr_selective_scan_fwd.argtypes = [vp] * 14 + [u32, vp, vp]
+        L.gdr_selective_scan_step.argtypes = [vp] * 11 + [u32, vp]
+        L.gdr_selective_scan_fold.argtypes = [vp] * 9 + [u32, vp]
+        L.gdr_selective_scan_bwd.argtypes = [vp] * 21 + [u32, vp, vp]
+        L.gdr_causal_conv1d_fold.argtypes = [vp] * 6
+        L.gdr_causal_conv1d_bwd.argtypes = [vp] * 8 + [u32, vp, vp]
+        L.gdr_verify_drafts.argtypes = [vp] * 9
+        L.gdr_selective_scan_workspace.argtypes = [i64, i64, i64, i32, i32, ctypes.c_int]
+        L.gdr_causal_conv1d_workspace.argtypes = [i64, i64, i32]
+        L.gdr_verify_drafts_workspace.argtypes = [i64, i64, i64]
+        for name in EXPORTS:
+            if name.endswith("_workspace"):
+                getattr(L, name).restype = i64
         L.gdr_ring_record_elements.argtypes = [i32, i32, i32]
         L.gdr_ring_record_elements.restype = ctypes.c_int64
         L.gdr_last_error_message.restype = ctypes.c_char_p
         L.gdr_version.restype = ctypes.c_char_p
-        for name in EXPORTS[:14]:
+        for name in EXPORTS[:EXPORTS.index("gdr_linear_attention_workspace")]:
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -249,16 +267,17 @@ def gdr_snapshot_rollback(state, state_indices, intermediate_states, accepted, *
 
 
 def gdr_causal_conv1d(x, weight, input_row_offsets, *, bias=None, conv_state=None,
-                      slot_idx=None, silu=False, out=None, stream=None):
+                      slot_idx=None, silu=False, keep_state=False, out=None, stream=None):
     """Pass-1 causal depthwise Conv1d producing qkv_conv_output (page
     "gated_delta_recurrence_fwd_gpu", Args).  Returns out (allocated here with
     torch, x's dtype and shape, when not passed in); conv_state is updated in
-    place."""
+    place, or with keep_state left as it is (a window of drafted tokens, whose
+    accepted prefix gdr_causal_conv1d_fold takes afterwards)."""
     if out is None:
         out = _new(x, stream=stream)
     ds = [describe(t) for t in (out, x, weight, bias, conv_state, slot_idx, input_row_offsets)]
-    rc = lib().gdr_causal_conv1d(*[_ref(d) for d in ds], GDR_FLAG_CONV_SILU if silu else 0,
-                                 _stream(stream))
+    flags = (GDR_FLAG_CONV_SILU if silu else 0) | (GDR_FLAG_KEEP_STATE if keep_state else 0)
+    rc = lib().gdr_causal_conv1d(*[_ref(d) for d in ds], flags, _stream(stream))
     _check("gdr_causal_conv1d", rc)
     return out
 
@@ -491,6 +510,177 @@ def gdr_block_norm_bwd(dh, dn, y, h, *, post_weight=None, group=0, gate=None, ac
     _check("gdr_block_norm_bwd", rc)
     return (dx if dx is not None else dh) if residual else None, dgate, dy, dpost_weight, \
         dpre_weight
+
+
+# ------------------------------------------------- state-space layers, drafts ---
+
+def gdr_causal_conv1d_fold(conv_state, x, input_row_offsets, accepted, slot_idx=None, *,
+                           stream=None):
+    """Advance each row's history over the first accepted[b] inputs of its
+    window x (0, or more than the row has, leaves it alone).  Returns
+    conv_state, updated in place."""
+    r, _buf = _describe_all((conv_state, x, input_row_offsets, accepted, slot_idx))
+    rc = lib().gdr_causal_conv1d_fold(*r, _stream_of(stream, x))
+    _check("gdr_causal_conv1d_fold", rc)
+    return conv_state
+
+
+def gdr_causal_conv1d_workspace(tokens, channels, width):
+    """float32 elements of workspace that gdr_causal_conv1d_bwd needs."""
+    return int(lib().gdr_causal_conv1d_workspace(tokens, channels, width))
+
+
+def gdr_causal_conv1d_bwd(dout, x, weight, input_row_offsets, *, bias=None, silu=False, dx=None,
+                          dweight=None, dbias=None, workspace=None, stream=None):
+    """Gradients of gdr_causal_conv1d without conv_state.  Returns (dx, dweight,
+    dbias), dbias None without bias.  Outputs and the workspace are allocated
+    here with torch when not passed in; tokens outside the rows are not written
+    (in a dx allocated here they hold anything)."""
+    dx = _new(x, stream=stream) if dx is None else dx
+    dweight = _new(weight, stream=stream) if dweight is None else dweight
+    if bias is not None and dbias is None:
+        dbias = _new(bias, stream=stream)
+    ws = workspace
+    if ws is None:
+        ws = _scratch(lib().gdr_causal_conv1d_workspace(*x.shape, weight.shape[1]), x, stream)
+    r, _buf = _describe_all((dout, x, weight, bias, input_row_offsets, dx, dweight, dbias, ws))
+    rc = lib().gdr_causal_conv1d_bwd(*r[:8], GDR_FLAG_CONV_SILU if silu else 0, r[8],
+                                     _stream_of(stream, x))
+    _check("gdr_causal_conv1d_bwd", rc)
+    return dx, dweight, dbias
+
+
+def gdr_selective_scan_workspace(tokens, rows, channels, state_size, groups=1, backward=False):
+    """float32 elements of workspace that one call needs (0: none)."""
+    return int(lib().gdr_selective_scan_workspace(tokens, rows, channels, state_size, groups,
+                                                  1 if backward else 0))
+
+
+def _scan_scratch(x, B, offsets, backward, workspace, stream):
+    if workspace is not None:
+        return workspace
+    T, D = x.shape
+    n = lib().gdr_selective_scan_workspace(T, offsets.shape[0] - 1, D, B.shape[2], B.shape[1],
+                                           backward)
+    return _scratch(n, x, stream)
+
+
+def gdr_selective_scan_fwd(x, dt, A, B, C, input_row_offsets, *, D=None, z=None, dt_bias=None,
+                           softplus=False, state=None, slot_idx=None, keep_state=False,
+                           initial_state=None, final_state=None, output_final_state=False,
+                           out=None, workspace=None, stream=None):
+    """Selective state space scan over ragged prompts: with step sizes delta =
+    dt + dt_bias (softplus of it on request), h_t = exp(delta A) h_{t-1} +
+    delta x_t B_t, out_t = (C_t . h_t + D x_t) silu(z_t).
+
+    x, dt, z [T, D]; A [D, N]; B, C [T, G, N]; D, dt_bias [D].  Returns (out,
+    final state): the pool itself, updated in place at slot_idx (or with
+    keep_state left as it is: a window of drafted tokens, whose accepted prefix
+    gdr_selective_scan_fold takes afterwards), when `state` is given, else
+    final_state (allocated here when output_final_state is set), else None.
+    out and the workspace are allocated here with torch when not passed in.
+    Tokens outside the rows are not written: in an out allocated here they hold
+    anything."""
+    if out is None:
+        out = _new(x, stream=stream)
+    if state is None and output_final_state and final_state is None:
+        dt_ = initial_state.dtype if initial_state is not None else torch.float32
+        final_state = _new(x, (input_row_offsets.shape[0] - 1, *A.shape), dt_, stream)
+    ws = _scan_scratch(x, B, input_row_offsets, 0, workspace, stream)
+    flags = (GDR_FLAG_DT_SOFTPLUS if softplus else 0) | (GDR_FLAG_KEEP_STATE if keep_state else 0)
+    r, _buf = _describe_all((out, x, dt, A, B, C, D, z, dt_bias, input_row_offsets, initial_state,
+                             final_state, state, slot_idx, ws))
+    rc = lib().gdr_selective_scan_fwd(*r[:14], flags, r[14], _stream_of(stream, x))
+    _check("gdr_selective_scan_fwd", rc)
+    return out, (state if state is not None else final_state)
+
+
+def gdr_selective_scan_step(x, dt, A, B, C, state, slot_idx=None, *, D=None, z=None, dt_bias=None,
+                            softplus=False, out=None, stream=None):
+    """One token for each row (x, dt, z [rows, D]; B, C [rows, G, N]), with the
+    row's state updated in place in its slot.  Returns out."""
+    if out is None:
+        out = _new(x, stream=stream)
+    r, _buf = _describe_all((out, x, dt, A, B, C, D, z, dt_bias, state, slot_idx))
+    rc = lib().gdr_selective_scan_step(*r, GDR_FLAG_DT_SOFTPLUS if softplus else 0,
+                                       _stream_of(stream, x))
+    _check("gdr_selective_scan_step", rc)
+    return out
+
+
+def gdr_selective_scan_fold(state, x, dt, A, B, input_row_offsets, accepted, slot_idx=None, *,
+                            dt_bias=None, softplus=False, stream=None):
+    """Advance each row's state over the first accepted[b] tokens of its window
+    (0, or more than the row has, leaves it alone).  Returns state, updated in
+    place."""
+    r, _buf = _describe_all((state, x, dt, A, B, dt_bias, input_row_offsets, accepted, slot_idx))
+    rc = lib().gdr_selective_scan_fold(*r, GDR_FLAG_DT_SOFTPLUS if softplus else 0,
+                                       _stream_of(stream, x))
+    _check("gdr_selective_scan_fold", rc)
+    return state
+
+
+def gdr_selective_scan_bwd(dout, x, dt, A, B, C, input_row_offsets, *, D=None, z=None,
+                           dt_bias=None, softplus=False, initial_state=None, dfinal_state=None,
+                           need_dinitial_state=None, dx=None, ddt=None, dA=None, dB=None, dC=None,
+                           dD=None, dz=None, ddt_bias=None, dinitial_state=None, workspace=None,
+                           stream=None):
+    """Gradients of gdr_selective_scan_fwd (dense states).  Returns (dx, ddt,
+    dA, dB, dC, dD, dz, ddt_bias, dinitial_state), None for what the forward
+    did not have; dinitial_state None unless there is an initial_state (or
+    need_dinitial_state is set).  Outputs and the workspace are allocated here
+    with torch when not passed in; tokens outside the rows are not written (in
+    outputs allocated here they hold anything)."""
+    def like(t, given):
+        return _new(t, stream=stream) if given is None and t is not None else given
+
+    dx, ddt, dA, dB, dC = like(x, dx), like(dt, ddt), like(A, dA), like(B, dB), like(C, dC)
+    dD, dz, ddt_bias = like(D, dD), like(z, dz), like(dt_bias, ddt_bias)
+    if need_dinitial_state is None:
+        need_dinitial_state = initial_state is not None
+    if need_dinitial_state and dinitial_state is None:
+        of = initial_state if initial_state is not None else dfinal_state
+        dinitial_state = _new(x, (input_row_offsets.shape[0] - 1, *A.shape),
+                              of.dtype if of is not None else torch.float32, stream)
+    ws = _scan_scratch(x, B, input_row_offsets, 1, workspace, stream)
+    r, _buf = _describe_all((dout, x, dt, A, B, C, D, z, dt_bias, input_row_offsets, initial_state,
+                             dfinal_state, dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinitial_state,
+                             ws))
+    rc = lib().gdr_selective_scan_bwd(*r[:21], GDR_FLAG_DT_SOFTPLUS if softplus else 0, r[21],
+                                      _stream_of(stream, x))
+    _check("gdr_selective_scan_bwd", rc)
+    return dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dinitial_state
+
+
+def gdr_verify_drafts_workspace(tokens, rows, vocab):
+    """float32 elements of workspace that gdr_verify_drafts needs."""
+    return int(lib().gdr_verify_drafts_workspace(tokens, rows, vocab))
+
+
+def gdr_verify_drafts(tokens, target, input_row_offsets, *, draft=None, uniform=None,
+                      accepted=None, next_token=None, workspace=None, stream=None):
+    """Judge drafted tokens: a row's window (tokens [T], int32) holds a certain
+    token and then the drafts; target [T, V] says what follows each, draft
+    [T, V] what each draft was drawn from (None: drafts without probabilities),
+    uniform [T] float32 holds a random number for each draft and, at the row's
+    first token, the one that draws the next token.  Without uniform: greedily.
+    Returns (accepted, next_token), int32 [rows]: the window's tokens that
+    stand, the certain one among them, as the folds and the rollback take
+    them, and the token that each row goes on with."""
+    rows = input_row_offsets.shape[0] - 1
+    if accepted is None:
+        accepted = _new(tokens, (rows,), torch.int32, stream)
+    if next_token is None:
+        next_token = _new(tokens, (rows,), torch.int32, stream)
+    ws = workspace
+    if ws is None:
+        n = lib().gdr_verify_drafts_workspace(tokens.shape[0], rows, target.shape[1])
+        ws = _scratch(n, tokens, stream)
+    r, _buf = _describe_all((accepted, next_token, tokens, target, draft, uniform,
+                             input_row_offsets, ws))
+    rc = lib().gdr_verify_drafts(*r, _stream_of(stream, tokens))
+    _check("gdr_verify_drafts", rc)
+    return accepted, next_token
 
 
 def gdr_ring_record_elements(group, key_head_dim, value_head_dim):

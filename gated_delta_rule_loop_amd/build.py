@@ -22,7 +22,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdr.so")
 SOURCES = [os.path.join(CSRC, "gdr_api.cpp"), os.path.join(CSRC, "gdr_kernels.hip"),
            os.path.join(CSRC, "gdr_conv.hip"), os.path.join(CSRC, "gdr_block_api.cpp"),
-           os.path.join(CSRC, "gdr_linattn.hip"), os.path.join(CSRC, "gdr_norm.hip")]
+           os.path.join(CSRC, "gdr_linattn.hip"), os.path.join(CSRC, "gdr_norm.hip"),
+           os.path.join(CSRC, "gdr_scan_api.cpp"), os.path.join(CSRC, "gdr_scan.hip"),
+           os.path.join(CSRC, "gdr_scan_bwd.hip"), os.path.join(CSRC, "gdr_conv_bwd.hip"),
+           os.path.join(CSRC, "gdr_drafts.hip")]
 TABLE_SOURCE = os.path.join(CSRC, "gdr_rec_table.hip")
 # (work type, state storage type, kernel mode) of each recurrence table:
 # types float or uint16_t (bf16 bits); modes kPlain 0, kVerify 1, kSnap 2,

@@ -827,7 +827,7 @@ int gdr_causal_conv1d(const gdr_tensor* out, const gdr_tensor* x, const gdr_tens
                       uint32_t flags, void* stream) {
     const char* fn = "gdr_causal_conv1d";
     int rc;
-    if (flags & ~GDR_FLAG_CONV_SILU)
+    if (flags & ~(GDR_FLAG_CONV_SILU | GDR_FLAG_KEEP_STATE))
         return fail(GDR_ERR_INVALID_ARG, "%s: unknown flags 0x%x", fn, flags);
     if ((rc = check_tensor(fn, "x", x, 2, nullptr, true, true, false))) return rc;
     const int32_t work = x->dtype;
@@ -883,6 +883,7 @@ int gdr_causal_conv1d(const gdr_tensor* out, const gdr_tensor* x, const gdr_tens
     p.T = static_cast<int32_t>(T);
     p.W = static_cast<int32_t>(W);
     p.silu = (flags & GDR_FLAG_CONV_SILU) ? 1 : 0;
+    p.keep = (flags & GDR_FLAG_KEEP_STATE) ? 1 : 0;
     p.offsets = as_u32(input_row_offsets);
     p.slot_idx = as_u32(slot_idx);
     p.x = x->data;

@@ -9,30 +9,9 @@
 #include "gdr_linattn.h"
 #include "gdr_norm.h"
 
-using namespace gdr;
-
-namespace {
+namespace gdr {
 
 typedef long long ll;
-
-constexpr int64_t kLaMaxTokenStride = (int64_t{1} << 24) - 1;
-
-// [tokens, heads, dim] operand: unit innermost stride, 16-byte rows.  `walked`:
-// the walks read it, which address a chunk's tokens from one 64-bit base by
-// unsigned 32-bit offsets.
-int check_heads(const char* fn, const char* name, const gdr_tensor* t, int64_t T, int64_t heads,
-                int64_t dim, int32_t work, bool walked) {
-    const int64_t shape[3] = {T, heads, dim};
-    int rc = check_tensor(fn, name, t, 3, shape, true, true, false);
-    if (rc || (rc = check_work_dtype(fn, name, t, work))) return rc;
-    if ((rc = check_layout(fn, name, t, vec_mult(work)))) return rc;
-    if (T > 1 && heads > 0 && walked && t->stride[0] < 0)
-        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a negative token stride", fn, name);
-    if (T > 1 && heads > 0 && std::llabs(t->stride[0]) > kLaMaxTokenStride)
-        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a token stride above %lld elements", fn, name,
-                    static_cast<ll>(kLaMaxTokenStride));
-    return GDR_OK;
-}
 
 // Outputs are written by many workgroups: no two elements may share memory.
 int check_distinct(const char* fn, const char* name, const gdr_tensor* t) {
@@ -52,6 +31,71 @@ int check_distinct(const char* fn, const char* name, const gdr_tensor* t) {
                         name);
         need = t->stride[at] * (t->shape[at] - 1) + need;
     }
+    return GDR_OK;
+}
+
+int check_workspace(const char* fn, const gdr_tensor* ws, int64_t need) {
+    if (need == 0) return GDR_OK;
+    if (!present(ws))
+        return fail(GDR_ERR_INVALID_ARG, "%s: workspace is null (%lld floats needed, see "
+                    "the gdr_..._workspace functions)", fn,
+                    static_cast<ll>(need));
+    if (ws->ndim != 1 || ws->dtype != GDR_DTYPE_F32)
+        return fail(GDR_ERR_INVALID_ARG, "%s: workspace must be a float32 vector", fn);
+    if (ws->shape[0] < need)
+        return fail(GDR_ERR_INVALID_ARG, "%s: workspace has %lld floats, %lld needed", fn,
+                    static_cast<ll>(ws->shape[0]), static_cast<ll>(need));
+    if (ws->shape[0] > 1 && ws->stride[0] != 1)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: workspace must be contiguous", fn);
+    if (!aligned16(ws->data))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: workspace base must be 16-byte aligned", fn);
+    return GDR_OK;
+}
+
+// A launch holds fewer than 2^32 threads in a dimension.  Every launch of a call is
+// checked before the first, which may already change states.
+int check_grid(const char* fn, int64_t blocks, int64_t threads) {
+    if (blocks > UINT32_MAX / threads)
+        return fail(GDR_ERR_INVALID_ARG, "%s: batch too large for one launch", fn);
+    return GDR_OK;
+}
+
+int no_alias(const char* fn, const gdr_tensor* out, const char* name,
+             std::initializer_list<const gdr_tensor*> ins) {
+    if (empty(out)) return GDR_OK;
+    for (const gdr_tensor* t : ins)
+        if (present(t) && t->data == out->data)
+            return fail(GDR_ERR_INVALID_ARG, "%s: %s must not alias an input", fn, name);
+    return GDR_OK;
+}
+
+int done() {
+    clear_error();
+    return GDR_OK;
+}
+
+}  // namespace gdr
+
+using namespace gdr;
+
+namespace {
+
+constexpr int64_t kLaMaxTokenStride = (int64_t{1} << 24) - 1;
+
+// [tokens, heads, dim] operand: unit innermost stride, 16-byte rows.  `walked`:
+// the walks read it, which address a chunk's tokens from one 64-bit base by
+// unsigned 32-bit offsets.
+int check_heads(const char* fn, const char* name, const gdr_tensor* t, int64_t T, int64_t heads,
+                int64_t dim, int32_t work, bool walked) {
+    const int64_t shape[3] = {T, heads, dim};
+    int rc = check_tensor(fn, name, t, 3, shape, true, true, false);
+    if (rc || (rc = check_work_dtype(fn, name, t, work))) return rc;
+    if ((rc = check_layout(fn, name, t, vec_mult(work)))) return rc;
+    if (T > 1 && heads > 0 && walked && t->stride[0] < 0)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a negative token stride", fn, name);
+    if (T > 1 && heads > 0 && std::llabs(t->stride[0]) > kLaMaxTokenStride)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a token stride above %lld elements", fn, name,
+                    static_cast<ll>(kLaMaxTokenStride));
     return GDR_OK;
 }
 
@@ -183,24 +227,6 @@ LaPlan la_plan(int64_t T, int64_t B, int64_t nk, int64_t nv, int64_t K, int64_t 
     return p;
 }
 
-int check_workspace(const char* fn, const gdr_tensor* ws, int64_t need) {
-    if (need == 0) return GDR_OK;
-    if (!present(ws))
-        return fail(GDR_ERR_INVALID_ARG, "%s: workspace is null (%lld floats needed, see "
-                    "gdr_linear_attention_workspace and gdr_block_norm_workspace)", fn,
-                    static_cast<ll>(need));
-    if (ws->ndim != 1 || ws->dtype != GDR_DTYPE_F32)
-        return fail(GDR_ERR_INVALID_ARG, "%s: workspace must be a float32 vector", fn);
-    if (ws->shape[0] < need)
-        return fail(GDR_ERR_INVALID_ARG, "%s: workspace has %lld floats, %lld needed", fn,
-                    static_cast<ll>(ws->shape[0]), static_cast<ll>(need));
-    if (ws->shape[0] > 1 && ws->stride[0] != 1)
-        return fail(GDR_ERR_UNSUPPORTED, "%s: workspace must be contiguous", fn);
-    if (!aligned16(ws->data))
-        return fail(GDR_ERR_UNSUPPORTED, "%s: workspace base must be 16-byte aligned", fn);
-    return GDR_OK;
-}
-
 // The sizes that the linear-attention entries share, from q, k, v, g.
 struct LaDims {
     int64_t T, nk, nv, K, V, B;
@@ -241,14 +267,6 @@ int check_offsets(const char* fn, const gdr_tensor* off, LaDims& d) {
     d.B = off->shape[0] - 1;
     if (d.B < 0) return fail(GDR_ERR_INVALID_ARG, "%s: input_row_offsets is empty", fn);
     return check_index_vec(fn, "input_row_offsets", off, d.B + 1);
-}
-
-// A launch holds fewer than 2^32 threads in a dimension.  Every launch of a call is
-// checked before the first, which may already change states.
-int check_grid(const char* fn, int64_t blocks, int64_t threads) {
-    if (blocks > UINT32_MAX / threads)
-        return fail(GDR_ERR_INVALID_ARG, "%s: batch too large for one launch", fn);
-    return GDR_OK;
 }
 
 int check_scan(const char* fn, const LaDims& d, int64_t rows) {
@@ -348,20 +366,6 @@ hipError_t run_step(const LaDims& d, const gdr_tensor* o, const gdr_tensor* q, c
     p.most = kLaStepTokens;
     p.scale = scale;
     return launch_la_step(p, d.work == GDR_DTYPE_BF16, s);
-}
-
-int no_alias(const char* fn, const gdr_tensor* out, const char* name,
-             std::initializer_list<const gdr_tensor*> ins) {
-    if (empty(out)) return GDR_OK;
-    for (const gdr_tensor* t : ins)
-        if (present(t) && t->data == out->data)
-            return fail(GDR_ERR_INVALID_ARG, "%s: %s must not alias an input", fn, name);
-    return GDR_OK;
-}
-
-int done() {
-    clear_error();
-    return GDR_OK;
 }
 
 }  // namespace

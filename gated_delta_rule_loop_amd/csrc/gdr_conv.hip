@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_out_kernel(const ConvParams
         // A one-token row's history was read by this thread alone, so it
         // writes the new one (the slid window) here and conv_state_kernel
         // skips the row.
-        if (t1 - t0 == 1 && p.state && !pad) {
+        if (t1 - t0 == 1 && p.state && !pad && !p.keep) {
             WT* st = static_cast<WT*>(p.state) + static_cast<int64_t>(slot) * p.st_slot + c0;
 #pragma unroll
             for (int k = 0; k < H; ++k) store4(st + static_cast<int64_t>(k) * p.st_tok, win[k]);
@@ -197,7 +197,7 @@ hipError_t launch_conv_w(const ConvParams& p, hipStream_t stream) {
         hipLaunchKernelGGL((conv_out_kernel<W, WT, 1>), grid, dim3(kConvThreads), 0, stream, p);
     }
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.state) return e;
+    if (e != hipSuccess || !p.state || p.keep) return e;
     hipLaunchKernelGGL((conv_state_kernel<W, WT>), dim3(cblocks, p.B), dim3(kConvThreads), 0,
                        stream, p);
     return hipGetLastError();

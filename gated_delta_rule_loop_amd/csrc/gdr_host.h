@@ -1,10 +1,12 @@
 // Host helpers that every C entry point shares: the thread's error message,
 // checks of tensor descriptors, the optional index checks.  Defined in
-// gdr_api.cpp.  Not part of the public ABI.
+// gdr_api.cpp where nothing else is said.  Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <initializer_list>
 
 #include "gdr.h"
 
@@ -43,5 +45,13 @@ int run_debug_check(const char* fn, int64_t rows, const IndexCheck& c, void* str
 float resolve_scale(float scale, int64_t K);
 int hip_status(const char* fn, hipError_t e);
 const uint32_t* as_u32(const gdr_tensor* t);
+
+// Defined in gdr_block_api.cpp.
+int check_distinct(const char* fn, const char* name, const gdr_tensor* t);
+int check_workspace(const char* fn, const gdr_tensor* ws, int64_t need);
+int check_grid(const char* fn, int64_t blocks, int64_t threads);
+int no_alias(const char* fn, const gdr_tensor* out, const char* name,
+             std::initializer_list<const gdr_tensor*> ins);
+int done();
 
 }  // namespace gdr

@@ -79,7 +79,7 @@ struct RollbackParams {
 // Pass-1 causal depthwise Conv1d over ragged rows (strides in elements).
 struct ConvParams {
     int32_t B, C, T, W;
-    int32_t silu;
+    int32_t silu, keep;         // keep: the history is read and not written
     const uint32_t* offsets;    // [B+1]
     const uint32_t* slot_idx;   // [B] or nullptr (slot = row); kPadSlot pads
     const void* x; int64_t x_tok;       // [T, C], work type

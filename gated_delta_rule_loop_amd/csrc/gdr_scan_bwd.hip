@@ -1,0 +1,504 @@
+// gfx950 kernels of the selective scan's gradient.  With dy = dout silu(z):
+//     lam_t = dy_t C_t + a_{t+1} lam_{t+1}      w_t = lam_t a_t h_{t-1}
+//     dx = skip dy + delta sum_n lam B          ddelta = x sum_n lam B + sum_n A w
+//     dA = sum_t delta w     dB = sum_d lam delta x     dC = sum_d dy h
+//     dz = dout y silu'(z)   ddt = ddelta softplus'     dskip = sum dy x
+// The states h run forward and lam backward, and neither is kept by the forward.
+// Rows are cut into segments and segments into parts of kPart tokens:
+//   1. every segment walks forward from a zero state and leaves its state before
+//      each part, its end state, the sums of its step sizes, and what its tokens'
+//      dy C hand to its past (decayed from where each stands: a running product);
+//   2. both chains over a row's segments give the state that each starts from and
+//      the gradient that reaches its end;
+//   3. every segment goes through its parts from the last, one state n at a time:
+//      16 tokens' decays and states forward into registers (the part's local
+//      state plus what is left of the segment's start), then backward.  A lane
+//      owns a channel; dB and dC, sums over channels, are reduced over the wave by
+//      halving: 32 values in 64 lanes take 70 instructions, not 6 each;
+//   4. the parts of dB, dC (over channels), dA, dskip and dt_bias's gradient (over
+//      segments) are added in a fixed order.
+// Everything is float32; sums over segments are float64.  Bound by the vector
+// units: about 26 slots a token, channel and state.
+#include "gdr_scan_dev.h"
+
+namespace gdr {
+namespace {
+
+#define GDR_UNIFORM __attribute__((address_space(4)))
+
+constexpr int kPart = kScanPart;
+// Waves of a gradient's workgroup: carried sums of every state take 512 bytes of
+// LDS a wave and state, so that 64 states leave room for two.
+constexpr int grad_waves(int N) { return N > 32 ? 2 : 4; }
+// States that one workgroup of the first launch carries.
+constexpr int sum_states(int N) { return N < 16 ? N : 16; }
+
+template <typename WT, int N>
+__device__ __forceinline__ void uniform_row(const void* base, int64_t elem, float (&v)[N]) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(elem) * sizeof(WT);
+    const GDR_UNIFORM uint32_t* q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(at);
+    if constexpr (sizeof(WT) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(q[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const uint32_t w = q[i];
+            v[2 * i] = __uint_as_float(w << 16);
+            v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+    }
+}
+
+// The number of a segment's first part (segments are whole parts but for a row's last).
+__device__ __forceinline__ int64_t first_part(const ScanParams& p, const ScanSpan& o) {
+    return scan_first_seg(p.offsets[o.row], o.row, kPart) + static_cast<int64_t>(o.s) * (p.seg_len / kPart);
+}
+
+// ------------------------------------------------------------ 1: own sums ---
+
+// N: the states of this workgroup, of the channels' p.N.
+template <typename WT, int N>
+__global__ void __launch_bounds__(kScanThreads) grad_sums(const ScanParams p, const ScanGrad q) {
+    const int ctiles = p.G * p.tiles;
+    const int block = blockIdx.x / ctiles, tile = blockIdx.x - block * ctiles;
+    const int nblocks = p.N / N, seg = block / nblocks, n0 = (block - seg * nblocks) * N;
+    ScanSpan o;
+    if (!scan_locate(p, seg, o)) return;
+    const bool ends = o.s < o.count - 1, rev = o.s > 0;
+    if (o.n <= kPart && !ends && !rev) return;
+    const int g = tile / p.tiles;
+    const int cg = (tile - g * p.tiles) * kScanThreads + static_cast<int>(threadIdx.x);
+    const bool live = cg < p.gd;
+    const int d = g * p.gd + min(cg, p.gd - 1);
+    const int64_t DN = static_cast<int64_t>(p.D) * p.N;
+    float h[N], a2[N], P[N], R[N];
+    scan_load<N>(p.A + static_cast<int64_t>(d) * p.N + n0, a2);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        a2[i] *= kScanLog2e;
+        h[i] = 0.0f;
+        P[i] = 1.0f;
+        R[i] = 0.0f;
+    }
+    const float bias = p.bias ? p.bias[d] : 0.0f;
+    const WT* x = static_cast<const WT*>(p.x.p) + static_cast<int64_t>(o.t0) * p.x.tok;
+    const WT* dt = static_cast<const WT*>(p.dt.p) + static_cast<int64_t>(o.t0) * p.dt.tok;
+    const WT* d_o = static_cast<const WT*>(q.d_o.p) + static_cast<int64_t>(o.t0) * q.d_o.tok;
+    const bool gated = p.z.p != nullptr;
+    const WT* z = gated ? static_cast<const WT*>(p.z.p) + static_cast<int64_t>(o.t0) * p.z.tok : d_o;
+    const int64_t z_tok = gated ? p.z.tok : q.d_o.tok;
+    const int64_t b0 = static_cast<int64_t>(o.t0) * p.b.tok + static_cast<int64_t>(g) * p.b.grp + n0;
+    const int64_t c0 = static_cast<int64_t>(o.t0) * p.c.tok + static_cast<int64_t>(g) * p.c.grp + n0;
+    float* check = q.check + first_part(p, o) * (DN + p.D) + d;
+    float total = 0.0f;
+    constexpr int U = 4;
+    WT xs[U], ds[U], os[U], zs[U];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t u = min(t + i, o.n - 1);
+            xs[i] = (x + u * p.x.tok)[d];
+            ds[i] = (dt + u * p.dt.tok)[d];
+            if (rev) {
+                os[i] = (d_o + u * q.d_o.tok)[d];
+                zs[i] = (z + u * z_tok)[d];
+            }
+        }
+    };
+    fetch(0);
+    for (int t = 0; t < o.n; t += U) {
+        WT xc[U], dc[U], oc[U], zc[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            xc[i] = xs[i];
+            dc[i] = ds[i];
+            oc[i] = os[i];
+            zc[i] = zs[i];
+        }
+        if (t + U < o.n) fetch(t + U);
+        if (t % kPart == 0 && t && live) {  // the state before part t / kPart
+            float* at = check + (t / kPart) * (DN + p.D);
+#pragma unroll
+            for (int i = 0; i < N; ++i) at[static_cast<int64_t>(n0 + i) * p.D] = h[i];
+            if (n0 == 0) at[DN] = total;
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (t + i >= o.n) break;
+            float delta = scan_value(dc[i]) + bias;
+            if (p.softplus) delta = scan_softplus(delta);
+            const float u = delta * scan_value(xc[i]);
+            total += delta;
+            float b[N];
+            uniform_row<WT, N>(p.b.p, b0 + (t + i) * p.b.tok, b);
+            if (rev) {
+                float c[N], dy = scan_value(oc[i]);
+                uniform_row<WT, N>(p.c.p, c0 + (t + i) * p.c.tok, c);
+                if (gated) {
+                    const float zv = scan_value(zc[i]);
+                    dy *= zv * scan_sigmoid(zv);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const float a = __builtin_amdgcn_exp2f(delta * a2[k]);
+                    h[k] = __builtin_fmaf(a, h[k], u * b[k]);
+                    P[k] *= a;
+                    R[k] = __builtin_fmaf(P[k], dy * c[k], R[k]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < N; ++k)
+                    h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[k]), h[k], u * b[k]);
+            }
+        }
+    }
+    if (!live) return;
+    const int64_t mine = static_cast<int64_t>(seg) * DN + static_cast<int64_t>(n0) * p.D + d;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (ends) p.seg_state[mine + static_cast<int64_t>(k) * p.D] = h[k];
+        if (rev) q.seg_rev[mine + static_cast<int64_t>(k) * p.D] = R[k];
+    }
+    if (n0 == 0) p.seg_delta[static_cast<int64_t>(seg) * p.D + d] = total;
+}
+
+// --------------------------------------------------------------- 2: chains ---
+
+__device__ __forceinline__ float state_at(const ScanState& s, int64_t outer, int64_t i) {
+    if (!s.p) return 0.0f;
+    const int64_t j = outer * s.outer + i;
+    return s.bf16 ? scan_widen(static_cast<const uint16_t*>(s.p)[j])
+                  : static_cast<const float*>(s.p)[j];
+}
+
+__global__ void __launch_bounds__(256) grad_chains(const ScanParams p, const ScanGrad q) {
+    const int64_t DN = static_cast<int64_t>(p.D) * p.N;
+    const int blocks = static_cast<int>((DN + 255) / 256);
+    const int job = blockIdx.x / blocks, row = job >> 1;
+    const bool back = job & 1;
+    const int64_t i = static_cast<int64_t>(blockIdx.x - job * blocks) * 256 + threadIdx.x;
+    const uint32_t a = p.offsets[row];
+    const int n = static_cast<int>(p.offsets[row + 1] - a);
+    if (i >= DN || n <= p.seg_len) return;
+    const int count = (n + p.seg_len - 1) / p.seg_len;
+    const int64_t first = scan_first_seg(a, row, p.seg_len);
+    const int k = static_cast<int>(i / p.D), d = static_cast<int>(i - static_cast<int64_t>(k) * p.D);
+    const int64_t in_slot = static_cast<int64_t>(d) * p.N + k;
+    const float a2 = p.A[in_slot] * kScanLog2e;
+    float v = state_at(back ? q.dfinal : p.in, row, in_slot);
+    float* st = (back ? q.seg_rev : p.seg_state) + first * DN + i;
+    const float* dl = p.seg_delta + first * p.D + d;
+    constexpr int U = 8;
+    for (int j0 = 0; j0 < count; j0 += U) {
+        float e[U], s[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (j0 + j < count - 1) {
+                const int64_t at = back ? count - 1 - (j0 + j) : j0 + j;
+                e[j] = st[at * DN];
+                s[j] = dl[at * p.D];
+            }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (j0 + j < count) {
+                const int64_t at = back ? count - 1 - (j0 + j) : j0 + j;
+                st[at * DN] = v;
+                if (j0 + j < count - 1)
+                    v = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * s[j]), v, e[j]);
+            }
+    }
+}
+
+// ------------------------------------------------------------- 3: gradients ---
+
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)),
+                                                       CTRL, 0xf, 0xf, false));
+}
+// What a lane and its partner (named by CTRL) hold of x and y, added: x's in the
+// lanes where `up` is false, y's in their partners.
+template <int CTRL> __device__ __forceinline__ float halve(bool up, float x, float y) {
+    return (up ? y : x) + dpp<CTRL>(up ? x : y);
+}
+
+// Sums over the wave of x[0..15] and y[0..15]: lane l gets that of x[(l / 2) % 16]
+// below 32 and of y[...] from there on.
+__device__ __forceinline__ float sums32(float (&x)[16], float (&y)[16]) {
+    const int lane = threadIdx.x & 63;
+    float r[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[i]), __float_as_uint(y[i]),
+                                                        false, false);
+        r[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[i]),
+                                                        __float_as_uint(r[i + 8]), false, false);
+        r[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = halve<0x128>(lane & 8, r[i], r[i + 4]);  // 8 lanes round
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r[i] = halve<0x141>(lane & 4, r[i], r[i + 2]);  // mirrored in 8
+    r[0] = halve<0x4E>(lane & 2, r[0], r[1]);
+    return r[0] + dpp<0xB1>(r[0]);
+}
+
+template <typename WT, int N>
+__global__ void __launch_bounds__(64 * grad_waves(N))
+grad_walk(const ScanParams p, const ScanGrad q) {
+    constexpr int kGradWaves = grad_waves(N), kGradThreads = 64 * kGradWaves;
+    __shared__ __attribute__((aligned(16))) float bs[N][kPart], cs[N][kPart];
+    __shared__ float carry[kGradWaves][N][64], da[kGradWaves][N][64];
+    __shared__ float red[kGradWaves][N][2 * kPart];
+    const int gtiles = q.tiles, ctiles = p.G * gtiles;
+    const int seg = blockIdx.x / ctiles, tile = blockIdx.x - seg * ctiles;
+    const int g = tile / gtiles, gt = tile - g * gtiles;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int cg = gt * kGradThreads + tid;
+    const bool live = cg < p.gd;
+    const int d = g * p.gd + min(cg, p.gd - 1);
+    const int64_t DN = static_cast<int64_t>(p.D) * p.N;
+    const int64_t mine = static_cast<int64_t>(seg) * DN + d;
+    float* part_a = q.part_a + mine;
+    float* part_d = q.part_d + static_cast<int64_t>(seg) * 2 * p.D + d;
+    ScanSpan o;
+    if (!scan_locate(p, seg, o)) {
+        if (live) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) part_a[static_cast<int64_t>(n) * p.D] = 0.0f;
+            part_d[0] = 0.0f;
+            part_d[p.D] = 0.0f;
+        }
+        return;
+    }
+    const bool cut = o.count > 1;
+    for (int n = 0; n < N; ++n) {
+        carry[wave][n][lane] = cut ? q.seg_rev[mine + static_cast<int64_t>(n) * p.D]
+                                   : state_at(q.dfinal, o.row, static_cast<int64_t>(d) * N + n);
+        da[wave][n][lane] = 0.0f;
+    }
+    const float bias = p.bias ? p.bias[d] : 0.0f;
+    const float skip = p.skip ? p.skip[d] : 0.0f;
+    const bool gated = p.z.p != nullptr;
+    float dskip = 0.0f, dbias = 0.0f;
+    const float* check = q.check + first_part(p, o) * (DN + p.D) + d;
+    const WT* xp = static_cast<const WT*>(p.x.p) + d;
+    const WT* dtp = static_cast<const WT*>(p.dt.p) + d;
+    const WT* dop = static_cast<const WT*>(q.d_o.p) + d;
+    const WT* zp = static_cast<const WT*>(p.z.p) + d;
+    WT* dx = static_cast<WT*>(const_cast<void*>(q.dx.p)) + d;
+    WT* ddt = static_cast<WT*>(const_cast<void*>(q.ddt.p)) + d;
+    WT* dz = static_cast<WT*>(const_cast<void*>(q.dz.p)) + d;
+    auto put = [](float v) {
+        if constexpr (sizeof(WT) == 2) return scan_round(v);
+        else return v;
+    };
+    for (int part = (o.n - 1) / kPart; o.n > 0 && part >= 0; --part) {
+        const int64_t t0 = o.t0 + part * kPart;
+        const int m = min(kPart, o.n - part * kPart);
+        __syncthreads();  // the part before has been read
+        for (int i = tid; i < N * kPart; i += kGradThreads) {
+            const int k = i % N, t = i / N;
+            const int64_t at = t0 + min(t, m - 1);
+            bs[k][t] = scan_value(static_cast<const WT*>(p.b.p)[at * p.b.tok + g * p.b.grp + k]);
+            cs[k][t] = scan_value(static_cast<const WT*>(p.c.p)[at * p.c.tok + g * p.c.grp + k]);
+        }
+        float delta[kPart], u[kPart], dy[kPart], s1[kPart], s2[kPart], y[kPart];
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {  // tokens past the row's end: no step, no gradient
+            const int64_t at = t0 + min(i, m - 1);
+            float dl = scan_value(dtp[at * p.dt.tok]) + bias;
+            if (p.softplus) dl = scan_softplus(dl);
+            float gy = scan_value(dop[at * q.d_o.tok]);
+            if (gated) {
+                const float zv = scan_value(zp[at * p.z.tok]);
+                gy *= zv * scan_sigmoid(zv);
+            }
+            delta[i] = i < m ? dl : 0.0f;
+            dy[i] = i < m && live ? gy : 0.0f;
+            u[i] = i < m && live ? dl * scan_value(xp[at * p.x.tok]) : 0.0f;
+            s1[i] = s2[i] = y[i] = 0.0f;
+        }
+        const float* ck = check + part * (DN + p.D);
+        const float since = part ? ck[DN] : 0.0f;  // step sizes from the segment's start
+        __syncthreads();
+        for (int n = 0; n < N; ++n) {
+            const int64_t nd = static_cast<int64_t>(n) * p.D;
+            const float an = p.A[static_cast<int64_t>(d) * N + n], a2 = an * kScanLog2e;
+            float start = cut ? p.seg_state[mine + nd]
+                              : state_at(p.in, o.row, static_cast<int64_t>(d) * N + n);
+            if (part) start = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * since), start, ck[nd]);
+            float a[kPart], h[kPart], hp = start;
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+                a[i] = __builtin_amdgcn_exp2f(delta[i] * a2);
+                h[i] = __builtin_fmaf(a[i], hp, u[i] * bs[n][i]);
+                hp = h[i];
+                if (gated) y[i] = __builtin_fmaf(cs[n][i], h[i], y[i]);
+            }
+            float mu = carry[wave][n][lane], ga = 0.0f;
+#pragma unroll
+            for (int i = kPart - 1; i >= 0; --i) {
+                const float lam = __builtin_fmaf(dy[i], cs[n][i], mu);
+                s1[i] = __builtin_fmaf(lam, bs[n][i], s1[i]);
+                mu = a[i] * lam;
+                const float w = mu * (i ? h[i - 1] : start);
+                s2[i] = __builtin_fmaf(an, w, s2[i]);
+                ga = __builtin_fmaf(delta[i], w, ga);
+                a[i] = lam * u[i];
+                h[i] = dy[i] * h[i];
+            }
+            carry[wave][n][lane] = mu;
+            da[wave][n][lane] += ga;
+            const float sum = sums32(a, h);
+            if (!(lane & 1)) red[wave][n][lane >> 1] = sum;
+        }
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+            if (i < m) {
+                const int64_t at = t0 + i;
+                const float xv = scan_value(xp[at * p.x.tok]);
+                float dd = __builtin_fmaf(xv, s1[i], s2[i]);
+                if (p.softplus) dd *= scan_sigmoid(scan_value(dtp[at * p.dt.tok]) + bias);
+                dbias += dd;
+                dskip = __builtin_fmaf(dy[i], xv, dskip);
+                if (live) {
+                    dx[at * q.dx.tok] = put(__builtin_fmaf(skip, dy[i], delta[i] * s1[i]));
+                    ddt[at * q.ddt.tok] = put(dd);
+                    if (gated) {
+                        const float zv = scan_value(zp[at * p.z.tok]), sig = scan_sigmoid(zv);
+                        const float yv = __builtin_fmaf(skip, xv, y[i]);
+                        dz[at * q.dz.tok] = put(scan_value(dop[at * q.d_o.tok]) * yv *
+                                                (sig * __builtin_fmaf(zv, 1.0f - sig, 1.0f)));
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < 2 * kPart * N; i += kGradThreads) {
+            const int n = i % N, v = i / N;  // v: dB's tokens, then dC's
+            const int t = v % kPart;
+            if (t >= m) continue;
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kGradWaves; ++w) s += red[w][n][v];
+            q.part_bc[((static_cast<int64_t>(gt) * p.T + t0 + t) * p.G + g) * 2 * N +
+                      (v / kPart) * N + n] = s;
+        }
+    }
+    if (!live) return;
+    for (int n = 0; n < N; ++n) {
+        part_a[static_cast<int64_t>(n) * p.D] = da[wave][n][lane];
+        if (q.dinit && o.s == 0) {
+            const int64_t at = o.row * q.dinit_outer + static_cast<int64_t>(d) * N + n;
+            if (q.dinit_bf16) static_cast<uint16_t*>(q.dinit)[at] = scan_round(carry[wave][n][lane]);
+            else static_cast<float*>(q.dinit)[at] = carry[wave][n][lane];
+        }
+    }
+    part_d[0] = dskip;
+    part_d[p.D] = dbias;
+}
+
+// ---------------------------------------------------------- 4: sums of parts ---
+
+// Workgroups [0, n_bc): dB and dC; [n_bc, n_bc + n_a): dA; then dskip and dt_bias's.
+template <typename WT>
+__global__ void __launch_bounds__(256) grad_reduce(const ScanParams p, const ScanGrad q, int n_bc,
+                                                   int n_a) {
+    const int64_t DN = static_cast<int64_t>(p.D) * p.N;
+    const int gtiles = q.tiles;
+    const int block = blockIdx.x;
+    if (block < n_bc) {
+        const int64_t per = static_cast<int64_t>(p.G) * 2 * p.N, n = p.T * per;
+        const int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x;
+        if (i >= n) return;
+        const int64_t t = i / per;
+        if (t < p.offsets[0] || t >= p.offsets[p.B]) return;
+        float s = 0.0f;
+        for (int k = 0; k < gtiles; ++k) s += q.part_bc[k * n + i];
+        const int r = static_cast<int>(i - t * per), g = r / (2 * p.N), v = r - g * 2 * p.N;
+        const ScanHeads& out = v < p.N ? q.db : q.dc;
+        scan_put(static_cast<WT*>(const_cast<void*>(out.p)) + t * out.tok + g * out.grp +
+                     (v < p.N ? v : v - p.N), s);
+        return;
+    }
+    const bool isa = block < n_bc + n_a;
+    const int64_t n = isa ? DN : 2 * static_cast<int64_t>(p.D);
+    const int64_t i = static_cast<int64_t>(block - n_bc - (isa ? 0 : n_a)) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const float* part = (isa ? q.part_a : q.part_d) + i;
+    double s0 = 0.0, s1 = 0.0;
+    int r = 0;
+    for (; r + 8 <= p.segs; r += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = part[(r + k) * n];
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) {
+            s0 += static_cast<double>(v[k]);
+            s1 += static_cast<double>(v[k + 1]);
+        }
+    }
+    for (; r < p.segs; ++r) s0 += static_cast<double>(part[r * n]);
+    const float s = static_cast<float>(s0 + s1);
+    if (isa) {
+        const int64_t k = i / p.D, d = i - k * p.D;
+        q.dA[d * p.N + k] = s;
+    } else if (i < p.D) {
+        if (q.dskip) q.dskip[i] = s;
+    } else if (q.dbias) {
+        q.dbias[i - p.D] = s;
+    }
+}
+
+template <typename WT, int N>
+hipError_t bwd_n(const ScanParams& p, const ScanGrad& q, hipStream_t s) {
+    const int64_t DN = static_cast<int64_t>(p.D) * N;
+    hipError_t e;
+    if (p.segs) {
+        constexpr int S = sum_states(N);
+        hipLaunchKernelGGL((grad_sums<WT, S>),
+                           dim3(static_cast<unsigned>(p.segs) * (N / S) * p.G * p.tiles),
+                           dim3(kScanThreads), 0, s, p, q);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (p.seg_len) {
+        const unsigned blocks = static_cast<unsigned>((DN + 255) / 256);
+        hipLaunchKernelGGL(grad_chains, dim3(2u * p.B * blocks), dim3(256), 0, s, p, q);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (p.segs) {
+        hipLaunchKernelGGL((grad_walk<WT, N>), dim3(static_cast<unsigned>(p.segs) * p.G * q.tiles),
+                           dim3(64 * grad_waves(N)), 0, s, p, q);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    const int64_t bc = p.B > 0 ? static_cast<int64_t>(p.T) * p.G * 2 * N : 0;
+    const int n_bc = static_cast<int>((bc + 255) / 256), n_a = static_cast<int>((DN + 255) / 256);
+    const int n_d = (2 * p.D + 255) / 256;
+    hipLaunchKernelGGL(grad_reduce<WT>, dim3(n_bc + n_a + n_d), dim3(256), 0, s, p, q, n_bc, n_a);
+    return hipGetLastError();
+}
+
+template <typename WT> hipError_t bwd_wt(const ScanParams& p, const ScanGrad& q, hipStream_t s) {
+    switch (p.N) {
+        case 8: return bwd_n<WT, 8>(p, q, s);
+        case 16: return bwd_n<WT, 16>(p, q, s);
+        case 32: return bwd_n<WT, 32>(p, q, s);
+        case 64: return bwd_n<WT, 64>(p, q, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int scan_grad_channels(int N) { return 64 * grad_waves(N); }
+
+hipError_t launch_scan_bwd(const ScanParams& p, const ScanGrad& q, bool work_bf16, hipStream_t s) {
+    return work_bf16 ? bwd_wt<uint16_t>(p, q, s) : bwd_wt<float>(p, q, s);
+}
+
+}  // namespace gdr

@@ -1,0 +1,142 @@
+// Device helpers of the selective scan (gfx950).
+#pragma once
+
+#include "gdr_internal.h"
+#include "gdr_scan.h"
+
+namespace gdr {
+
+constexpr float kScanLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ float scan_widen(uint16_t b) {
+    return __uint_as_float(static_cast<uint32_t>(b) << 16);
+}
+__device__ __forceinline__ uint16_t scan_round(float x) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));  // to nearest even
+}
+__device__ __forceinline__ float scan_value(float v) { return v; }
+__device__ __forceinline__ float scan_value(uint16_t v) { return scan_widen(v); }
+__device__ __forceinline__ void scan_put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void scan_put(uint16_t* p, float v) { *p = scan_round(v); }
+
+// n values from p, as float32; p aligned to all of them (16 bytes at most).
+template <int n> __device__ __forceinline__ void scan_load(const float* p, float (&v)[n]) {
+    if constexpr (n % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < n; i += 4) {
+            const float4 w = *reinterpret_cast<const float4*>(p + i);
+            v[i] = w.x; v[i + 1] = w.y; v[i + 2] = w.z; v[i + 3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = p[i];
+    }
+}
+template <int n> __device__ __forceinline__ void scan_load(const uint16_t* p, float (&v)[n]) {
+    if constexpr (n % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < n; i += 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + i);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[i + 2 * j] = __uint_as_float(u[j] << 16);
+                v[i + 2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+            }
+        }
+    } else if constexpr (n % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < n; i += 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p + i);
+            v[i] = __uint_as_float(w.x << 16); v[i + 1] = __uint_as_float(w.x & 0xFFFF0000u);
+            v[i + 2] = __uint_as_float(w.y << 16); v[i + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = scan_widen(p[i]);
+    }
+}
+template <int n> __device__ __forceinline__ void scan_store(float* p, const float (&v)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int n> __device__ __forceinline__ void scan_store(uint16_t* p, const float (&v)[n]) {
+#pragma unroll
+    for (int i = 0; i < n; i += 8) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            u[j] = scan_round(v[i + 2 * j]) |
+                   (static_cast<uint32_t>(scan_round(v[i + 2 * j + 1])) << 16);
+        *reinterpret_cast<uint4*>(p + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
+// e^x to about one float32 rounding: what x log2(e) loses to its rounding is
+// put back as a factor (the compensated product: 2^hi (1 + lo ln 2)).  Results
+// below 2^-126 are 0.
+__device__ __forceinline__ float scan_exp(float x) {
+    x = x < -150.0f ? -150.0f : x;
+    x = x > 128.0f ? 128.0f : x;
+    const float hi = x * kScanLog2e;
+    const float lo = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, kScanLog2e, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return __builtin_fmaf(e, lo * 0.693147181f, e);
+}
+__device__ __forceinline__ float scan_sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + scan_exp(-x));
+}
+// log(1 + e^x) = max(x, 0) + log(1 + t), t = e^-|x|.  log(1 + t) = 2 atanh(s) with
+// s = t / (2 + t) <= 1/3: an odd series in s, its tail after s fitted by a cubic
+// in s^2 (off by 1.6e-8 of the result at most), so that small t keep all their bits.
+__device__ __forceinline__ float scan_softplus(float x) {
+    const float t = scan_exp(-__builtin_fabsf(x));
+    const float s = t * __builtin_amdgcn_rcpf(2.0f + t), v = s * s;
+    float q = __builtin_fmaf(0.134337738f, v, 0.141169786f);
+    q = __builtin_fmaf(q, v, 0.200038359f);
+    q = __builtin_fmaf(q, v, 0.333333194f);
+    const float l = __builtin_fmaf(2.0f * s, v * q, 2.0f * s);
+    return (x > 0.0f ? x : 0.0f) + l;
+}
+
+// The number of the segment that row b's tokens start with, when rows are cut
+// into segments of `len` tokens: rows own disjoint ranges of numbers, with at
+// most one number unused at the end of each.
+__device__ __forceinline__ int64_t scan_first_seg(uint32_t off, int b, int len) {
+    return static_cast<int64_t>(off / static_cast<uint32_t>(len)) + b;
+}
+
+struct ScanSpan {
+    int row, s, count;  // the segment's row, its number there, the row's segments
+    int t0, n;          // its tokens
+};
+
+// Which tokens segment `seg` spans; false where it spans none.  Uniform.
+__device__ __forceinline__ bool scan_locate(const ScanParams& p, int seg, ScanSpan& o) {
+    if (p.seg_len == 0) {
+        o.row = seg;
+        o.s = 0;
+        o.count = 1;
+        o.t0 = static_cast<int>(p.offsets[seg]);
+        o.n = static_cast<int>(p.offsets[seg + 1]) - o.t0;
+        return true;
+    }
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {  // the last row whose first segment is at or before seg
+        const int mid = (lo + hi + 1) >> 1;
+        if (scan_first_seg(p.offsets[mid], mid, p.seg_len) <= seg) lo = mid; else hi = mid - 1;
+    }
+    const uint32_t a = p.offsets[lo];
+    const int n = static_cast<int>(p.offsets[lo + 1] - a);
+    const int64_t first = scan_first_seg(a, lo, p.seg_len);
+    o.row = lo;
+    o.s = static_cast<int>(seg - first);
+    o.count = n <= p.seg_len ? 1 : (n + p.seg_len - 1) / p.seg_len;
+    if (seg < first || o.s >= o.count) return false;
+    o.t0 = static_cast<int>(a) + o.s * p.seg_len;
+    o.n = min(p.seg_len, n - o.s * p.seg_len);
+    return true;
+}
+
+}  // namespace gdr

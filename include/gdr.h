@@ -79,6 +79,14 @@ extern "C" {
 #define GDR_FLAG_GATE_SIGMOID 4u
 #define GDR_FLAG_GATE_SILU 8u
 
+/* gdr_causal_conv1d and gdr_selective_scan_fwd flag: the pool's histories or
+ * states are read and not written (a window of drafted tokens, of which a fold
+ * takes the accepted prefix afterwards). */
+#define GDR_FLAG_KEEP_STATE 16u
+
+/* gdr_selective_scan_* flag: step sizes are softplus(dt + dt_bias). */
+#define GDR_FLAG_DT_SOFTPLUS 32u
+
 /* Head dims built (recurrence entries): K == V in {16, 32, 64, 128, 256}; the fused update also
  * takes (K, V) in {(64, 128), (128, 64), (128, 256), (256, 128)}. */
 #define GDR_MAX_HEAD_DIM 256
@@ -269,7 +277,8 @@ int gdr_snapshot_rollback(const gdr_tensor* state, const gdr_tensor* state_indic
  *   input_row_offsets [B+1] u32|i32 (B is shape[0] - 1); tokens of x
  *                     outside [off[0], off[B]) belong to no row: they are not
  *                     read and their output rows are not written
- *   flags             GDR_FLAG_CONV_SILU or 0
+ *   flags             GDR_FLAG_CONV_SILU and GDR_FLAG_KEEP_STATE (conv_state is
+ *                     not written: a drafted window, see gdr_causal_conv1d_fold)
  * Rows of length 0 touch nothing.  Two kernel launches on `stream` (outputs,
  * then the history update).
  */
@@ -423,6 +432,199 @@ int gdr_block_norm_bwd(const gdr_tensor* dresidual, const gdr_tensor* dy, const 
                        const gdr_tensor* h, const gdr_tensor* gate, const gdr_tensor* post_weight,
                        const gdr_tensor* pre_weight, int64_t group, float residual_scale,
                        float eps, uint32_t flags, const gdr_tensor* workspace, void* stream);
+
+/*
+ * gdr_causal_conv1d_fold - advance each row's history over its accepted prefix,
+ * after a gdr_causal_conv1d over a window of drafted tokens that left the
+ * histories alone (GDR_FLAG_KEEP_STATE).
+ *   conv_state        [slots, H, C] f32|bf16 (in/out), H in {1, 2, 3}
+ *   x                 [T, C] of the same dtype: what the window's call read
+ *   input_row_offsets [B+1] u32|i32
+ *   accepted          [B] u32|i32 (device): accepted tokens n of row b.  n == 0
+ *                     or above the row's length leaves the row alone; otherwise
+ *                     its history becomes the last H inputs of history ++ the
+ *                     row's first n, a copy of the bits.
+ *   slot_idx          [B] u32|i32, or absent (slot = row); 0xFFFFFFFF = padding
+ */
+int gdr_causal_conv1d_fold(const gdr_tensor* conv_state, const gdr_tensor* x,
+                           const gdr_tensor* input_row_offsets, const gdr_tensor* accepted,
+                           const gdr_tensor* slot_idx, void* stream);
+
+/* Floats of workspace that gdr_causal_conv1d_bwd needs, or -1 for arguments out
+ * of range.  Host only. */
+int64_t gdr_causal_conv1d_workspace(int64_t tokens, int64_t channels, int32_t width);
+
+/*
+ * gdr_causal_conv1d_bwd - gradients of gdr_causal_conv1d without conv_state
+ * (every row starts from zeros).  With g_t the gradient of the output before
+ * SiLU (recomputed from x):
+ *     dx_s = sum_k weight[W-1-k] g_{s+k}  over the tokens s+k of the row
+ *     dweight[j] = sum_t g_t x_{t-(W-1-j)};   dbias = sum_t g_t
+ *   dout, x           [T, C] work dtype (in), as in the forward
+ *   weight, bias, input_row_offsets, flags (GDR_FLAG_CONV_SILU or 0) as there
+ *   dx                [T, C] work (out); tokens outside the rows are not written
+ *   dweight           [C, W] f32 (out), unit stride over the taps
+ *   dbias             [C] f32 (out) or absent; needs bias
+ *   workspace         f32 scratch of gdr_causal_conv1d_workspace() floats
+ * Outputs must not overlap inputs or one another.  The sums' order is fixed.
+ */
+int gdr_causal_conv1d_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gdr_tensor* weight,
+                          const gdr_tensor* bias, const gdr_tensor* input_row_offsets,
+                          const gdr_tensor* dx, const gdr_tensor* dweight, const gdr_tensor* dbias,
+                          uint32_t flags, const gdr_tensor* workspace, void* stream);
+
+/*
+ * Selective state space scan.  Channel d of D carries N states, token by token:
+ *     delta = dt_t[d] + dt_bias[d]   (softplus of it with GDR_FLAG_DT_SOFTPLUS)
+ *     h_t[n] = exp(delta A[d, n]) h_{t-1}[n] + delta x_t[d] B_t[g, n]
+ *     out_t[d] = (sum_n C_t[g, n] h_t[n] + D[d] x_t[d]) silu(z_t[d])
+ * with g = d / (D / G): the channels of a group share B and C.  float32
+ * arithmetic and sums.
+ *
+ * Common arguments
+ *   x, dt, z, out     [T, D] work dtype: f32 or bf16; 16-byte rows at any
+ *                     stride (halves of a projection's output can be given as
+ *                     they are); D / G a multiple of 4.  z absent: no gate.
+ *   A                 [D, N] f32 contiguous; N in {8, 16, 32, 64}
+ *   B, C              [T, G, N] work, unit stride over N, 16-byte rows
+ *   D, dt_bias        [D] f32 or absent (zeros)
+ *   input_row_offsets [B+1] u32|i32; tokens outside [off[0], off[B]) belong to
+ *                     no row, their outputs are not written
+ *   states            [.., D, N] f32|bf16, each D x N block dense, 16-byte
+ *                     aligned; bf16 states are rounded once, when stored
+ *   workspace         f32 scratch of gdr_selective_scan_workspace() floats,
+ *                     16-byte aligned; may be absent when that is 0.  Held by
+ *                     the call until its work on `stream` is done.
+ * Outputs must not overlap inputs or one another.  A value that is not finite
+ * can reach the later outputs of its row (in a gradient: every output of its
+ * row, and the weights' gradients), but no other row's.
+ */
+
+/* Floats of workspace for one call (0: none), or -1 for arguments that are not
+ * positive.  `backward`: 0 for gdr_selective_scan_fwd, else for
+ * gdr_selective_scan_bwd.  Host only. */
+int64_t gdr_selective_scan_workspace(int64_t tokens, int64_t rows, int64_t channels,
+                                     int32_t state_size, int32_t groups, int backward);
+
+/*
+ * gdr_selective_scan_fwd - ragged forward over prompts and windows.
+ *   state             [slots, D, N] pool, read and written in place at slot_idx
+ *                     (at the row's number when slot_idx is absent); rows of
+ *                     length 0 leave their slot alone.  With
+ *                     GDR_FLAG_KEEP_STATE it is not written: a window of
+ *                     drafted tokens, whose accepted prefix
+ *                     gdr_selective_scan_fold takes afterwards.
+ *   slot_idx          [B] u32|i32; 0xFFFFFFFF marks a padding row (its tokens'
+ *                     outputs are +0.0, no state is touched)
+ *   initial_state     [B, D, N] or absent (zeros), and
+ *   final_state       [B, D, N] (out) of the same dtype, or absent: dense
+ *                     states instead of a pool
+ *   flags             GDR_FLAG_DT_SOFTPLUS, GDR_FLAG_KEEP_STATE
+ */
+int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr_tensor* dt,
+                           const gdr_tensor* A, const gdr_tensor* B, const gdr_tensor* C,
+                           const gdr_tensor* D, const gdr_tensor* z, const gdr_tensor* dt_bias,
+                           const gdr_tensor* input_row_offsets, const gdr_tensor* initial_state,
+                           const gdr_tensor* final_state, const gdr_tensor* state,
+                           const gdr_tensor* slot_idx, uint32_t flags,
+                           const gdr_tensor* workspace, void* stream);
+
+/*
+ * gdr_selective_scan_step - one token for each of T rows: token t is row t,
+ * with the state in slot slot_idx[t] (slot t when slot_idx is absent), updated
+ * in place.  Padding rows as above.
+ */
+int gdr_selective_scan_step(const gdr_tensor* out, const gdr_tensor* x, const gdr_tensor* dt,
+                            const gdr_tensor* A, const gdr_tensor* B, const gdr_tensor* C,
+                            const gdr_tensor* D, const gdr_tensor* z, const gdr_tensor* dt_bias,
+                            const gdr_tensor* state, const gdr_tensor* slot_idx, uint32_t flags,
+                            void* stream);
+
+/*
+ * gdr_selective_scan_fold - advance each row's state over its accepted prefix:
+ * what gdr_selective_scan_fwd leaves after the row's first accepted[b] tokens
+ * (the same bits where the forward takes the row token by token in one piece:
+ * calls of up to 64 tokens, rows of up to 16 in any call of more than 8 rows).
+ *   accepted          [B] u32|i32 (device): 0 or above the row's length leaves
+ *                     the row alone
+ */
+int gdr_selective_scan_fold(const gdr_tensor* state, const gdr_tensor* x, const gdr_tensor* dt,
+                            const gdr_tensor* A, const gdr_tensor* B, const gdr_tensor* dt_bias,
+                            const gdr_tensor* input_row_offsets, const gdr_tensor* accepted,
+                            const gdr_tensor* slot_idx, uint32_t flags, void* stream);
+
+/*
+ * gdr_selective_scan_bwd - gradients of gdr_selective_scan_fwd with dense
+ * states.  With dy = dout silu(z):
+ *     lam_t = dy_t C_t + a_{t+1} lam_{t+1}  (dfinal_state at the end)
+ *     w_t = lam_t a_t h_{t-1}
+ *     dx = D dy + delta sum_n lam B;   ddelta = x sum_n lam B + sum_n A w
+ *     dA = sum_t delta w;   dB = sum_d lam delta x;   dC = sum_d dy h
+ *     dD = sum_t dy x;   dz = dout y silu'(z);   dinitial_state = a_1 lam_1
+ * and through the softplus to dt and dt_bias.
+ *   dout              [T, D] work (in): gradient of out
+ *   initial_state     as in the forward, or absent
+ *   dfinal_state      [B, D, N] f32|bf16: gradient of final_state, or absent
+ *   dx, ddt, dz       [T, D] work (out); dz exactly when z is given
+ *   dA                [D, N] f32 (out), contiguous
+ *   dB, dC            like B, C (out)
+ *   dD, ddt_bias      [D] f32 (out), exactly when D and dt_bias are given
+ *   dinitial_state    [B, D, N] f32|bf16 (out) or absent
+ *   flags             GDR_FLAG_DT_SOFTPLUS or 0
+ * Tokens outside the rows are not written.  The sums' order is fixed: the same
+ * call gives the same bits.
+ */
+int gdr_selective_scan_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gdr_tensor* dt,
+                           const gdr_tensor* A, const gdr_tensor* B, const gdr_tensor* C,
+                           const gdr_tensor* D, const gdr_tensor* z, const gdr_tensor* dt_bias,
+                           const gdr_tensor* input_row_offsets, const gdr_tensor* initial_state,
+                           const gdr_tensor* dfinal_state, const gdr_tensor* dx,
+                           const gdr_tensor* ddt, const gdr_tensor* dA, const gdr_tensor* dB,
+                           const gdr_tensor* dC, const gdr_tensor* dD, const gdr_tensor* dz,
+                           const gdr_tensor* ddt_bias, const gdr_tensor* dinitial_state,
+                           uint32_t flags, const gdr_tensor* workspace, void* stream);
+
+/* Floats of workspace that gdr_verify_drafts needs, or -1 for arguments out of
+ * range.  Host only. */
+int64_t gdr_verify_drafts_workspace(int64_t tokens, int64_t rows, int64_t vocab);
+
+/*
+ * gdr_verify_drafts - which of a window's drafted tokens stand, judged by the
+ * target's probabilities from given random numbers, and the token that each
+ * row goes on with.  A row's window holds a token that is certain and then the
+ * drafts; row t of target says what follows token t.  With i counted from the
+ * row's start, p_i and q_i rows i of the window in target and draft:
+ *     draft x_i (i >= 1) stands while uniform_i q_i(x_i) < p_{i-1}(x_i)
+ *     accepted = 1 + the drafts before the first that falls
+ *     next_token: drawn by uniform_0 from max(p_{accepted-1} - q_accepted, 0)
+ *     where a draft fell (from p_{accepted-1} itself if that is zero everywhere),
+ *     from p_{accepted-1} behind the last draft
+ * Drawn: the lowest token whose running sum of weights, in float64, exceeds
+ * uniform_0 times their whole sum (the last token with a weight if none does,
+ * -1 if none has one).  Weights need not sum to 1; NaN and infinite ones count
+ * as 0.  Without uniform, greedily: a draft stands while it is the largest of
+ * row i-1 of target (scores of any kind; the lowest token of equal ones, NaN
+ * is no value), and next_token is the largest of row accepted-1 (-1 in a row
+ * of NaN).
+ *   accepted          [B] u32|i32 (out): tokens of the window that stand, as
+ *                     gdr_state_fold, gdr_snapshot_rollback,
+ *                     gdr_selective_scan_fold and gdr_causal_conv1d_fold take
+ *                     them; 0 for a row without tokens
+ *   next_token        [B] u32|i32 (out); -1 for a row without tokens
+ *   tokens            [T] u32|i32; a draft outside the vocabulary falls
+ *   target            [T, V] f32|bf16, unit stride over V, rows at any stride
+ *   draft             [T, V] of the same dtype: row t is what token t was drawn
+ *                     from (a window's first row is not read); absent: drafts
+ *                     without probabilities of their own (q_i(x_i) = 1)
+ *   uniform           [T] f32 in [0, 1), or absent (greedy)
+ *   input_row_offsets [B+1] u32|i32
+ *   workspace         f32 scratch of gdr_verify_drafts_workspace() floats,
+ *                     16-byte aligned
+ */
+int gdr_verify_drafts(const gdr_tensor* accepted, const gdr_tensor* next_token,
+                      const gdr_tensor* tokens, const gdr_tensor* target, const gdr_tensor* draft,
+                      const gdr_tensor* uniform, const gdr_tensor* input_row_offsets,
+                      const gdr_tensor* workspace, void* stream);
 
 /*
  * gdr_fwd_output_shape - shape of recurrence_output for the given conv
