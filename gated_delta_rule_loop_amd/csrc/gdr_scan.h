@@ -57,6 +57,7 @@ struct ScanGrad {
                                     // step sizes from the segment's start (parts: T/kScanPart + B)
     float* seg_rev;                 // [segs, N, D] what a segment hands to its past; the
                                     // gradient keeps seg_state in that order too
+    float* turned;                  // [parts, G, 2, N, kScanPart] B and C
     float* part_bc;                 // [tiles of a group, T, G, 2, N]
     float* part_a;                  // [segs, N, D]
     float* part_d;                  // [segs, 2, D]

@@ -206,7 +206,7 @@ FwdPlan fwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
 // How a gradient is cut, and where its workspace holds what.
 struct BwdPlan {
     int64_t gtiles, seg_len, segs, parts;
-    int64_t state, rev, delta, check, bc, a, dd, end;
+    int64_t state, rev, delta, check, turned, bc, a, dd, end;
 };
 
 BwdPlan bwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
@@ -230,6 +230,7 @@ BwdPlan bwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
         p.delta = take(p.segs * D);
     }
     p.check = take(p.parts * (D * N + D));
+    p.turned = take(p.parts * G * 2 * N * kScanPart);
     p.bc = take(p.gtiles * T * G * 2 * N);
     p.a = take(p.segs * D * N);
     p.dd = take(p.segs * 2 * D);
@@ -516,12 +517,13 @@ int gdr_selective_scan_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gd
     g.tiles = static_cast<int32_t>(pl.gtiles);
     g.check = ws + pl.check;
     g.seg_rev = ws + pl.rev;
+    g.turned = ws + pl.turned;
     g.part_bc = ws + pl.bc;
     g.part_a = ws + pl.a;
     g.part_d = ws + pl.dd;
     const int64_t threads = scan_grad_channels(static_cast<int>(d.N));
     const int64_t DN = d.D * d.N;
-    if ((rc = check_grid(fn, pl.segs * (d.N > 16 ? d.N / 16 : 1) * d.G * d.tiles(), kScanThreads)) ||
+    if ((rc = check_grid(fn, pl.segs * d.G * ((d.N > 16 ? d.N / 16 : 1) * d.tiles() + 1), kScanThreads)) ||
         (rc = check_grid(fn, 2 * d.B * ceil_div(DN, 256), 256)) ||
         (rc = check_grid(fn, pl.segs * d.G * pl.gtiles, threads)) ||
         (rc = check_grid(fn, ceil_div(d.T * d.G * 2 * d.N, 256) + ceil_div(DN, 256) +

@@ -57,13 +57,40 @@ __device__ __forceinline__ int64_t first_part(const ScanParams& p, const ScanSpa
 
 // ------------------------------------------------------------ 1: own sums ---
 
+// B and C of a segment's parts as float32 [n][token], so that the walk reads a state's
+// tokens with scalar loads; zeros past the row's end.
+template <typename WT>
+__device__ __forceinline__ void turn_parts(const ScanParams& p, const ScanGrad& q,
+                                           const ScanSpan& o, int g) {
+    const int64_t first = first_part(p, o);
+    for (int part = 0; part * kPart < o.n; ++part) {
+        const int m = o.n - part * kPart;
+        float* to = q.turned + ((first + part) * p.G + g) * 2 * p.N * kPart;
+        for (int i = threadIdx.x; i < 2 * p.N * kPart; i += kScanThreads) {
+            const int n = i % p.N, v = i / p.N, t = v % kPart;  // v: B's tokens, then C's
+            const ScanHeads& from = v < kPart ? p.b : p.c;
+            float x = 0.0f;
+            if (t < m)
+                x = scan_value(static_cast<const WT*>(
+                    from.p)[(static_cast<int64_t>(o.t0) + part * kPart + t) * from.tok +
+                            g * from.grp + n]);
+            to[(v / kPart * p.N + n) * kPart + t] = x;
+        }
+    }
+}
+
 // N: the states of this workgroup, of the channels' p.N.
 template <typename WT, int N>
 __global__ void __launch_bounds__(kScanThreads) grad_sums(const ScanParams p, const ScanGrad q) {
-    const int ctiles = p.G * p.tiles;
+    const int ctiles = p.G * p.tiles, nblocks = p.N / N;
     const int block = blockIdx.x / ctiles, tile = blockIdx.x - block * ctiles;
-    const int nblocks = p.N / N, seg = block / nblocks, n0 = (block - seg * nblocks) * N;
+    const int seg = block / nblocks, n0 = (block - seg * nblocks) * N;
     ScanSpan o;
+    if (seg >= p.segs) {  // the last workgroups turn B and C
+        const int job = blockIdx.x - p.segs * nblocks * ctiles;
+        if (scan_locate(p, job / p.G, o)) turn_parts<WT>(p, q, o, job % p.G);
+        return;
+    }
     if (!scan_locate(p, seg, o)) return;
     const bool ends = o.s < o.count - 1, rev = o.s > 0;
     if (o.n <= kPart && !ends && !rev) return;
@@ -247,11 +274,23 @@ __device__ __forceinline__ float sums32(float (&x)[16], float (&y)[16]) {
     return r[0] + dpp<0xB1>(r[0]);
 }
 
-template <typename WT, int N>
-__global__ void __launch_bounds__(64 * grad_waves(N))
+// A token's raw operands of a part, all loaded before the first is used.
+template <typename WT> struct PartRows {
+    WT v[kPart];
+    __device__ __forceinline__ void load(const void* base, int64_t tok, int64_t t0, int m, int d) {
+        const WT* at = static_cast<const WT*>(base) + t0 * tok;
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+            v[i] = at[d];
+            at += i + 1 < m ? tok : 0;  // past the row's end: its last token again
+        }
+    }
+};
+
+template <typename WT, int N, bool GATED>
+__global__ void __launch_bounds__(64 * grad_waves(N), 2)
 grad_walk(const ScanParams p, const ScanGrad q) {
     constexpr int kGradWaves = grad_waves(N), kGradThreads = 64 * kGradWaves;
-    __shared__ __attribute__((aligned(16))) float bs[N][kPart], cs[N][kPart];
     __shared__ float carry[kGradWaves][N][64], da[kGradWaves][N][64];
     __shared__ float red[kGradWaves][N][2 * kPart];
     const int gtiles = q.tiles, ctiles = p.G * gtiles;
@@ -268,7 +307,6 @@ grad_walk(const ScanParams p, const ScanGrad q) {
     ScanSpan o;
     if (!scan_locate(p, seg, o)) {
         if (live) {
-#pragma unroll
             for (int n = 0; n < N; ++n) part_a[static_cast<int64_t>(n) * p.D] = 0.0f;
             part_d[0] = 0.0f;
             part_d[p.D] = 0.0f;
@@ -283,68 +321,80 @@ grad_walk(const ScanParams p, const ScanGrad q) {
     }
     const float bias = p.bias ? p.bias[d] : 0.0f;
     const float skip = p.skip ? p.skip[d] : 0.0f;
-    const bool gated = p.z.p != nullptr;
     float dskip = 0.0f, dbias = 0.0f;
-    const float* check = q.check + first_part(p, o) * (DN + p.D) + d;
-    const WT* xp = static_cast<const WT*>(p.x.p) + d;
-    const WT* dtp = static_cast<const WT*>(p.dt.p) + d;
-    const WT* dop = static_cast<const WT*>(q.d_o.p) + d;
-    const WT* zp = static_cast<const WT*>(p.z.p) + d;
-    WT* dx = static_cast<WT*>(const_cast<void*>(q.dx.p)) + d;
-    WT* ddt = static_cast<WT*>(const_cast<void*>(q.ddt.p)) + d;
-    WT* dz = static_cast<WT*>(const_cast<void*>(q.dz.p)) + d;
-    auto put = [](float v) {
-        if constexpr (sizeof(WT) == 2) return scan_round(v);
-        else return v;
-    };
+    const int64_t first = first_part(p, o);
+    const float* check = q.check + first * (DN + p.D) + d;
     for (int part = (o.n - 1) / kPart; o.n > 0 && part >= 0; --part) {
         const int64_t t0 = o.t0 + part * kPart;
         const int m = min(kPart, o.n - part * kPart);
-        __syncthreads();  // the part before has been read
-        for (int i = tid; i < N * kPart; i += kGradThreads) {
-            const int k = i % N, t = i / N;
-            const int64_t at = t0 + min(t, m - 1);
-            bs[k][t] = scan_value(static_cast<const WT*>(p.b.p)[at * p.b.tok + g * p.b.grp + k]);
-            cs[k][t] = scan_value(static_cast<const WT*>(p.c.p)[at * p.c.tok + g * p.c.grp + k]);
-        }
-        float delta[kPart], u[kPart], dy[kPart], s1[kPart], s2[kPart], y[kPart];
-#pragma unroll
-        for (int i = 0; i < kPart; ++i) {  // tokens past the row's end: no step, no gradient
-            const int64_t at = t0 + min(i, m - 1);
-            float dl = scan_value(dtp[at * p.dt.tok]) + bias;
-            if (p.softplus) dl = scan_softplus(dl);
-            float gy = scan_value(dop[at * q.d_o.tok]);
-            if (gated) {
-                const float zv = scan_value(zp[at * p.z.tok]);
-                gy *= zv * scan_sigmoid(zv);
-            }
-            delta[i] = i < m ? dl : 0.0f;
-            dy[i] = i < m && live ? gy : 0.0f;
-            u[i] = i < m && live ? dl * scan_value(xp[at * p.x.tok]) : 0.0f;
-            s1[i] = s2[i] = y[i] = 0.0f;
-        }
+        PartRows<WT> xr, dr, gr, zr;
+        dr.load(p.dt.p, p.dt.tok, t0, m, d);
+        xr.load(p.x.p, p.x.tok, t0, m, d);
+        gr.load(q.d_o.p, q.d_o.tok, t0, m, d);
+        if constexpr (GATED) zr.load(p.z.p, p.z.tok, t0, m, d);
         const float* ck = check + part * (DN + p.D);
         const float since = part ? ck[DN] : 0.0f;  // step sizes from the segment's start
-        __syncthreads();
+        const float* bc = q.turned + ((first + part) * p.G + g) * 2 * N * kPart;
+        // delta, its slope, delta x, dy, dout times the gate's slope, and the sums over n.
+        // Tokens past the row's end have no step and no gradient.
+        float delta[kPart], slope[kPart], u[kPart], dy[kPart], gz[kPart];
+        float s1[kPart], s2[kPart], y[kPart];
+        if (p.softplus) {
+#pragma unroll
+            for (int i = 0; i < kPart; ++i)
+                delta[i] = scan_softplus(scan_value(dr.v[i]) + bias, slope[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+                delta[i] = scan_value(dr.v[i]) + bias;
+                slope[i] = 1.0f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) {
+            const bool in = i < m && live;
+            float gy = scan_value(gr.v[i]);
+            if constexpr (GATED) {
+                const float zv = scan_value(zr.v[i]), sig = scan_sigmoid(zv);
+                gz[i] = gy * (sig * __builtin_fmaf(zv, 1.0f - sig, 1.0f));
+                gy *= zv * sig;
+            }
+            delta[i] = i < m ? delta[i] : 0.0f;
+            dy[i] = in ? gy : 0.0f;
+            u[i] = in ? delta[i] * scan_value(xr.v[i]) : 0.0f;
+            s1[i] = s2[i] = y[i] = 0.0f;
+        }
+        __syncthreads();  // the sums of the part before have been read
+        float an1, st1, ck1 = 0.0f;  // the next state's operands
+        auto fetch = [&](int n) {
+            const int64_t nd = static_cast<int64_t>(n) * p.D, dn = static_cast<int64_t>(d) * N + n;
+            an1 = p.A[dn];
+            st1 = cut ? p.seg_state[mine + nd] : state_at(p.in, o.row, dn);
+            if (part) ck1 = ck[nd];
+        };
+        fetch(0);
         for (int n = 0; n < N; ++n) {
-            const int64_t nd = static_cast<int64_t>(n) * p.D;
-            const float an = p.A[static_cast<int64_t>(d) * N + n], a2 = an * kScanLog2e;
-            float start = cut ? p.seg_state[mine + nd]
-                              : state_at(p.in, o.row, static_cast<int64_t>(d) * N + n);
-            if (part) start = __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * since), start, ck[nd]);
+            const float an = an1, a2 = an * kScanLog2e;
+            const float start = part ? __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * since), st1, ck1)
+                                     : st1;
+            if (n + 1 < N) fetch(n + 1);
+            float mu = carry[wave][n][lane];
+            float b[kPart], c[kPart];
+            uniform_row<float, kPart>(bc, n * kPart, b);
+            uniform_row<float, kPart>(bc, (N + n) * kPart, c);
             float a[kPart], h[kPart], hp = start;
 #pragma unroll
             for (int i = 0; i < kPart; ++i) {
                 a[i] = __builtin_amdgcn_exp2f(delta[i] * a2);
-                h[i] = __builtin_fmaf(a[i], hp, u[i] * bs[n][i]);
+                h[i] = __builtin_fmaf(a[i], hp, u[i] * b[i]);
                 hp = h[i];
-                if (gated) y[i] = __builtin_fmaf(cs[n][i], h[i], y[i]);
+                if constexpr (GATED) y[i] = __builtin_fmaf(c[i], h[i], y[i]);
             }
-            float mu = carry[wave][n][lane], ga = 0.0f;
+            float ga = 0.0f;
 #pragma unroll
             for (int i = kPart - 1; i >= 0; --i) {
-                const float lam = __builtin_fmaf(dy[i], cs[n][i], mu);
-                s1[i] = __builtin_fmaf(lam, bs[n][i], s1[i]);
+                const float lam = __builtin_fmaf(dy[i], c[i], mu);
+                s1[i] = __builtin_fmaf(lam, b[i], s1[i]);
                 mu = a[i] * lam;
                 const float w = mu * (i ? h[i - 1] : start);
                 s2[i] = __builtin_fmaf(an, w, s2[i]);
@@ -357,26 +407,23 @@ grad_walk(const ScanParams p, const ScanGrad q) {
             const float sum = sums32(a, h);
             if (!(lane & 1)) red[wave][n][lane >> 1] = sum;
         }
+        WT* dx = static_cast<WT*>(const_cast<void*>(q.dx.p)) + t0 * q.dx.tok;
+        WT* ddt = static_cast<WT*>(const_cast<void*>(q.ddt.p)) + t0 * q.ddt.tok;
+        WT* dz = static_cast<WT*>(const_cast<void*>(q.dz.p)) + t0 * q.dz.tok;
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
-            if (i < m) {
-                const int64_t at = t0 + i;
-                const float xv = scan_value(xp[at * p.x.tok]);
-                float dd = __builtin_fmaf(xv, s1[i], s2[i]);
-                if (p.softplus) dd *= scan_sigmoid(scan_value(dtp[at * p.dt.tok]) + bias);
-                dbias += dd;
-                dskip = __builtin_fmaf(dy[i], xv, dskip);
-                if (live) {
-                    dx[at * q.dx.tok] = put(__builtin_fmaf(skip, dy[i], delta[i] * s1[i]));
-                    ddt[at * q.ddt.tok] = put(dd);
-                    if (gated) {
-                        const float zv = scan_value(zp[at * p.z.tok]), sig = scan_sigmoid(zv);
-                        const float yv = __builtin_fmaf(skip, xv, y[i]);
-                        dz[at * q.dz.tok] = put(scan_value(dop[at * q.d_o.tok]) * yv *
-                                                (sig * __builtin_fmaf(zv, 1.0f - sig, 1.0f)));
-                    }
-                }
+            const float xv = scan_value(xr.v[i]);
+            const float dd = i < m ? __builtin_fmaf(xv, s1[i], s2[i]) * slope[i] : 0.0f;
+            dbias += dd;
+            dskip = __builtin_fmaf(dy[i], xv, dskip);
+            if (i < m && live) {
+                scan_put(dx + d, __builtin_fmaf(skip, dy[i], delta[i] * s1[i]));
+                scan_put(ddt + d, dd);
+                if constexpr (GATED) scan_put(dz + d, gz[i] * __builtin_fmaf(skip, xv, y[i]));
             }
+            dx += q.dx.tok;
+            ddt += q.ddt.tok;
+            if constexpr (GATED) dz += q.dz.tok;
         }
         __syncthreads();
         for (int i = tid; i < 2 * kPart * N; i += kGradThreads) {
@@ -462,7 +509,7 @@ hipError_t bwd_n(const ScanParams& p, const ScanGrad& q, hipStream_t s) {
     if (p.segs) {
         constexpr int S = sum_states(N);
         hipLaunchKernelGGL((grad_sums<WT, S>),
-                           dim3(static_cast<unsigned>(p.segs) * (N / S) * p.G * p.tiles),
+                           dim3(static_cast<unsigned>(p.segs) * p.G * (N / S * p.tiles + 1)),
                            dim3(kScanThreads), 0, s, p, q);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
@@ -472,8 +519,9 @@ hipError_t bwd_n(const ScanParams& p, const ScanGrad& q, hipStream_t s) {
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (p.segs) {
-        hipLaunchKernelGGL((grad_walk<WT, N>), dim3(static_cast<unsigned>(p.segs) * p.G * q.tiles),
-                           dim3(64 * grad_waves(N)), 0, s, p, q);
+        const dim3 grid(static_cast<unsigned>(p.segs) * p.G * q.tiles), block(64 * grad_waves(N));
+        if (p.z.p) hipLaunchKernelGGL((grad_walk<WT, N, true>), grid, block, 0, s, p, q);
+        else hipLaunchKernelGGL((grad_walk<WT, N, false>), grid, block, 0, s, p, q);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const int64_t bc = p.B > 0 ? static_cast<int64_t>(p.T) * p.G * 2 * N : 0;

@@ -90,14 +90,20 @@ __device__ __forceinline__ float scan_sigmoid(float x) {
 // log(1 + e^x) = max(x, 0) + log(1 + t), t = e^-|x|.  log(1 + t) = 2 atanh(s) with
 // s = t / (2 + t) <= 1/3: an odd series in s, its tail after s fitted by a cubic
 // in s^2 (off by 1.6e-8 of the result at most), so that small t keep all their bits.
-__device__ __forceinline__ float scan_softplus(float x) {
+// `slope`: its derivative, the sigmoid.
+__device__ __forceinline__ float scan_softplus(float x, float& slope) {
     const float t = scan_exp(-__builtin_fabsf(x));
     const float s = t * __builtin_amdgcn_rcpf(2.0f + t), v = s * s;
     float q = __builtin_fmaf(0.134337738f, v, 0.141169786f);
     q = __builtin_fmaf(q, v, 0.200038359f);
     q = __builtin_fmaf(q, v, 0.333333194f);
     const float l = __builtin_fmaf(2.0f * s, v * q, 2.0f * s);
+    slope = (x > 0.0f ? 1.0f : t) * __builtin_amdgcn_rcpf(1.0f + t);
     return (x > 0.0f ? x : 0.0f) + l;
+}
+__device__ __forceinline__ float scan_softplus(float x) {
+    float slope;
+    return scan_softplus(x, slope);
 }
 
 // The number of the segment that row b's tokens start with, when rows are cut
