@@ -144,26 +144,6 @@ template <typename WT, typename ST> hipError_t narrow_n(const ScanParams& p, hip
 
 // --------------------------------------------------------------- wide walk ---
 
-// A pointer whose loads at wave-uniform addresses are scalar loads.
-#define GDR_UNIFORM __attribute__((address_space(4)))
-
-template <typename WT, int N>
-__device__ __forceinline__ void uniform_row(const void* base, int64_t elem, float (&v)[N]) {
-    const uint64_t at = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(elem) * sizeof(WT);
-    const GDR_UNIFORM uint32_t* q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(at);
-    if constexpr (sizeof(WT) == 4) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(q[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const uint32_t w = q[i];
-            v[2 * i] = __uint_as_float(w << 16);
-            v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-        }
-    }
-}
-
 constexpr int kAhead = 4;  // tokens whose x, dt and z are loaded before those in work
 
 template <typename WT, int N, bool SUMS>
@@ -178,7 +158,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
     const int cg = (tile - g * p.tiles) * kScanThreads + static_cast<int>(threadIdx.x);
     const bool live = cg < p.gd;
     const int d = g * p.gd + min(cg, p.gd - 1);
-    const uint32_t slot = p.slot_idx ? p.slot_idx[o.row] : static_cast<uint32_t>(o.row);
+    const uint32_t slot = p.slot_idx ? scan_index(p.slot_idx, o.row) : static_cast<uint32_t>(o.row);
     const bool pad = p.slot_idx != nullptr && slot == kPadSlot;
     if (pad) {
         if (!SUMS && live && p.out)

@@ -27,11 +27,22 @@ struct ScanDims {
 };
 
 // [T, D] operand: unit innermost stride, 16-byte rows.
+// Tokens are addressed by unsigned 32-bit offsets from a part's first.
+constexpr int64_t kMaxTokenStride = (int64_t{1} << 24) - 1;
+
+int check_token_stride(const char* fn, const char* name, const gdr_tensor* t) {
+    if (t->shape[0] > 1 && !empty(t) && (t->stride[0] < 0 || t->stride[0] > kMaxTokenStride))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: %s has a token stride outside 0..%lld elements", fn,
+                    name, static_cast<ll>(kMaxTokenStride));
+    return GDR_OK;
+}
+
 int check_rows(const char* fn, const char* name, const gdr_tensor* t, const ScanDims& d, bool out) {
     const int64_t shape[2] = {d.T, d.D};
     int rc = check_tensor(fn, name, t, 2, shape, true, true, false);
     if (rc || (rc = check_work_dtype(fn, name, t, d.work)) ||
-        (rc = check_layout(fn, name, t, vec_mult(d.work))))
+        (rc = check_layout(fn, name, t, vec_mult(d.work))) ||
+        (rc = check_token_stride(fn, name, t)))
         return rc;
     return out ? check_distinct(fn, name, t) : GDR_OK;
 }
@@ -41,7 +52,8 @@ int check_groups(const char* fn, const char* name, const gdr_tensor* t, const Sc
     const int64_t shape[3] = {d.T, d.G, d.N};
     int rc = check_tensor(fn, name, t, 3, shape, true, true, false);
     if (rc || (rc = check_work_dtype(fn, name, t, d.work)) ||
-        (rc = check_layout(fn, name, t, vec_mult(d.work))))
+        (rc = check_layout(fn, name, t, vec_mult(d.work))) ||
+        (rc = check_token_stride(fn, name, t)))
         return rc;
     return out ? check_distinct(fn, name, t) : GDR_OK;
 }

@@ -19,12 +19,12 @@
 //      segments) are added in a fixed order.
 // Everything is float32; sums over segments are float64.  Bound by the vector
 // units: about 26 slots a token, channel and state.
+#include <type_traits>
+
 #include "gdr_scan_dev.h"
 
 namespace gdr {
 namespace {
-
-#define GDR_UNIFORM __attribute__((address_space(4)))
 
 constexpr int kPart = kScanPart;
 // Waves of a gradient's workgroup: carried sums of every state take 512 bytes of
@@ -33,26 +33,9 @@ constexpr int grad_waves(int N) { return N > 32 ? 2 : 4; }
 // States that one workgroup of the first launch carries.
 constexpr int sum_states(int N) { return N < 16 ? N : 16; }
 
-template <typename WT, int N>
-__device__ __forceinline__ void uniform_row(const void* base, int64_t elem, float (&v)[N]) {
-    const uint64_t at = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(elem) * sizeof(WT);
-    const GDR_UNIFORM uint32_t* q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(at);
-    if constexpr (sizeof(WT) == 4) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(q[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-            const uint32_t w = q[i];
-            v[2 * i] = __uint_as_float(w << 16);
-            v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-        }
-    }
-}
-
 // The number of a segment's first part (segments are whole parts but for a row's last).
 __device__ __forceinline__ int64_t first_part(const ScanParams& p, const ScanSpan& o) {
-    return scan_first_seg(p.offsets[o.row], o.row, kPart) + static_cast<int64_t>(o.s) * (p.seg_len / kPart);
+    return scan_first_seg(scan_index(p.offsets, o.row), o.row, kPart) + static_cast<int64_t>(o.s) * (p.seg_len / kPart);
 }
 
 // ------------------------------------------------------------ 1: own sums ---
@@ -81,7 +64,7 @@ __device__ __forceinline__ void turn_parts(const ScanParams& p, const ScanGrad& 
 
 // N: the states of this workgroup, of the channels' p.N.
 template <typename WT, int N>
-__global__ void __launch_bounds__(kScanThreads) grad_sums(const ScanParams p, const ScanGrad q) {
+__global__ void __launch_bounds__(kScanThreads, 3) grad_sums(const ScanParams p, const ScanGrad q) {
     const int ctiles = p.G * p.tiles, nblocks = p.N / N;
     const int block = blockIdx.x / ctiles, tile = blockIdx.x - block * ctiles;
     const int seg = block / nblocks, n0 = (block - seg * nblocks) * N;
@@ -109,12 +92,11 @@ __global__ void __launch_bounds__(kScanThreads) grad_sums(const ScanParams p, co
         R[i] = 0.0f;
     }
     const float bias = p.bias ? p.bias[d] : 0.0f;
-    const WT* x = static_cast<const WT*>(p.x.p) + static_cast<int64_t>(o.t0) * p.x.tok;
-    const WT* dt = static_cast<const WT*>(p.dt.p) + static_cast<int64_t>(o.t0) * p.dt.tok;
-    const WT* d_o = static_cast<const WT*>(q.d_o.p) + static_cast<int64_t>(o.t0) * q.d_o.tok;
     const bool gated = p.z.p != nullptr;
-    const WT* z = gated ? static_cast<const WT*>(p.z.p) + static_cast<int64_t>(o.t0) * p.z.tok : d_o;
-    const int64_t z_tok = gated ? p.z.tok : q.d_o.tok;
+    const ScanRows zrow = gated ? p.z : q.d_o;
+    const uint32_t at = static_cast<uint32_t>(d) * sizeof(WT);
+    const uint32_t sx = scan_step<WT>(p.x), sd = scan_step<WT>(p.dt), so = scan_step<WT>(q.d_o),
+                   sz = scan_step<WT>(zrow);
     const int64_t b0 = static_cast<int64_t>(o.t0) * p.b.tok + static_cast<int64_t>(g) * p.b.grp + n0;
     const int64_t c0 = static_cast<int64_t>(o.t0) * p.c.tok + static_cast<int64_t>(g) * p.c.grp + n0;
     float* check = q.check + first_part(p, o) * (DN + p.D) + d;
@@ -122,14 +104,16 @@ __global__ void __launch_bounds__(kScanThreads) grad_sums(const ScanParams p, co
     constexpr int U = 4;
     WT xs[U], ds[U], os[U], zs[U];
     auto fetch = [&](int t) {
+        const char *bx = scan_base<WT>(p.x, o.t0 + t), *bd = scan_base<WT>(p.dt, o.t0 + t);
+        const char *bo = scan_base<WT>(q.d_o, o.t0 + t), *bz = scan_base<WT>(zrow, o.t0 + t);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            const int64_t u = min(t + i, o.n - 1);
-            xs[i] = (x + u * p.x.tok)[d];
-            ds[i] = (dt + u * p.dt.tok)[d];
+            const uint32_t k = min(i, o.n - 1 - t);
+            xs[i] = scan_at<WT>(bx, at + k * sx);
+            ds[i] = scan_at<WT>(bd, at + k * sd);
             if (rev) {
-                os[i] = (d_o + u * q.d_o.tok)[d];
-                zs[i] = (z + u * z_tok)[d];
+                os[i] = scan_at<WT>(bo, at + k * so);
+                zs[i] = scan_at<WT>(bz, at + k * sz);
             }
         }
     };
@@ -145,10 +129,10 @@ __global__ void __launch_bounds__(kScanThreads) grad_sums(const ScanParams p, co
         }
         if (t + U < o.n) fetch(t + U);
         if (t % kPart == 0 && t && live) {  // the state before part t / kPart
-            float* at = check + (t / kPart) * (DN + p.D);
+            float* to = check + (t / kPart) * (DN + p.D);
 #pragma unroll
-            for (int i = 0; i < N; ++i) at[static_cast<int64_t>(n0 + i) * p.D] = h[i];
-            if (n0 == 0) at[DN] = total;
+            for (int i = 0; i < N; ++i) to[static_cast<int64_t>(n0 + i) * p.D] = h[i];
+            if (n0 == 0) to[DN] = total;
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -197,6 +181,20 @@ __device__ __forceinline__ float state_at(const ScanState& s, int64_t outer, int
     const int64_t j = outer * s.outer + i;
     return s.bf16 ? scan_widen(static_cast<const uint16_t*>(s.p)[j])
                   : static_cast<const float*>(s.p)[j];
+}
+
+template <int N>
+__device__ __forceinline__ void state_row(const ScanState& s, int64_t outer, int64_t i,
+                                          float (&v)[N]) {
+    const int64_t j = outer * s.outer + i;
+    if (!s.p) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = 0.0f;
+    } else if (s.bf16) {
+        scan_load<N>(static_cast<const uint16_t*>(s.p) + j, v);
+    } else {
+        scan_load<N>(static_cast<const float*>(s.p) + j, v);
+    }
 }
 
 __global__ void __launch_bounds__(256) grad_chains(const ScanParams p, const ScanGrad q) {
@@ -274,18 +272,33 @@ __device__ __forceinline__ float sums32(float (&x)[16], float (&y)[16]) {
     return r[0] + dpp<0xB1>(r[0]);
 }
 
-// A token's raw operands of a part, all loaded before the first is used.
-template <typename WT> struct PartRows {
+// A part's raw operands, all loaded before the first is used; past the row's end
+// its last token again.
+template <typename WT, bool FULL> struct PartRows {
     WT v[kPart];
-    __device__ __forceinline__ void load(const void* base, int64_t tok, int64_t t0, int m, int d) {
-        const WT* at = static_cast<const WT*>(base) + t0 * tok;
+    __device__ __forceinline__ void load(const ScanRows& r, int64_t t0, int m, uint32_t off) {
+        const char* base = scan_base<WT>(r, t0);
+        const uint32_t step = scan_step<WT>(r);
+        asm volatile("" : "+v"(off));  // the same for every part: not kept in registers
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
-            v[i] = at[d];
-            at += i + 1 < m ? tok : 0;  // past the row's end: its last token again
+            v[i] = scan_at<WT>(base, off);
+            off += FULL || i + 1 < m ? step : 0;
         }
     }
 };
+template <typename WT, bool FULL>
+__device__ __forceinline__ void part_store(const ScanRows& r, int64_t t0, int m, uint32_t off,
+                                           const float (&v)[kPart]) {
+    char* base = const_cast<char*>(scan_base<WT>(r, t0));
+    const uint32_t step = scan_step<WT>(r);
+    asm volatile("" : "+v"(off));
+#pragma unroll
+    for (int i = 0; i < kPart; ++i) {
+        if (FULL || i < m) scan_put(reinterpret_cast<WT*>(base + off), v[i]);
+        off += step;
+    }
+}
 
 template <typename WT, int N, bool GATED>
 __global__ void __launch_bounds__(64 * grad_waves(N), 2)
@@ -314,24 +327,36 @@ grad_walk(const ScanParams p, const ScanGrad q) {
         return;
     }
     const bool cut = o.count > 1;
-    for (int n = 0; n < N; ++n) {
-        carry[wave][n][lane] = cut ? q.seg_rev[mine + static_cast<int64_t>(n) * p.D]
-                                   : state_at(q.dfinal, o.row, static_cast<int64_t>(d) * N + n);
-        da[wave][n][lane] = 0.0f;
+    {
+        float v[N];
+        if (cut) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = q.seg_rev[mine + static_cast<int64_t>(n) * p.D];
+        } else {
+            state_row<N>(q.dfinal, o.row, static_cast<int64_t>(d) * N, v);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            carry[wave][n][lane] = v[n];
+            da[wave][n][lane] = 0.0f;
+        }
     }
     const float bias = p.bias ? p.bias[d] : 0.0f;
     const float skip = p.skip ? p.skip[d] : 0.0f;
     float dskip = 0.0f, dbias = 0.0f;
+    const uint32_t at = static_cast<uint32_t>(d) * sizeof(WT);  // within a token
     const int64_t first = first_part(p, o);
     const float* check = q.check + first * (DN + p.D) + d;
-    for (int part = (o.n - 1) / kPart; o.n > 0 && part >= 0; --part) {
+    // One part; FULL: of kPart tokens.
+    auto walk = [&](int part, auto full) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)::value;
         const int64_t t0 = o.t0 + part * kPart;
         const int m = min(kPart, o.n - part * kPart);
-        PartRows<WT> xr, dr, gr, zr;
-        dr.load(p.dt.p, p.dt.tok, t0, m, d);
-        xr.load(p.x.p, p.x.tok, t0, m, d);
-        gr.load(q.d_o.p, q.d_o.tok, t0, m, d);
-        if constexpr (GATED) zr.load(p.z.p, p.z.tok, t0, m, d);
+        PartRows<WT, FULL> xr, dr, gr, zr;
+        dr.load(p.dt, t0, m, at);
+        xr.load(p.x, t0, m, at);
+        gr.load(q.d_o, t0, m, at);
+        if constexpr (GATED) zr.load(p.z, t0, m, at);
         const float* ck = check + part * (DN + p.D);
         const float since = part ? ck[DN] : 0.0f;  // step sizes from the segment's start
         const float* bc = q.turned + ((first + part) * p.G + g) * 2 * N * kPart;
@@ -352,14 +377,14 @@ grad_walk(const ScanParams p, const ScanGrad q) {
         }
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
-            const bool in = i < m && live;
+            const bool in = (FULL || i < m) && live;
             float gy = scan_value(gr.v[i]);
             if constexpr (GATED) {
                 const float zv = scan_value(zr.v[i]), sig = scan_sigmoid(zv);
                 gz[i] = gy * (sig * __builtin_fmaf(zv, 1.0f - sig, 1.0f));
                 gy *= zv * sig;
             }
-            delta[i] = i < m ? delta[i] : 0.0f;
+            delta[i] = FULL || i < m ? delta[i] : 0.0f;
             dy[i] = in ? gy : 0.0f;
             u[i] = in ? delta[i] * scan_value(xr.v[i]) : 0.0f;
             s1[i] = s2[i] = y[i] = 0.0f;
@@ -407,35 +432,37 @@ grad_walk(const ScanParams p, const ScanGrad q) {
             const float sum = sums32(a, h);
             if (!(lane & 1)) red[wave][n][lane >> 1] = sum;
         }
-        WT* dx = static_cast<WT*>(const_cast<void*>(q.dx.p)) + t0 * q.dx.tok;
-        WT* ddt = static_cast<WT*>(const_cast<void*>(q.ddt.p)) + t0 * q.ddt.tok;
-        WT* dz = static_cast<WT*>(const_cast<void*>(q.dz.p)) + t0 * q.dz.tok;
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
             const float xv = scan_value(xr.v[i]);
-            const float dd = i < m ? __builtin_fmaf(xv, s1[i], s2[i]) * slope[i] : 0.0f;
+            const float dd = FULL || i < m ? __builtin_fmaf(xv, s1[i], s2[i]) * slope[i] : 0.0f;
             dbias += dd;
             dskip = __builtin_fmaf(dy[i], xv, dskip);
-            if (i < m && live) {
-                scan_put(dx + d, __builtin_fmaf(skip, dy[i], delta[i] * s1[i]));
-                scan_put(ddt + d, dd);
-                if constexpr (GATED) scan_put(dz + d, gz[i] * __builtin_fmaf(skip, xv, y[i]));
-            }
-            dx += q.dx.tok;
-            ddt += q.ddt.tok;
-            if constexpr (GATED) dz += q.dz.tok;
+            s2[i] = dd;
+            s1[i] = __builtin_fmaf(skip, dy[i], delta[i] * s1[i]);
+            if constexpr (GATED) gz[i] *= __builtin_fmaf(skip, xv, y[i]);
+        }
+        if (live) {
+            part_store<WT, FULL>(q.dx, t0, m, at, s1);
+            part_store<WT, FULL>(q.ddt, t0, m, at, s2);
+            if constexpr (GATED) part_store<WT, FULL>(q.dz, t0, m, at, gz);
         }
         __syncthreads();
         for (int i = tid; i < 2 * kPart * N; i += kGradThreads) {
             const int n = i % N, v = i / N;  // v: dB's tokens, then dC's
             const int t = v % kPart;
-            if (t >= m) continue;
+            if (!FULL && t >= m) continue;
             float s = 0.0f;
 #pragma unroll
             for (int w = 0; w < kGradWaves; ++w) s += red[w][n][v];
             q.part_bc[((static_cast<int64_t>(gt) * p.T + t0 + t) * p.G + g) * 2 * N +
                       (v / kPart) * N + n] = s;
         }
+    };
+    const int parts = (o.n + kPart - 1) / kPart;
+    for (int part = parts - 1; part >= 0; --part) {
+        if ((part + 1) * kPart <= o.n) walk(part, std::true_type());
+        else walk(part, std::false_type());
     }
     if (!live) return;
     for (int n = 0; n < N; ++n) {

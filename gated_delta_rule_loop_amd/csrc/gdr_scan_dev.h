@@ -73,37 +73,74 @@ template <int n> __device__ __forceinline__ void scan_store(uint16_t* p, const f
     }
 }
 
-// e^x to about one float32 rounding: what x log2(e) loses to its rounding is
-// put back as a factor (the compensated product: 2^hi (1 + lo ln 2)).  Results
-// below 2^-126 are 0.
+// The value `off` bytes behind a wave-uniform base: one 32-bit register a lane.
+template <typename WT> __device__ __forceinline__ WT scan_at(const char* base, uint32_t off) {
+    return *reinterpret_cast<const WT*>(base + off);
+}
+template <typename WT>
+__device__ __forceinline__ const char* scan_base(const ScanRows& r, int64_t tok) {
+    return static_cast<const char*>(r.p) + tok * r.tok * static_cast<int64_t>(sizeof(WT));
+}
+template <typename WT> __device__ __forceinline__ uint32_t scan_step(const ScanRows& r) {
+    return static_cast<uint32_t>(r.tok) * static_cast<uint32_t>(sizeof(WT));
+}
+
+// e^x for finite x to about one float32 rounding: what x log2(e) loses to its
+// rounding is put back as a factor (the compensated product: 2^hi (1 + lo ln 2)).
+// Results below 2^-126 are 0.
 __device__ __forceinline__ float scan_exp(float x) {
-    x = x < -150.0f ? -150.0f : x;
-    x = x > 128.0f ? 128.0f : x;
     const float hi = x * kScanLog2e;
     const float lo = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, kScanLog2e, -hi));
     const float e = __builtin_amdgcn_exp2f(hi);
     return __builtin_fmaf(e, lo * 0.693147181f, e);
 }
+// 1 / (1 + e^-x); of NaN it is a number (callers multiply by x, which is none).
 __device__ __forceinline__ float scan_sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + scan_exp(-x));
+    return __builtin_amdgcn_rcpf(1.0f + scan_exp(__builtin_amdgcn_fmed3f(-x, -150.0f, 128.0f)));
 }
 // log(1 + e^x) = max(x, 0) + log(1 + t), t = e^-|x|.  log(1 + t) = 2 atanh(s) with
 // s = t / (2 + t) <= 1/3: an odd series in s, its tail after s fitted by a cubic
 // in s^2 (off by 1.6e-8 of the result at most), so that small t keep all their bits.
 // `slope`: its derivative, the sigmoid.
 __device__ __forceinline__ float scan_softplus(float x, float& slope) {
-    const float t = scan_exp(-__builtin_fabsf(x));
+    const float t = scan_exp(__builtin_fmaxf(-__builtin_fabsf(x), -150.0f));
     const float s = t * __builtin_amdgcn_rcpf(2.0f + t), v = s * s;
     float q = __builtin_fmaf(0.134337738f, v, 0.141169786f);
     q = __builtin_fmaf(q, v, 0.200038359f);
     q = __builtin_fmaf(q, v, 0.333333194f);
     const float l = __builtin_fmaf(2.0f * s, v * q, 2.0f * s);
     slope = (x > 0.0f ? 1.0f : t) * __builtin_amdgcn_rcpf(1.0f + t);
-    return (x > 0.0f ? x : 0.0f) + l;
+    return (x <= 0.0f ? 0.0f : x) + l;  // NaN stays NaN
 }
 __device__ __forceinline__ float scan_softplus(float x) {
     float slope;
     return scan_softplus(x, slope);
+}
+
+// A pointer whose loads at wave-uniform addresses are scalar loads.
+#define GDR_UNIFORM __attribute__((address_space(4)))
+
+// An index vector's element at a wave-uniform place.
+__device__ __forceinline__ uint32_t scan_index(const uint32_t* v, int64_t i) {
+    return *reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(v + i));
+}
+
+// N values of a [.., N] operand at a wave-uniform place.
+template <typename WT, int N>
+__device__ __forceinline__ void uniform_row(const void* base, int64_t elem, float (&v)[N]) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(elem) * sizeof(WT);
+    const GDR_UNIFORM uint32_t* q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(at);
+    if constexpr (sizeof(WT) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __uint_as_float(q[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const uint32_t w = q[i];
+            v[2 * i] = __uint_as_float(w << 16);
+            v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+        }
+    }
 }
 
 // The number of the segment that row b's tokens start with, when rows are cut
@@ -124,17 +161,17 @@ __device__ __forceinline__ bool scan_locate(const ScanParams& p, int seg, ScanSp
         o.row = seg;
         o.s = 0;
         o.count = 1;
-        o.t0 = static_cast<int>(p.offsets[seg]);
-        o.n = static_cast<int>(p.offsets[seg + 1]) - o.t0;
+        o.t0 = static_cast<int>(scan_index(p.offsets, seg));
+        o.n = static_cast<int>(scan_index(p.offsets, seg + 1)) - o.t0;
         return true;
     }
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {  // the last row whose first segment is at or before seg
         const int mid = (lo + hi + 1) >> 1;
-        if (scan_first_seg(p.offsets[mid], mid, p.seg_len) <= seg) lo = mid; else hi = mid - 1;
+        if (scan_first_seg(scan_index(p.offsets, mid), mid, p.seg_len) <= seg) lo = mid; else hi = mid - 1;
     }
-    const uint32_t a = p.offsets[lo];
-    const int n = static_cast<int>(p.offsets[lo + 1] - a);
+    const uint32_t a = scan_index(p.offsets, lo);
+    const int n = static_cast<int>(scan_index(p.offsets, lo + 1) - a);
     const int64_t first = scan_first_seg(a, lo, p.seg_len);
     o.row = lo;
     o.s = static_cast<int>(seg - first);

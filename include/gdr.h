@@ -482,9 +482,10 @@ int gdr_causal_conv1d_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gdr
  * arithmetic and sums.
  *
  * Common arguments
- *   x, dt, z, out     [T, D] work dtype: f32 or bf16; 16-byte rows at any
- *                     stride (halves of a projection's output can be given as
- *                     they are); D / G a multiple of 4.  z absent: no gate.
+ *   x, dt, z, out     [T, D] work dtype: f32 or bf16; 16-byte rows (halves of
+ *                     a projection's output can be given as they are); D / G a
+ *                     multiple of 4.  z absent: no gate.  Token strides here
+ *                     and of B and C are 0 to 2^24 - 1 elements.
  *   A                 [D, N] f32 contiguous; N in {8, 16, 32, 64}
  *   B, C              [T, G, N] work, unit stride over N, 16-byte rows
  *   D, dt_bias        [D] f32 or absent (zeros)

@@ -114,6 +114,8 @@ def _scan_args(**over):
     (dict(z=D([200, 64], stride=[130, 1])), -2, "multiple of 4"),
     (dict(x=D([200, 64], data=FAKE + 8)), -2, "aligned"),
     (dict(x=D([200, 64], stride=[128, 2])), -2, "innermost"),
+    (dict(x=D([200, 64], data=FAKE * 64, stride=[-64, 1])), -2, "x has a token stride"),
+    (dict(C=D([200, 2, 16], stride=[2 ** 24, 16, 1])), -2, "C has a token stride"),
     (dict(out=D([200, 64], data=FAKE * 2, stride=[32, 1])), -1, "overlap"),
     (dict(out=D([200, 64])), -1, "alias"),
     (dict(off=D([0], I32)), -1, "empty"),
