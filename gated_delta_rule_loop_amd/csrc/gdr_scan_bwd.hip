@@ -29,7 +29,7 @@ namespace {
 constexpr int kPart = kScanPart;
 // Waves of a gradient's workgroup: carried sums of every state take 512 bytes of
 // LDS a wave and state, so that 64 states leave room for two.
-constexpr int grad_waves(int N) { return N > 32 ? 2 : 4; }
+constexpr int grad_waves(int N) { return N > 32 ? 1 : N > 16 ? 2 : 4; }
 // States that one workgroup of the first launch carries.
 constexpr int sum_states(int N) { return N < 16 ? N : 16; }
 
@@ -301,11 +301,13 @@ __device__ __forceinline__ void part_store(const ScanRows& r, int64_t t0, int m,
 }
 
 template <typename WT, int N, bool GATED>
-__global__ void __launch_bounds__(64 * grad_waves(N), 2)
+__global__ void __launch_bounds__(64 * grad_waves(N), N > 16 ? 1 : 2)
 grad_walk(const ScanParams p, const ScanGrad q) {
     constexpr int kGradWaves = grad_waves(N), kGradThreads = 64 * kGradWaves;
-    __shared__ float carry[kGradWaves][N][64], da[kGradWaves][N][64];
-    __shared__ float red[kGradWaves][N][2 * kPart];
+    // a lane's own: what comes from behind, A, dA so far, the state before the part
+    __shared__ float carry[kGradWaves][N][64], as[kGradWaves][N][64], da[kGradWaves][N][64];
+    __shared__ float hs[kGradWaves][N][64];
+    __shared__ float red[kGradWaves][N][2 * kPart + 1];
     const int gtiles = q.tiles, ctiles = p.G * gtiles;
     const int seg = blockIdx.x / ctiles, tile = blockIdx.x - seg * ctiles;
     const int g = tile / gtiles, gt = tile - g * gtiles;
@@ -328,7 +330,8 @@ grad_walk(const ScanParams p, const ScanGrad q) {
     }
     const bool cut = o.count > 1;
     {
-        float v[N];
+        float v[N], a[N];
+        scan_load<N>(p.A + static_cast<int64_t>(d) * N, a);
         if (cut) {
 #pragma unroll
             for (int n = 0; n < N; ++n) v[n] = q.seg_rev[mine + static_cast<int64_t>(n) * p.D];
@@ -338,6 +341,7 @@ grad_walk(const ScanParams p, const ScanGrad q) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             carry[wave][n][lane] = v[n];
+            as[wave][n][lane] = a[n];
             da[wave][n][lane] = 0.0f;
         }
     }
@@ -358,31 +362,43 @@ grad_walk(const ScanParams p, const ScanGrad q) {
         gr.load(q.d_o, t0, m, at);
         if constexpr (GATED) zr.load(p.z, t0, m, at);
         const float* ck = check + part * (DN + p.D);
-        const float since = part ? ck[DN] : 0.0f;  // step sizes from the segment's start
+        {   // all of the states' loads at once
+            float st[N], at_part[N];
+            if (cut) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) st[n] = p.seg_state[mine + static_cast<int64_t>(n) * p.D];
+            } else {
+                state_row<N>(p.in, o.row, static_cast<int64_t>(d) * N, st);
+            }
+            if (part) {
+                const float since = ck[DN] * kScanLog2e;  // step sizes from the segment's start
+#pragma unroll
+                for (int n = 0; n < N; ++n) at_part[n] = ck[static_cast<int64_t>(n) * p.D];
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+                    st[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(as[wave][n][lane] * since), st[n],
+                                           at_part[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) hs[wave][n][lane] = st[n];
+        }
         const float* bc = q.turned + ((first + part) * p.G + g) * 2 * N * kPart;
-        // delta, its slope, delta x, dy, dout times the gate's slope, and the sums over n.
+        // delta, delta x, dy, and the sums over n.
         // Tokens past the row's end have no step and no gradient.
-        float delta[kPart], slope[kPart], u[kPart], dy[kPart], gz[kPart];
-        float s1[kPart], s2[kPart], y[kPart];
+        float delta[kPart], u[kPart], dy[kPart], s1[kPart], s2[kPart], y[kPart];
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) delta[i] = scan_value(dr.v[i]) + bias;
         if (p.softplus) {
 #pragma unroll
-            for (int i = 0; i < kPart; ++i)
-                delta[i] = scan_softplus(scan_value(dr.v[i]) + bias, slope[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPart; ++i) {
-                delta[i] = scan_value(dr.v[i]) + bias;
-                slope[i] = 1.0f;
-            }
+            for (int i = 0; i < kPart; ++i) delta[i] = scan_softplus(delta[i]);
         }
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
             const bool in = (FULL || i < m) && live;
             float gy = scan_value(gr.v[i]);
             if constexpr (GATED) {
-                const float zv = scan_value(zr.v[i]), sig = scan_sigmoid(zv);
-                gz[i] = gy * (sig * __builtin_fmaf(zv, 1.0f - sig, 1.0f));
-                gy *= zv * sig;
+                const float zv = scan_value(zr.v[i]);
+                gy *= zv * scan_sigmoid(zv);
             }
             delta[i] = FULL || i < m ? delta[i] : 0.0f;
             dy[i] = in ? gy : 0.0f;
@@ -390,23 +406,46 @@ grad_walk(const ScanParams p, const ScanGrad q) {
             s1[i] = s2[i] = y[i] = 0.0f;
         }
         __syncthreads();  // the sums of the part before have been read
-        float an1, st1, ck1 = 0.0f;  // the next state's operands
-        auto fetch = [&](int n) {
-            const int64_t nd = static_cast<int64_t>(n) * p.D, dn = static_cast<int64_t>(d) * N + n;
-            an1 = p.A[dn];
-            st1 = cut ? p.seg_state[mine + nd] : state_at(p.in, o.row, dn);
-            if (part) ck1 = ck[nd];
-        };
-        fetch(0);
+        // The next state's operands are fetched a state ahead (gradients of 2 x 2048 tokens
+        // without a gate 315 us, 338 without; 1024 channels of 64 states 295 and 334), but not
+        // with a gate and few states, where registers run out (402 us, 384 without).
+        constexpr bool AHEAD = !GATED || N > 16;
+        float b1[kPart], c1[kPart], an1, st1, mu1;
+        if constexpr (AHEAD) {
+            uniform_row<float, kPart>(bc, 0, b1);
+            uniform_row<float, kPart>(bc, N * kPart, c1);
+            an1 = as[wave][0][lane];
+            st1 = hs[wave][0][lane];
+            mu1 = carry[wave][0][lane];
+        }
         for (int n = 0; n < N; ++n) {
-            const float an = an1, a2 = an * kScanLog2e;
-            const float start = part ? __builtin_fmaf(__builtin_amdgcn_exp2f(a2 * since), st1, ck1)
-                                     : st1;
-            if (n + 1 < N) fetch(n + 1);
-            float mu = carry[wave][n][lane];
+            if constexpr (!AHEAD) {
+                an1 = as[wave][n][lane];
+                st1 = hs[wave][n][lane];
+                mu1 = carry[wave][n][lane];
+            }
+            const float an = an1, a2 = an * kScanLog2e, start = st1;
+            float mu = mu1;
+            if (AHEAD && n + 1 < N) {
+                an1 = as[wave][n + 1][lane];
+                st1 = hs[wave][n + 1][lane];
+                mu1 = carry[wave][n + 1][lane];
+            }
             float b[kPart], c[kPart];
-            uniform_row<float, kPart>(bc, n * kPart, b);
-            uniform_row<float, kPart>(bc, (N + n) * kPart, c);
+            if constexpr (AHEAD) {
+#pragma unroll
+                for (int i = 0; i < kPart; ++i) {
+                    b[i] = b1[i];
+                    c[i] = c1[i];
+                }
+                if (n + 1 < N) {
+                    uniform_row<float, kPart>(bc, (n + 1) * kPart, b1);
+                    uniform_row<float, kPart>(bc, (N + n + 1) * kPart, c1);
+                }
+            } else {
+                uniform_row<float, kPart>(bc, n * kPart, b);
+                uniform_row<float, kPart>(bc, (N + n) * kPart, c);
+            }
             float a[kPart], h[kPart], hp = start;
 #pragma unroll
             for (int i = 0; i < kPart; ++i) {
@@ -432,20 +471,42 @@ grad_walk(const ScanParams p, const ScanGrad q) {
             const float sum = sums32(a, h);
             if (!(lane & 1)) red[wave][n][lane >> 1] = sum;
         }
+        // The raw operands once more (from the caches): kept through the loop above they
+        // would take 48 registers that it does not have.
+        xr.load(p.x, t0, m, at);
+        if (p.softplus) {
+            dr.load(p.dt, t0, m, at);
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+                float slope;
+                scan_softplus(scan_value(dr.v[i]) + bias, slope);
+                s2[i] = __builtin_fmaf(scan_value(xr.v[i]), s1[i], s2[i]) * slope;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) s2[i] = __builtin_fmaf(scan_value(xr.v[i]), s1[i], s2[i]);
+        }
 #pragma unroll
         for (int i = 0; i < kPart; ++i) {
             const float xv = scan_value(xr.v[i]);
-            const float dd = FULL || i < m ? __builtin_fmaf(xv, s1[i], s2[i]) * slope[i] : 0.0f;
-            dbias += dd;
+            dbias += FULL || i < m ? s2[i] : 0.0f;
             dskip = __builtin_fmaf(dy[i], xv, dskip);
-            s2[i] = dd;
             s1[i] = __builtin_fmaf(skip, dy[i], delta[i] * s1[i]);
-            if constexpr (GATED) gz[i] *= __builtin_fmaf(skip, xv, y[i]);
+            if constexpr (GATED) y[i] = __builtin_fmaf(skip, xv, y[i]);
+        }
+        if constexpr (GATED) {
+            gr.load(q.d_o, t0, m, at);
+            zr.load(p.z, t0, m, at);
+#pragma unroll
+            for (int i = 0; i < kPart; ++i) {
+                const float zv = scan_value(zr.v[i]), sig = scan_sigmoid(zv);
+                y[i] *= scan_value(gr.v[i]) * (sig * __builtin_fmaf(zv, 1.0f - sig, 1.0f));
+            }
         }
         if (live) {
             part_store<WT, FULL>(q.dx, t0, m, at, s1);
             part_store<WT, FULL>(q.ddt, t0, m, at, s2);
-            if constexpr (GATED) part_store<WT, FULL>(q.dz, t0, m, at, gz);
+            if constexpr (GATED) part_store<WT, FULL>(q.dz, t0, m, at, y);
         }
         __syncthreads();
         for (int i = tid; i < 2 * kPart * N; i += kGradThreads) {
