@@ -40,7 +40,8 @@ struct ScanParams {
     int32_t narrow_most;            // rows up to this many tokens are taken by the narrow walk
     int32_t hand_on;                // the narrow walk writes the states of empty rows too
     // long rows, cut into segments of seg_len tokens (0: none is cut)
-    int32_t seg_len, segs, tiles;   // tiles: workgroups over one group's channels
+    int32_t seg_skip;               // rows up to this many tokens have no segment
+    int32_t seg_len, segs, tiles;   // tiles: waves over one group's channels
     float* seg_state;               // [segs, D, N]
     float* seg_delta;               // [segs, D]
 };
@@ -92,7 +93,9 @@ struct DraftParams {
     double* part;                   // sampled: [B, 2, splits]; greedy: [T, splits] pairs
 };
 
-constexpr int kScanThreads = 64;
+// Workgroups of four waves that need nothing of one another: one for each SIMD.
+constexpr int kScanThreads = 256;
+inline unsigned scan_blocks(int64_t waves) { return static_cast<unsigned>((waves + 3) / 4); }
 constexpr int kScanNarrowThreads = 256;
 constexpr int kScanPart = 16;       // tokens that a gradient holds in registers
 int scan_grad_channels(int N);      // channels of a gradient's workgroup

@@ -16,6 +16,8 @@
 // Narrow walk (single tokens, drafted windows, folds): a lane owns 16 bytes of a
 // channel's state, so that states are read and written in whole lines; the
 // output is summed over a channel's 1 to 16 lanes by lane permutations.
+#include <type_traits>
+
 #include "gdr_scan_dev.h"
 
 namespace gdr {
@@ -40,7 +42,8 @@ template <typename WT, int S> struct Token {  // one token's operands of a lane
     float x, dt, z, b[S], c[S];
 };
 
-template <typename WT, typename ST, int N, bool OUT>
+// U: tokens whose operands are loaded ahead of those in work.
+template <typename WT, typename ST, int N, bool OUT, int U>
 __global__ void __launch_bounds__(kScanNarrowThreads) scan_narrow(const ScanParams p) {
     constexpr int S = N < static_cast<int>(16 / sizeof(ST)) ? N : 16 / sizeof(ST);
     constexpr int L = N / S;                       // lanes a channel
@@ -95,25 +98,36 @@ __global__ void __launch_bounds__(kScanNarrowThreads) scan_narrow(const ScanPara
     };
 #pragma unroll
     for (int i = 0; i < S; ++i) a2[i] *= kScanLog2e;
-    Token<WT, S> next;
-    if (n > 0) fetch(0, next);
-    for (int t = 0; t < n; ++t) {
-        const Token<WT, S> k = next;
-        if (t + 1 < n) fetch(t + 1, next);
-        float delta = k.dt + bias;
-        if (p.softplus) delta = scan_softplus(delta);
-        const float u = delta * k.x;
-        float y = 0.0f;
+    Token<WT, S> next[U];
+    auto fetch_all = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[i]), h[i], u * k.b[i]);
-            if constexpr (OUT) y = __builtin_fmaf(h[i], k.c[i], y);
-        }
-        if constexpr (OUT) {
-            y = __builtin_fmaf(skip, k.x, lane_sum<L>(y));
-            if (z) y *= k.z * scan_sigmoid(k.z);
-            if (sub == 0)
-                scan_put(static_cast<WT*>(p.out) + static_cast<int64_t>(t0 + t) * p.o_tok + d, y);
+        for (int j = 0; j < U; ++j) fetch(min(t + j, n - 1), next[j]);
+    };
+    if (n > 0) fetch_all(0);
+    for (int t = 0; t < n; t += U) {
+        Token<WT, S> now[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) now[j] = next[j];
+        if (t + U < n) fetch_all(t + U);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (t + j >= n) break;
+            const Token<WT, S>& k = now[j];
+            float delta = k.dt + bias;
+            if (p.softplus) delta = scan_softplus(delta);
+            const float u = delta * k.x;
+            float y = 0.0f;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[i]), h[i], u * k.b[i]);
+                if constexpr (OUT) y = __builtin_fmaf(h[i], k.c[i], y);
+            }
+            if constexpr (OUT) {
+                y = __builtin_fmaf(skip, k.x, lane_sum<L>(y));
+                if (z) y *= k.z * scan_sigmoid(k.z);
+                if (sub == 0)
+                    scan_put(static_cast<WT*>(p.out) + static_cast<int64_t>(t0 + t + j) * p.o_tok + d, y);
+            }
         }
     }
     if (p.last && !p.keep)
@@ -125,10 +139,16 @@ hipError_t narrow_out(const ScanParams& p, hipStream_t s) {
     constexpr int S = N < static_cast<int>(16 / sizeof(ST)) ? N : 16 / sizeof(ST);
     const int per = kScanNarrowThreads / (N / S);
     const dim3 grid(static_cast<unsigned>(p.B) * ((p.D + per - 1) / per));
-    if (p.out)
-        hipLaunchKernelGGL((scan_narrow<WT, ST, N, true>), grid, dim3(kScanNarrowThreads), 0, s, p);
+    // rows of about one token have nothing to load ahead for
+    const bool one = p.T <= p.B + p.B / 2;
+    if (p.out && one)
+        hipLaunchKernelGGL((scan_narrow<WT, ST, N, true, 1>), grid, dim3(kScanNarrowThreads), 0, s, p);
+    else if (p.out)
+        hipLaunchKernelGGL((scan_narrow<WT, ST, N, true, 4>), grid, dim3(kScanNarrowThreads), 0, s, p);
+    else if (one)
+        hipLaunchKernelGGL((scan_narrow<WT, ST, N, false, 1>), grid, dim3(kScanNarrowThreads), 0, s, p);
     else
-        hipLaunchKernelGGL((scan_narrow<WT, ST, N, false>), grid, dim3(kScanNarrowThreads), 0, s, p);
+        hipLaunchKernelGGL((scan_narrow<WT, ST, N, false, 4>), grid, dim3(kScanNarrowThreads), 0, s, p);
     return hipGetLastError();
 }
 
@@ -146,16 +166,48 @@ template <typename WT, typename ST> hipError_t narrow_n(const ScanParams& p, hip
 
 constexpr int kAhead = 4;  // tokens whose x, dt and z are loaded before those in work
 
+// B and C of some tokens as they stand in memory, in scalar registers.
+template <typename WT, int N, int S, bool TWO> struct ScalarRows {
+    static constexpr int R = N * static_cast<int>(sizeof(WT)) / 4;
+    uint32_t b[S][R], c[S][TWO ? R : 1];
+    __device__ __forceinline__ void load(const char* pb, const char* pc, uint32_t sb, uint32_t sc,
+                                         int t, int n) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const uint64_t u = static_cast<uint64_t>(min(t + i, n - 1));
+            const GDR_UNIFORM uint32_t* q =
+                reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(pb) + u * sb);
+#pragma unroll
+            for (int k = 0; k < R; ++k) b[i][k] = q[k];
+            if constexpr (TWO) {
+                q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(pc) + u * sc);
+#pragma unroll
+                for (int k = 0; k < R; ++k) c[i][k] = q[k];
+            }
+        }
+    }
+    // Scalar loads return in any order, so that a wait for one is a wait for all: these
+    // have to be there before the next are asked for.
+    __device__ __forceinline__ void arrive() {
+        asm volatile("" : "+s"(b[S - 1][R - 1]));
+        if constexpr (TWO) asm volatile("" : "+s"(c[S - 1][R - 1]));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    static __device__ __forceinline__ float value(const uint32_t (&r)[R], int i) {
+        if constexpr (sizeof(WT) == 4) return __uint_as_float(r[i]);
+        return __uint_as_float(i & 1 ? r[i / 2] & 0xFFFF0000u : r[i / 2] << 16);
+    }
+};
+
 template <typename WT, int N, bool SUMS>
 __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
-    const int ctiles = p.G * p.tiles;
-    const int seg = blockIdx.x / ctiles, tile = blockIdx.x - seg * ctiles;
+    const int ctiles = p.G * p.tiles, wave = scan_wave();
+    const int seg = wave / ctiles, tile = wave - seg * ctiles;
     ScanSpan o;
-    if (!scan_locate(p, seg, o)) return;
-    if (o.n <= 0 || (o.count == 1 && o.n <= p.narrow_most)) return;
+    if (seg >= p.segs || !scan_locate(p, seg, o)) return;
     if (SUMS && o.s == o.count - 1) return;
     const int g = tile / p.tiles;
-    const int cg = (tile - g * p.tiles) * kScanThreads + static_cast<int>(threadIdx.x);
+    const int cg = (tile - g * p.tiles) * 64 + static_cast<int>(threadIdx.x & 63);
     const bool live = cg < p.gd;
     const int d = g * p.gd + min(cg, p.gd - 1);
     const uint32_t slot = p.slot_idx ? scan_index(p.slot_idx, o.row) : static_cast<uint32_t>(o.row);
@@ -185,56 +237,69 @@ __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
     }
     const float bias = p.bias ? p.bias[d] : 0.0f;
     const float skip = !SUMS && p.skip ? p.skip[d] : 0.0f;
-    const WT* x = static_cast<const WT*>(p.x.p) + static_cast<int64_t>(o.t0) * p.x.tok;
-    const WT* dt = static_cast<const WT*>(p.dt.p) + static_cast<int64_t>(o.t0) * p.dt.tok;
     const bool gated = !SUMS && p.z.p != nullptr;
-    const WT* z = gated ? static_cast<const WT*>(p.z.p) + static_cast<int64_t>(o.t0) * p.z.tok : x;
-    const int64_t z_tok = gated ? p.z.tok : p.x.tok;
-    WT* out = static_cast<WT*>(p.out) + (SUMS ? 0 : static_cast<int64_t>(o.t0) * p.o_tok);
-    const int64_t b0 = static_cast<int64_t>(o.t0) * p.b.tok + static_cast<int64_t>(g) * p.b.grp;
-    const int64_t c0 = SUMS ? 0 : static_cast<int64_t>(o.t0) * p.c.tok + static_cast<int64_t>(g) * p.c.grp;
+    const ScanRows zrow = gated ? p.z : p.x;
+    const uint32_t off = static_cast<uint32_t>(d) * sizeof(WT);
+    const uint32_t sx = scan_step<WT>(p.x), sd = scan_step<WT>(p.dt), sz = scan_step<WT>(zrow);
+    const ScanRows orow = {p.out, p.o_tok};
+    char* out = const_cast<char*>(scan_base<WT>(orow, o.t0));
+    const uint32_t so = scan_step<WT>(orow);
+    const char* pb = static_cast<const char*>(p.b.p) +
+                     (static_cast<int64_t>(o.t0) * p.b.tok + static_cast<int64_t>(g) * p.b.grp) * static_cast<int64_t>(sizeof(WT));
+    const char* pc = SUMS ? pb : static_cast<const char*>(p.c.p) +
+                     (static_cast<int64_t>(o.t0) * p.c.tok + static_cast<int64_t>(g) * p.c.grp) * static_cast<int64_t>(sizeof(WT));
+    const uint32_t sb = static_cast<uint32_t>(p.b.tok) * sizeof(WT);
+    const uint32_t sc = static_cast<uint32_t>(p.c.tok) * sizeof(WT);
     WT xs[kAhead], ds[kAhead], zs[kAhead];
     auto fetch = [&](int t) {
+        const char *bx = scan_base<WT>(p.x, o.t0 + t), *bd = scan_base<WT>(p.dt, o.t0 + t);
+        const char* bz = scan_base<WT>(zrow, o.t0 + t);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            const int64_t u = min(t + i, o.n - 1);
-            xs[i] = (x + u * p.x.tok)[d];
-            ds[i] = (dt + u * p.dt.tok)[d];
-            if constexpr (!SUMS) zs[i] = (z + u * z_tok)[d];
+            const uint32_t k = min(i, o.n - 1 - t);
+            xs[i] = scan_at<WT>(bx, off + k * sx);
+            ds[i] = scan_at<WT>(bd, off + k * sd);
+            if constexpr (!SUMS) zs[i] = scan_at<WT>(bz, off + k * sz);
         }
     };
     float total = 0.0f;
-    auto token = [&](int t, WT xr, WT dr, WT zr) {
+    // B and C are loaded S tokens ahead, as many as two sets of them leave scalar registers.
+    constexpr int R = N * static_cast<int>(sizeof(WT)) / 4;
+    constexpr int S = R <= 8 ? 2 : 1;
+    typedef ScalarRows<WT, N, S, !SUMS> Rows;
+    auto token = [&](const Rows& r, int i, WT xr, WT dr, WT zr, char* to) {
         const float xv = scan_value(xr);
         float delta = scan_value(dr) + bias;
         if (p.softplus) delta = scan_softplus(delta);
         const float u = delta * xv;
-        float b[N];
-        uniform_row<WT, N>(p.b.p, b0 + t * p.b.tok, b);
         if constexpr (SUMS) {
             total += delta;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[i]), h[i], u * b[i]);
+            for (int k = 0; k < N; ++k)
+                h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[k]), h[k],
+                                      u * Rows::value(r.b[i], k));
         } else {
-            float c[N], y0 = 0.0f, y1 = 0.0f;
-            uniform_row<WT, N>(p.c.p, c0 + t * p.c.tok, c);
+            float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[i]), h[i], u * b[i]);
-                if (i & 1) y1 = __builtin_fmaf(h[i], c[i], y1);
-                else y0 = __builtin_fmaf(h[i], c[i], y0);
+            for (int k = 0; k < N; ++k) {
+                h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[k]), h[k],
+                                      u * Rows::value(r.b[i], k));
+                if (k & 1) y1 = __builtin_fmaf(h[k], Rows::value(r.c[i], k), y1);
+                else y0 = __builtin_fmaf(h[k], Rows::value(r.c[i], k), y0);
             }
             float y = __builtin_fmaf(skip, xv, y0 + y1);
             if (gated) {
                 const float zv = scan_value(zr);
                 y *= zv * scan_sigmoid(zv);
             }
-            if (live) scan_put(out + t * p.o_tok + d, y);
+            if (live) scan_put(reinterpret_cast<WT*>(to + off), y);
         }
     };
     fetch(0);
-    for (int t = 0; t < o.n; t += kAhead) {
+    Rows rows[2];
+    rows[0].load(pb, pc, sb, sc, 0, o.n);
+    auto block = [&](int t, auto full) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)::value;
         WT xc[kAhead], dc[kAhead], zc[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
@@ -244,9 +309,21 @@ __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
         }
         if (t + kAhead < o.n) fetch(t + kAhead);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (t + i < o.n) token(t + i, xc[i], dc[i], SUMS ? xc[i] : zc[i]);
-    }
+        for (int i = 0; i < kAhead; i += S) {
+            Rows &now = rows[(i / S) & 1], &next = rows[(i / S + 1) & 1];
+            now.arrive();
+            next.load(pb, pc, sb, sc, t + i + S, o.n);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (FULL || t + i + j < o.n)
+                    token(now, j, xc[i + j], dc[i + j], SUMS ? xc[i + j] : zc[i + j],
+                          out + static_cast<uint64_t>(t + i + j) * so);
+        }
+    };
+    int t = 0;
+    for (; t + kAhead <= o.n; t += kAhead) block(t, std::true_type());
+    if (t < o.n) block(t, std::false_type());
     if (!live) return;
     if constexpr (SUMS) {
         scan_store<N>(p.seg_state + mine, h);
@@ -265,13 +342,13 @@ __global__ void __launch_bounds__(256) scan_chain(const ScanParams p) {
     const int blocks = static_cast<int>((DN + 255) / 256);
     const int row = blockIdx.x / blocks;
     const int64_t i = static_cast<int64_t>(blockIdx.x - row * blocks) * 256 + threadIdx.x;
-    const uint32_t a = p.offsets[row];
-    const int n = static_cast<int>(p.offsets[row + 1] - a);
-    if (i >= DN || n <= p.seg_len) return;
+    const int n = static_cast<int>(p.offsets[row + 1] - p.offsets[row]);
+    if (n <= p.seg_len) return;
+    const int64_t first = scan_first_seg(p, row);
+    if (i >= DN) return;
     const uint32_t slot = p.slot_idx ? p.slot_idx[row] : static_cast<uint32_t>(row);
     if (p.slot_idx != nullptr && slot == kPadSlot) return;
     const int count = (n + p.seg_len - 1) / p.seg_len;
-    const int64_t first = scan_first_seg(a, row, p.seg_len);
     const float a2 = p.A[i] * kScanLog2e;
     float h = 0.0f;
     if (p.in.p) {
@@ -301,7 +378,7 @@ __global__ void __launch_bounds__(256) scan_chain(const ScanParams p) {
 }
 
 template <typename WT, int N> hipError_t wide_sums(const ScanParams& p, bool sums, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.segs) * p.G * p.tiles);
+    const dim3 grid(scan_blocks(static_cast<int64_t>(p.segs) * p.G * p.tiles));
     if (sums)
         hipLaunchKernelGGL((scan_wide<WT, N, true>), grid, dim3(kScanThreads), 0, s, p);
     else

@@ -23,7 +23,7 @@ constexpr int64_t kMaxChannels = int64_t{1} << 24;
 struct ScanDims {
     int64_t T, D, N, G, B;
     int32_t work;
-    int64_t tiles() const { return ceil_div(D / G, kScanThreads); }
+    int64_t tiles() const { return ceil_div(D / G, 64); }
 };
 
 // [T, D] operand: unit innermost stride, 16-byte rows.
@@ -196,15 +196,18 @@ struct FwdPlan {
     bool wide;
 };
 
+constexpr int64_t kNarrowAll = 64;  // tokens of a call up to which every row goes narrowly
+
 FwdPlan fwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
     FwdPlan p{};
-    const int64_t ctiles = G * ceil_div(D / G, kScanThreads);
-    p.narrow = T <= 64 ? 64 : B > 8 ? 16 : 0;
-    p.wide = T > 64;
+    const int64_t ctiles = G * ceil_div(D / G, 64);
+    p.narrow = T <= kNarrowAll ? kNarrowAll : B > 8 ? 16 : 0;
+    p.wide = T > kNarrowAll;
     p.segs = B;
     if (p.wide) {
-        const int64_t want = std::max<int64_t>(1, 2048 / ctiles);
-        const int64_t len = std::max<int64_t>(64, round_up(ceil_div(T, want), 16));
+        const bool full = B * ctiles >= 2048;
+        const int64_t want = std::max<int64_t>(1, (full ? 1024 : 8192) / ctiles);
+        const int64_t len = std::max<int64_t>(16, round_up(ceil_div(T, want), 16));
         if (len < T) {
             p.seg_len = len;
             p.segs = T / len + B;
@@ -372,6 +375,7 @@ int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr
     set_states(p, initial_state, final_state, state);
     p.narrow_most = static_cast<int32_t>(pl.narrow);
     p.hand_on = present(final_state);  // also of rows without tokens
+    p.seg_skip = p.narrow_most;
     p.seg_len = static_cast<int32_t>(pl.seg_len);
     p.segs = static_cast<int32_t>(pl.segs);
     if (pl.seg_len) {
@@ -379,7 +383,7 @@ int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr
         p.seg_delta = p.seg_state + pl.delta;
     }
     if ((rc = check_grid(fn, narrow_blocks(d, p.in.bf16), kScanNarrowThreads)) ||
-        (pl.wide && (rc = check_grid(fn, pl.segs * d.G * d.tiles(), kScanThreads))) ||
+        (pl.wide && (rc = check_grid(fn, ceil_div(pl.segs * d.G * d.tiles(), 4), kScanThreads))) ||
         (pl.seg_len && (rc = check_grid(fn, d.B * ceil_div(d.D * d.N, 256), 256))) ||
         (rc = run_debug_check(fn, d.B, index_check(d, input_row_offsets, state, slot_idx), stream)))
         return rc;
@@ -505,6 +509,7 @@ int gdr_selective_scan_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gd
     p.c = heads_of(Cm);
     p.skip = floats(D);
     p.in = state_of(initial_state);
+    p.seg_skip = -1;  // rows without tokens too: they hand on the state's gradient
     p.seg_len = static_cast<int32_t>(pl.seg_len);
     p.segs = static_cast<int32_t>(pl.segs);
     float* ws = present(workspace) ? static_cast<float*>(workspace->data) : nullptr;
@@ -535,7 +540,8 @@ int gdr_selective_scan_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gd
     g.part_d = ws + pl.dd;
     const int64_t threads = scan_grad_channels(static_cast<int>(d.N));
     const int64_t DN = d.D * d.N;
-    if ((rc = check_grid(fn, pl.segs * d.G * ((d.N > 16 ? d.N / 16 : 1) * d.tiles() + 1), kScanThreads)) ||
+    if ((rc = check_grid(fn, ceil_div(pl.segs * d.G * ((d.N > 16 ? d.N / 16 : 1) * d.tiles() + 1), 4),
+                         kScanThreads)) ||
         (rc = check_grid(fn, 2 * d.B * ceil_div(DN, 256), 256)) ||
         (rc = check_grid(fn, pl.segs * d.G * pl.gtiles, threads)) ||
         (rc = check_grid(fn, ceil_div(d.T * d.G * 2 * d.N, 256) + ceil_div(DN, 256) +

@@ -30,12 +30,12 @@ constexpr int kPart = kScanPart;
 // Waves of a gradient's workgroup: carried sums of every state take 512 bytes of
 // LDS a wave and state, so that 64 states leave room for two.
 constexpr int grad_waves(int N) { return N > 32 ? 1 : N > 16 ? 2 : 4; }
-// States that one workgroup of the first launch carries.
+// States that one wave of the first launch carries.
 constexpr int sum_states(int N) { return N < 16 ? N : 16; }
 
 // The number of a segment's first part (segments are whole parts but for a row's last).
 __device__ __forceinline__ int64_t first_part(const ScanParams& p, const ScanSpan& o) {
-    return scan_first_seg(scan_index(p.offsets, o.row), o.row, kPart) + static_cast<int64_t>(o.s) * (p.seg_len / kPart);
+    return scan_first_part(scan_index(p.offsets, o.row), o.row, kPart) + static_cast<int64_t>(o.s) * (p.seg_len / kPart);
 }
 
 // ------------------------------------------------------------ 1: own sums ---
@@ -49,7 +49,7 @@ __device__ __forceinline__ void turn_parts(const ScanParams& p, const ScanGrad& 
     for (int part = 0; part * kPart < o.n; ++part) {
         const int m = o.n - part * kPart;
         float* to = q.turned + ((first + part) * p.G + g) * 2 * p.N * kPart;
-        for (int i = threadIdx.x; i < 2 * p.N * kPart; i += kScanThreads) {
+        for (int i = threadIdx.x & 63; i < 2 * p.N * kPart; i += 64) {
             const int n = i % p.N, v = i / p.N, t = v % kPart;  // v: B's tokens, then C's
             const ScanHeads& from = v < kPart ? p.b : p.c;
             float x = 0.0f;
@@ -62,23 +62,24 @@ __device__ __forceinline__ void turn_parts(const ScanParams& p, const ScanGrad& 
     }
 }
 
-// N: the states of this workgroup, of the channels' p.N.
+// N: the states of this wave, of the channels' p.N.
 template <typename WT, int N>
 __global__ void __launch_bounds__(kScanThreads, 3) grad_sums(const ScanParams p, const ScanGrad q) {
-    const int ctiles = p.G * p.tiles, nblocks = p.N / N;
-    const int block = blockIdx.x / ctiles, tile = blockIdx.x - block * ctiles;
+    const int ctiles = p.G * p.tiles, nblocks = p.N / N, wave = scan_wave();
+    const int block = wave / ctiles, tile = wave - block * ctiles;
     const int seg = block / nblocks, n0 = (block - seg * nblocks) * N;
     ScanSpan o;
-    if (seg >= p.segs) {  // the last workgroups turn B and C
-        const int job = blockIdx.x - p.segs * nblocks * ctiles;
-        if (scan_locate(p, job / p.G, o)) turn_parts<WT>(p, q, o, job % p.G);
+    if (seg >= p.segs) {  // the last waves turn B and C
+        const int job = wave - p.segs * nblocks * ctiles;
+        if (job < p.segs * p.G && scan_locate(p, job / p.G, o))
+            turn_parts<WT>(p, q, o, job % p.G);
         return;
     }
     if (!scan_locate(p, seg, o)) return;
     const bool ends = o.s < o.count - 1, rev = o.s > 0;
     if (o.n <= kPart && !ends && !rev) return;
     const int g = tile / p.tiles;
-    const int cg = (tile - g * p.tiles) * kScanThreads + static_cast<int>(threadIdx.x);
+    const int cg = (tile - g * p.tiles) * 64 + static_cast<int>(threadIdx.x & 63);
     const bool live = cg < p.gd;
     const int d = g * p.gd + min(cg, p.gd - 1);
     const int64_t DN = static_cast<int64_t>(p.D) * p.N;
@@ -203,11 +204,11 @@ __global__ void __launch_bounds__(256) grad_chains(const ScanParams p, const Sca
     const int job = blockIdx.x / blocks, row = job >> 1;
     const bool back = job & 1;
     const int64_t i = static_cast<int64_t>(blockIdx.x - job * blocks) * 256 + threadIdx.x;
-    const uint32_t a = p.offsets[row];
-    const int n = static_cast<int>(p.offsets[row + 1] - a);
-    if (i >= DN || n <= p.seg_len) return;
+    const int n = static_cast<int>(p.offsets[row + 1] - p.offsets[row]);
+    if (n <= p.seg_len) return;
+    const int64_t first = scan_first_seg(p, row);
+    if (i >= DN) return;
     const int count = (n + p.seg_len - 1) / p.seg_len;
-    const int64_t first = scan_first_seg(a, row, p.seg_len);
     const int k = static_cast<int>(i / p.D), d = static_cast<int>(i - static_cast<int64_t>(k) * p.D);
     const int64_t in_slot = static_cast<int64_t>(d) * p.N + k;
     const float a2 = p.A[in_slot] * kScanLog2e;
@@ -597,7 +598,7 @@ hipError_t bwd_n(const ScanParams& p, const ScanGrad& q, hipStream_t s) {
     if (p.segs) {
         constexpr int S = sum_states(N);
         hipLaunchKernelGGL((grad_sums<WT, S>),
-                           dim3(static_cast<unsigned>(p.segs) * p.G * (N / S * p.tiles + 1)),
+                           dim3(scan_blocks(static_cast<int64_t>(p.segs) * p.G * (N / S * p.tiles + 1))),
                            dim3(kScanThreads), 0, s, p, q);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
