@@ -10,12 +10,13 @@
 // so that x and dout are read once and nothing else is, and keeps the run's part
 // of the weights' gradient in registers.  A second launch adds the runs' parts
 // in float64 in a fixed order.  A stream over x, dout and dx: bound by HBM.
+#include <type_traits>
+
 #include "gdr_scan_dev.h"
 
 namespace gdr {
 namespace {
 
-constexpr int kConvBwdThreads = 64;
 constexpr int kConvBwdAhead = 4;
 
 __device__ __forceinline__ void put4(float* p, const float (&v)[4]) {
@@ -27,15 +28,26 @@ __device__ __forceinline__ void put4(uint16_t* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
 }
 
+// 4 values as they stand in memory.
+__device__ __forceinline__ float4 raw4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ uint2 raw4(const uint16_t* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ void wide4(const float4& w, float (&v)[4]) {
+    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+}
+__device__ __forceinline__ void wide4(const uint2& w, float (&v)[4]) {
+    v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
 template <int W, typename WT, bool SILU>
-__global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvGrad p) {
+__global__ void __launch_bounds__(kScanThreads) conv_bwd_kernel(const ConvGrad p) {
     constexpr int H = W - 1;
-    const int ctiles = (p.C / 4 + kConvBwdThreads - 1) / kConvBwdThreads;
-    const int run = blockIdx.x / ctiles;
-    const int c0 = ((blockIdx.x - run * ctiles) * kConvBwdThreads + threadIdx.x) * 4;
-    const int first = static_cast<int>(p.offsets[0]);
-    const int end = static_cast<int>(p.offsets[p.B]);  // rows hold tokens [first, end)
-    if (c0 >= p.C) return;
+    const int ctiles = (p.C / 4 + 63) / 64, wave = scan_wave();
+    const int run = wave / ctiles;
+    const int c0 = ((wave - run * ctiles) * 64 + static_cast<int>(threadIdx.x & 63)) * 4;
+    if (run >= p.runs || c0 >= p.C) return;
+    const int first = static_cast<int>(scan_index(p.offsets, 0));
+    const int end = static_cast<int>(scan_index(p.offsets, p.B));  // rows hold tokens [first, end)
     const int a = run * p.run, b = a + min(p.run, p.T - a);  // this run's tokens
     const WT* x = static_cast<const WT*>(p.x.p) + c0;
     const WT* d_o = static_cast<const WT*>(p.d_o.p) + c0;
@@ -56,9 +68,9 @@ __global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvGra
         int row = 0, hi = p.B - 1;
         while (row < hi) {
             const int mid = (row + hi + 1) >> 1;
-            if (static_cast<int>(p.offsets[mid]) <= from) row = mid; else hi = mid - 1;
+            if (static_cast<int>(scan_index(p.offsets, mid)) <= from) row = mid; else hi = mid - 1;
         }
-        int t0 = static_cast<int>(p.offsets[row]), t1 = static_cast<int>(p.offsets[row + 1]);
+        int t0 = static_cast<int>(scan_index(p.offsets, row)), t1 = static_cast<int>(scan_index(p.offsets, row + 1));
         float xw[H][4], acc[W][4];  // acc[k]: gradient of the input of token t - k so far
 #pragma unroll
         for (int k = 0; k < H; ++k) {
@@ -72,35 +84,39 @@ __global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvGra
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[k][v] = 0.0f;
         const int last = min(upto + H, end);   // tokens read
-        float xn[kConvBwdAhead][4], gn[kConvBwdAhead][4];
+        typedef decltype(raw4(x)) Raw;
+        Raw xn[kConvBwdAhead], gn[kConvBwdAhead];
         auto fetch = [&](int t) {
 #pragma unroll
             for (int i = 0; i < kConvBwdAhead; ++i) {
                 const int64_t u = min(t + i, last - 1);
-                scan_load<4>(x + u * p.x.tok, xn[i]);
-                scan_load<4>(d_o + u * p.d_o.tok, gn[i]);
+                xn[i] = raw4(x + u * p.x.tok);
+                gn[i] = raw4(d_o + u * p.d_o.tok);
             }
         };
         fetch(from);
-        for (int tb = from; tb < upto + H; tb += kConvBwdAhead) {
-            float xc[kConvBwdAhead][4], gc[kConvBwdAhead][4];
+        // FULL: every token and those that it is summed into are in one row and in the run.
+        auto block = [&](int tb, auto full) __attribute__((always_inline)) {
+            constexpr bool FULL = decltype(full)::value;
+            Raw xr[kConvBwdAhead], gr[kConvBwdAhead];
 #pragma unroll
-            for (int i = 0; i < kConvBwdAhead; ++i)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    xc[i][v] = xn[i][v];
-                    gc[i][v] = gn[i][v];
-                }
+            for (int i = 0; i < kConvBwdAhead; ++i) {
+                xr[i] = xn[i];
+                gr[i] = gn[i];
+            }
             if (tb + kConvBwdAhead < last) fetch(tb + kConvBwdAhead);
 #pragma unroll
             for (int i = 0; i < kConvBwdAhead; ++i) {
                 const int t = tb + i;
-                if (t < last) {
-                    if (t >= t1) {  // the next row that has tokens; nothing passes between rows
+                float xc[4], gc[4];
+                wide4(xr[i], xc);
+                wide4(gr[i], gc);
+                if (FULL || t < last) {
+                    if (!FULL && t >= t1) {  // the next row that has tokens; nothing passes between rows
                         do {
                             ++row;
                             t0 = t1;
-                            t1 = static_cast<int>(p.offsets[row + 1]);
+                            t1 = static_cast<int>(scan_index(p.offsets, row + 1));
                         } while (t >= t1);
 #pragma unroll
                         for (int k = 0; k < H; ++k)
@@ -109,32 +125,32 @@ __global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvGra
                     }
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        float g = gc[i][v];
+                        float g = gc[v];
                         if constexpr (SILU) {
                             float pre = bias[v];
 #pragma unroll
                             for (int j = 0; j < H; ++j) pre = __builtin_fmaf(w[j][v], xw[j][v], pre);
-                            pre = __builtin_fmaf(w[H][v], xc[i][v], pre);
+                            pre = __builtin_fmaf(w[H][v], xc[v], pre);
                             const float sig = scan_sigmoid(pre);
                             g *= sig * __builtin_fmaf(pre, 1.0f - sig, 1.0f);
                         }
 #pragma unroll
                         for (int k = 0; k < W; ++k)
-                            if (t - k >= t0) acc[k][v] = __builtin_fmaf(g, w[H - k][v], acc[k][v]);
-                        if (t < upto) {
+                            if (FULL || t - k >= t0) acc[k][v] = __builtin_fmaf(g, w[H - k][v], acc[k][v]);
+                        if (FULL || t < upto) {
 #pragma unroll
                             for (int j = 0; j < H; ++j)
                                 dw[j][v] = __builtin_fmaf(g, xw[j][v], dw[j][v]);
-                            dw[H][v] = __builtin_fmaf(g, xc[i][v], dw[H][v]);
+                            dw[H][v] = __builtin_fmaf(g, xc[v], dw[H][v]);
                             db[v] += g;
                         }
 #pragma unroll
                         for (int k = 0; k + 1 < H; ++k) xw[k][v] = xw[k + 1][v];
-                        xw[H - 1][v] = xc[i][v];
+                        xw[H - 1][v] = xc[v];
                     }
                 }
                 const int s = t - H;  // complete now
-                if (s >= from && s < upto) put4(dx + static_cast<int64_t>(s) * p.dx.tok, acc[H]);
+                if (FULL || (s >= from && s < upto)) put4(dx + static_cast<int64_t>(s) * p.dx.tok, acc[H]);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
 #pragma unroll
@@ -142,6 +158,12 @@ __global__ void __launch_bounds__(kConvBwdThreads) conv_bwd_kernel(const ConvGra
                     acc[0][v] = 0.0f;
                 }
             }
+        };
+        for (int tb = from; tb < upto + H; tb += kConvBwdAhead) {
+            if (tb - H >= max(t0, from) && tb + kConvBwdAhead <= min(t1, upto))
+                block(tb, std::true_type());
+            else
+                block(tb, std::false_type());
         }
     }
     float* part = p.part + static_cast<int64_t>(run) * (W + 1) * p.C + c0;
@@ -174,13 +196,12 @@ __global__ void __launch_bounds__(256) conv_bwd_reduce(const ConvGrad p) {
 }
 
 template <int W, typename WT> hipError_t conv_bwd_w(const ConvGrad& p, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.runs) *
-                    ((p.C / 4 + kConvBwdThreads - 1) / kConvBwdThreads));
+    const dim3 grid(scan_blocks(static_cast<int64_t>(p.runs) * ((p.C / 4 + 63) / 64)));
     if (p.runs) {
         if (p.silu)
-            hipLaunchKernelGGL((conv_bwd_kernel<W, WT, true>), grid, dim3(kConvBwdThreads), 0, s, p);
+            hipLaunchKernelGGL((conv_bwd_kernel<W, WT, true>), grid, dim3(kScanThreads), 0, s, p);
         else
-            hipLaunchKernelGGL((conv_bwd_kernel<W, WT, false>), grid, dim3(kConvBwdThreads), 0, s, p);
+            hipLaunchKernelGGL((conv_bwd_kernel<W, WT, false>), grid, dim3(kScanThreads), 0, s, p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -121,15 +121,31 @@ __global__ void __launch_bounds__(kDraftThreads) drafts_sums(const DraftParams p
     const int64_t from = static_cast<int64_t>(s) * p.span;
     const int64_t upto = min(from + p.span, static_cast<int64_t>(p.V));
     double sum = 0.0, whole = 0.0;
-    for (int64_t j = from + threadIdx.x * 8; j < upto; j += kDraftThreads * 8) {
-        float pv[8], qv[8];
-        load8(r.p + j, upto - j, pv);
-        if (r.q) load8(r.q + j, upto - j, qv);
+    constexpr int kStep = kDraftThreads * 8;
+    auto add = [&](int64_t j, const float (&pv)[8], const float (&qv)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            sum += r.at(j + i, pv[i], r.q ? qv[i] : 0.0f);
+            sum += r.at(j + i, pv[i], qv[i]);
             whole += weight(static_cast<double>(pv[i]));
         }
+    };
+    int64_t j = from + threadIdx.x * 8;
+    for (; j + kStep + 8 <= upto; j += 2 * kStep) {  // two loads of each in flight
+        float p0[8], p1[8], q0[8] = {}, q1[8] = {};
+        any8(r.p + j, p0);
+        any8(r.p + j + kStep, p1);
+        if (r.q) {
+            any8(r.q + j, q0);
+            any8(r.q + j + kStep, q1);
+        }
+        add(j, p0, q0);
+        add(j + kStep, p1, q1);
+    }
+    for (; j < upto; j += kStep) {
+        float pv[8], qv[8] = {};
+        load8(r.p + j, upto - j, pv);
+        if (r.q) load8(r.q + j, upto - j, qv);
+        add(j, pv, qv);
     }
     sum = wave_sum(sum);
     whole = wave_sum(whole);
@@ -184,8 +200,8 @@ __device__ __forceinline__ int block_pick(bool yes, bool some, int* box) {
 template <typename PT>
 __global__ void __launch_bounds__(kDraftThreads) drafts_draw(const DraftParams p) {
     __shared__ double red[kDraftThreads / 64];
-    __shared__ double carried;
-    __shared__ int box[2];
+    __shared__ double carried, run_before;
+    __shared__ int box[2], offset;
     const int b = blockIdx.x, tid = threadIdx.x;
     const int64_t a = p.offsets[b];
     const int len = static_cast<int>(p.offsets[b + 1] - p.offsets[b]);
@@ -224,17 +240,35 @@ __global__ void __launch_bounds__(kDraftThreads) drafts_draw(const DraftParams p
     }
     block_scan(sum, red, before);
     const int t = block_pick(sum > 0.0 && base + (before + sum) > goal, sum > 0.0, box);
-    if (tid != t) return;
-    double run = 0.0;
-    int64_t found = -1;  // the first that passes, else the last that has a weight
-    for (int64_t j = from; j < upto; ++j) {
-        const double w = r.at(j, scan_value(r.p[j]), r.q ? scan_value(r.q[j]) : 0.0f);
-        if (!(w > 0.0)) continue;
-        run += w;
-        found = j;
-        if (base + (before + run) > goal) break;
+    if (tid == t) {
+        run_before = base + before;
+        offset = static_cast<int>(from - static_cast<int64_t>(s) * p.span);
     }
-    p.next[b] = static_cast<int32_t>(found);
+    __syncthreads();
+    // that thread's values, 64 at a time, one a lane of the first wave
+    if (tid >= 64) return;
+    const int64_t first = static_cast<int64_t>(s) * p.span + offset;
+    const int64_t last = min(first + each, static_cast<int64_t>(p.V));
+    double run = run_before;
+    int64_t found = -1;  // the first that passes, else the last that has a weight
+    for (int64_t j0 = first; j0 < last; j0 += 64) {
+        const int64_t j = j0 + tid;
+        double w = 0.0;
+        if (j < last) w = r.at(j, scan_value(r.p[j]), r.q ? scan_value(r.q[j]) : 0.0f);
+        double inc = w;
+        for (int d = 1; d < 64; d <<= 1) {
+            const double up = __shfl_up(inc, d);
+            if (tid >= d) inc += up;
+        }
+        const uint64_t some = __ballot(w > 0.0), yes = __ballot(w > 0.0 && run + inc > goal);
+        if (yes) {
+            found = j0 + __ffsll(static_cast<unsigned long long>(yes)) - 1;
+            break;
+        }
+        if (some) found = j0 + 63 - __clzll(static_cast<long long>(some));
+        run += __shfl(inc, 63);
+    }
+    if (tid == 0) p.next[b] = static_cast<int32_t>(found);
 }
 
 // ----------------------------------------------------------------- greedy ---
@@ -257,14 +291,47 @@ __global__ void __launch_bounds__(kDraftThreads) drafts_best(const DraftParams p
     const PT* row = static_cast<const PT*>(p.p) + t * p.p_tok;
     const int64_t from = static_cast<int64_t>(s) * p.span;
     const int64_t upto = min(from + p.span, static_cast<int64_t>(p.V));
-    uint64_t best = 0;
-    for (int64_t j = from + threadIdx.x * 8; j < upto; j += kDraftThreads * 8) {
-        float v[8];
-        load8(row + j, upto - j, v);
+    // A thread meets its values in rising order: the first of the largest stays.
+    constexpr int kStep = kDraftThreads * 8, kAhead = 4;
+    float top = -__builtin_inff();
+    int at = -1;
+    auto look = [&](int64_t j, const float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (j + i < upto) best = later(best, key_of(v[i], static_cast<uint32_t>(j + i)));
+            if (v[i] > top) {
+                top = v[i];
+                at = static_cast<int>(j) + i;
+            }
+    };
+    const int64_t mine = from + threadIdx.x * 8;
+    int64_t j = mine;
+    for (; j + (kAhead - 1) * kStep + 8 <= upto; j += kAhead * kStep) {
+        float v[kAhead][8];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) any8(row + j + k * kStep, v[k]);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) look(j + k * kStep, v[k]);
     }
+    for (; j < upto; j += kStep) {
+        if (j + 8 <= upto) {
+            float v[8];
+            any8(row + j, v);
+            look(j, v);
+        } else {
+            for (int64_t i = j; i < upto; ++i) {
+                const float v = scan_value(row[i]);
+                if (v > top) {
+                    top = v;
+                    at = static_cast<int>(i);
+                }
+            }
+        }
+    }
+    if (at < 0)  // nothing above -inf: the first -inf itself, if there is one
+        for (int64_t k = mine; k < upto && at < 0; k += kStep)
+            for (int64_t i = k; i < min(k + 8, upto); ++i)
+                if (at < 0 && scan_value(row[i]) == top) at = static_cast<int>(i);
+    uint64_t best = at < 0 ? 0 : key_of(top, static_cast<uint32_t>(at));
     for (int d = 32; d; d >>= 1) best = later(best, __shfl_xor(best, d));
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = best;
     __syncthreads();

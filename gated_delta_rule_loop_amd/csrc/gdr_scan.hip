@@ -103,33 +103,57 @@ __global__ void __launch_bounds__(kScanNarrowThreads) scan_narrow(const ScanPara
 #pragma unroll
         for (int j = 0; j < U; ++j) fetch(min(t + j, n - 1), next[j]);
     };
-    if (n > 0) fetch_all(0);
-    for (int t = 0; t < n; t += U) {
+    // U tokens: what does not depend on the state for all of them first, so that their
+    // long chains (softplus, sigmoid) run beside one another.  FULL: none is past the row.
+    auto block = [&](int t, auto full) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)::value;
         Token<WT, S> now[U];
+        float delta[U], gate[U], y[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) now[j] = next[j];
         if (t + U < n) fetch_all(t + U);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (t + j >= n) break;
-            const Token<WT, S>& k = now[j];
-            float delta = k.dt + bias;
-            if (p.softplus) delta = scan_softplus(delta);
-            const float u = delta * k.x;
-            float y = 0.0f;
+        for (int j = 0; j < U; ++j) delta[j] = now[j].dt + bias;
+        if (p.softplus) {
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[i]), h[i], u * k.b[i]);
-                if constexpr (OUT) y = __builtin_fmaf(h[i], k.c[i], y);
-            }
-            if constexpr (OUT) {
-                y = __builtin_fmaf(skip, k.x, lane_sum<L>(y));
-                if (z) y *= k.z * scan_sigmoid(k.z);
-                if (sub == 0)
-                    scan_put(static_cast<WT*>(p.out) + static_cast<int64_t>(t0 + t + j) * p.o_tok + d, y);
+            for (int j = 0; j < U; ++j) delta[j] = scan_softplus(delta[j]);
+        }
+        if constexpr (OUT) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) gate[j] = 1.0f;
+            if (z) {
+#pragma unroll
+                for (int j = 0; j < U; ++j) gate[j] = now[j].z * scan_sigmoid(now[j].z);
             }
         }
-    }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (!FULL && t + j >= n) continue;
+            const float u = delta[j] * now[j].x;
+            y[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta[j] * a2[i]), h[i], u * now[j].b[i]);
+                if constexpr (OUT) y[j] = __builtin_fmaf(h[i], now[j].c[i], y[j]);
+            }
+        }
+        if constexpr (OUT) {
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                y[j] = __builtin_fmaf(skip, now[j].x, lane_sum<L>(y[j])) * gate[j];
+            if (sub == 0) {
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (FULL || t + j < n)
+                        scan_put(static_cast<WT*>(p.out) + static_cast<int64_t>(t0 + t + j) * p.o_tok + d,
+                                 y[j]);
+            }
+        }
+    };
+    if (n > 0) fetch_all(0);
+    int t = 0;
+    for (; t + U <= n; t += U) block(t, std::true_type());
+    if (t < n) block(t, std::false_type());
     if (p.last && !p.keep)
         scan_store<S>(static_cast<ST*>(p.last) + static_cast<int64_t>(slot) * p.last_outer + at, h);
 }
@@ -165,39 +189,6 @@ template <typename WT, typename ST> hipError_t narrow_n(const ScanParams& p, hip
 // --------------------------------------------------------------- wide walk ---
 
 constexpr int kAhead = 4;  // tokens whose x, dt and z are loaded before those in work
-
-// B and C of some tokens as they stand in memory, in scalar registers.
-template <typename WT, int N, int S, bool TWO> struct ScalarRows {
-    static constexpr int R = N * static_cast<int>(sizeof(WT)) / 4;
-    uint32_t b[S][R], c[S][TWO ? R : 1];
-    __device__ __forceinline__ void load(const char* pb, const char* pc, uint32_t sb, uint32_t sc,
-                                         int t, int n) {
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const uint64_t u = static_cast<uint64_t>(min(t + i, n - 1));
-            const GDR_UNIFORM uint32_t* q =
-                reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(pb) + u * sb);
-#pragma unroll
-            for (int k = 0; k < R; ++k) b[i][k] = q[k];
-            if constexpr (TWO) {
-                q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(pc) + u * sc);
-#pragma unroll
-                for (int k = 0; k < R; ++k) c[i][k] = q[k];
-            }
-        }
-    }
-    // Scalar loads return in any order, so that a wait for one is a wait for all: these
-    // have to be there before the next are asked for.
-    __device__ __forceinline__ void arrive() {
-        asm volatile("" : "+s"(b[S - 1][R - 1]));
-        if constexpr (TWO) asm volatile("" : "+s"(c[S - 1][R - 1]));
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    static __device__ __forceinline__ float value(const uint32_t (&r)[R], int i) {
-        if constexpr (sizeof(WT) == 4) return __uint_as_float(r[i]);
-        return __uint_as_float(i & 1 ? r[i / 2] & 0xFFFF0000u : r[i / 2] << 16);
-    }
-};
 
 template <typename WT, int N, bool SUMS>
 __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
@@ -263,9 +254,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
         }
     };
     float total = 0.0f;
-    // B and C are loaded S tokens ahead, as many as two sets of them leave scalar registers.
-    constexpr int R = N * static_cast<int>(sizeof(WT)) / 4;
-    constexpr int S = R <= 8 ? 2 : 1;
+    constexpr int S = scan_ahead<WT>(N);
     typedef ScalarRows<WT, N, S, !SUMS> Rows;
     auto token = [&](const Rows& r, int i, WT xr, WT dr, WT zr, char* to) {
         const float xv = scan_value(xr);

@@ -229,7 +229,7 @@ BwdPlan bwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
     p.gtiles = ceil_div(D / G, scan_grad_channels(static_cast<int>(N)));
     if (B == 0) return p;  // no row: the weights' gradients are zeros
     const int64_t want = std::max<int64_t>(1, 1024 / (G * p.gtiles));
-    const int64_t len = std::min<int64_t>(512, std::max<int64_t>(64, round_up(ceil_div(T, want), 16)));
+    const int64_t len = std::min<int64_t>(512, std::max<int64_t>(16, round_up(ceil_div(T, want), 16)));
     p.seg_len = len < T ? len : 0;
     p.segs = p.seg_len ? T / len + B : B;
     p.parts = T / kScanPart + B;
@@ -681,7 +681,7 @@ int gdr_causal_conv1d_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gdr
     IndexCheck ic;
     ic.offsets = input_row_offsets;
     ic.total_tokens = T;
-    if ((rc = check_grid(fn, p.runs * ceil_div(C / 4, 64), 64)) ||
+    if ((rc = check_grid(fn, ceil_div(p.runs * ceil_div(C / 4, 64), 4), kScanThreads)) ||
         (rc = check_grid(fn, ceil_div((W + 1) * C, 256), 256)) ||
         (rc = run_debug_check(fn, B, ic, stream)))
         return rc;

@@ -98,8 +98,12 @@ __global__ void __launch_bounds__(kScanThreads, 3) grad_sums(const ScanParams p,
     const uint32_t at = static_cast<uint32_t>(d) * sizeof(WT);
     const uint32_t sx = scan_step<WT>(p.x), sd = scan_step<WT>(p.dt), so = scan_step<WT>(q.d_o),
                    sz = scan_step<WT>(zrow);
-    const int64_t b0 = static_cast<int64_t>(o.t0) * p.b.tok + static_cast<int64_t>(g) * p.b.grp + n0;
-    const int64_t c0 = static_cast<int64_t>(o.t0) * p.c.tok + static_cast<int64_t>(g) * p.c.grp + n0;
+    const char* pb = static_cast<const char*>(p.b.p) +
+                     (o.t0 * p.b.tok + g * p.b.grp + n0) * static_cast<int64_t>(sizeof(WT));
+    const char* pc = static_cast<const char*>(p.c.p) +
+                     (o.t0 * p.c.tok + g * p.c.grp + n0) * static_cast<int64_t>(sizeof(WT));
+    const uint32_t sb = static_cast<uint32_t>(p.b.tok) * sizeof(WT);
+    const uint32_t sc = static_cast<uint32_t>(p.c.tok) * sizeof(WT);
     float* check = q.check + first_part(p, o) * (DN + p.D) + d;
     float total = 0.0f;
     constexpr int U = 4;
@@ -118,8 +122,36 @@ __global__ void __launch_bounds__(kScanThreads, 3) grad_sums(const ScanParams p,
             }
         }
     };
-    fetch(0);
-    for (int t = 0; t < o.n; t += U) {
+    constexpr int S = scan_ahead<WT>(N);
+    typedef ScalarRows<WT, N, S, true> Rows;
+    auto token = [&](const Rows& r, int i, WT xr, WT dr, WT gr, WT zr, auto back) {
+        float delta = scan_value(dr) + bias;
+        if (p.softplus) delta = scan_softplus(delta);
+        const float u = delta * scan_value(xr);
+        total += delta;
+        if constexpr (decltype(back)::value) {
+            float dy = scan_value(gr);
+            if (gated) {
+                const float zv = scan_value(zr);
+                dy *= zv * scan_sigmoid(zv);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float a = __builtin_amdgcn_exp2f(delta * a2[k]);
+                h[k] = __builtin_fmaf(a, h[k], u * Rows::value(r.b[i], k));
+                P[k] *= a;
+                R[k] = __builtin_fmaf(P[k], dy * Rows::value(r.c[i], k), R[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[k]), h[k],
+                                      u * Rows::value(r.b[i], k));
+        }
+    };
+    Rows rows[2];
+    auto step = [&](int t, auto full, auto back) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)::value;
         WT xc[U], dc[U], oc[U], zc[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -136,35 +168,26 @@ __global__ void __launch_bounds__(kScanThreads, 3) grad_sums(const ScanParams p,
             if (n0 == 0) to[DN] = total;
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (t + i >= o.n) break;
-            float delta = scan_value(dc[i]) + bias;
-            if (p.softplus) delta = scan_softplus(delta);
-            const float u = delta * scan_value(xc[i]);
-            total += delta;
-            float b[N];
-            uniform_row<WT, N>(p.b.p, b0 + (t + i) * p.b.tok, b);
-            if (rev) {
-                float c[N], dy = scan_value(oc[i]);
-                uniform_row<WT, N>(p.c.p, c0 + (t + i) * p.c.tok, c);
-                if (gated) {
-                    const float zv = scan_value(zc[i]);
-                    dy *= zv * scan_sigmoid(zv);
-                }
+        for (int i = 0; i < U; i += S) {
+            Rows &now = rows[(i / S) & 1], &next = rows[(i / S + 1) & 1];
+            now.arrive();
+            next.load(pb, pc, sb, sc, t + i + S, o.n);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const float a = __builtin_amdgcn_exp2f(delta * a2[k]);
-                    h[k] = __builtin_fmaf(a, h[k], u * b[k]);
-                    P[k] *= a;
-                    R[k] = __builtin_fmaf(P[k], dy * c[k], R[k]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; ++k)
-                    h[k] = __builtin_fmaf(__builtin_amdgcn_exp2f(delta * a2[k]), h[k], u * b[k]);
-            }
+            for (int j = 0; j < S; ++j)
+                if (FULL || t + i + j < o.n)
+                    token(now, j, xc[i + j], dc[i + j], oc[i + j], zc[i + j], back);
         }
-    }
+    };
+    auto walk = [&](auto back) __attribute__((always_inline)) {
+        fetch(0);
+        rows[0].load(pb, pc, sb, sc, 0, o.n);
+        int t = 0;
+        for (; t + U <= o.n; t += U) step(t, std::true_type(), back);
+        if (t < o.n) step(t, std::false_type(), back);
+    };
+    if (rev) walk(std::true_type());
+    else walk(std::false_type());
     if (!live) return;
     const int64_t mine = static_cast<int64_t>(seg) * DN + static_cast<int64_t>(n0) * p.D + d;
 #pragma unroll

@@ -143,6 +143,45 @@ __device__ __forceinline__ void uniform_row(const void* base, int64_t elem, floa
     }
 }
 
+// B and C of some tokens as they stand in memory, in scalar registers.
+template <typename WT, int N, int S, bool TWO> struct ScalarRows {
+    static constexpr int R = N * static_cast<int>(sizeof(WT)) / 4;
+    uint32_t b[S][R], c[S][TWO ? R : 1];
+    __device__ __forceinline__ void load(const char* pb, const char* pc, uint32_t sb, uint32_t sc,
+                                         int t, int n) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const uint64_t u = static_cast<uint64_t>(min(t + i, n - 1));
+            const GDR_UNIFORM uint32_t* q =
+                reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(pb) + u * sb);
+#pragma unroll
+            for (int k = 0; k < R; ++k) b[i][k] = q[k];
+            if constexpr (TWO) {
+                q = reinterpret_cast<const GDR_UNIFORM uint32_t*>(reinterpret_cast<uint64_t>(pc) + u * sc);
+#pragma unroll
+                for (int k = 0; k < R; ++k) c[i][k] = q[k];
+            }
+        }
+    }
+    // Scalar loads return in any order, so that a wait for one is a wait for all: these
+    // have to be there before the next are asked for.
+    __device__ __forceinline__ void arrive() {
+        asm volatile("" : "+s"(b[S - 1][R - 1]));
+        if constexpr (TWO) asm volatile("" : "+s"(c[S - 1][R - 1]));
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    static __device__ __forceinline__ float value(const uint32_t (&r)[R], int i) {
+        if constexpr (sizeof(WT) == 4) return __uint_as_float(r[i]);
+        return __uint_as_float(i & 1 ? r[i / 2] & 0xFFFF0000u : r[i / 2] << 16);
+    }
+};
+
+// Tokens that B and C are loaded ahead: as many as leave scalar registers beside two
+// sets of them.
+template <typename WT> constexpr int scan_ahead(int N) {
+    return N * static_cast<int>(sizeof(WT)) <= 32 ? 2 : 1;
+}
+
 // The number of row b's first part, when rows are cut into parts of `len` tokens:
 // rows own disjoint ranges of numbers, with at most one unused at the end of each.
 __device__ __forceinline__ int64_t scan_first_part(uint32_t off, int b, int len) {
