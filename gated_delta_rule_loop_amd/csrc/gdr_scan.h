@@ -39,6 +39,7 @@ struct ScanParams {
     void* last; int64_t last_outer; // written states (in's type), or nullptr
     int32_t narrow_most;            // rows up to this many tokens are taken by the narrow walk
     int32_t hand_on;                // the narrow walk writes the states of empty rows too
+    int32_t lane_most;              // longer rows up to this many are taken by the lane walk
     // long rows, cut into segments of seg_len tokens (0: none is cut)
     int32_t seg_skip;               // rows up to this many tokens have no segment
     int32_t seg_len, segs, tiles;   // tiles: waves over one group's channels
@@ -97,11 +98,13 @@ struct DraftParams {
 constexpr int kScanThreads = 256;
 inline unsigned scan_blocks(int64_t waves) { return static_cast<unsigned>((waves + 3) / 4); }
 constexpr int kScanNarrowThreads = 256;
+constexpr int kScanLaneChannels = 16;  // channels of a lane walk's workgroup
 constexpr int kScanPart = 16;       // tokens that a gradient holds in registers
 int scan_grad_channels(int N);      // channels of a gradient's workgroup
 
 hipError_t launch_scan_narrow(const ScanParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_scan_wide(const ScanParams& p, bool work_bf16, bool sums, hipStream_t s);
+hipError_t launch_scan_lanes(const ScanParams& p, bool work_bf16, hipStream_t s);
 hipError_t launch_scan_chain(const ScanParams& p, hipStream_t s);
 
 hipError_t launch_scan_bwd(const ScanParams& p, const ScanGrad& g, bool work_bf16, hipStream_t s);

@@ -25,10 +25,6 @@ namespace {
 
 // ------------------------------------------------------------- narrow walk ---
 
-template <int CTRL> __device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)),
-                                                       CTRL, 0xf, 0xf, false));
-}
 // Sum over n neighbouring lanes (a power of two up to 16, aligned), in each.
 template <int n> __device__ __forceinline__ float lane_sum(float v) {
     if constexpr (n >= 2) v += dpp<0xB1>(v);   // quad lanes 1 0 3 2
@@ -324,6 +320,162 @@ __global__ void __launch_bounds__(kScanThreads) scan_wide(const ScanParams p) {
     }
 }
 
+// --------------------------------------------------------------- lane walk ---
+
+// A wave takes four channels, 16 lanes each, and 16 tokens at a time.  Lane j of a
+// channel holds N / 16 of its states and is also the one that reads token j's x, dt and z
+// and takes their softplus and gate, once for all states; step sizes go to the
+// channel's lanes as broadcast operands.  The 16 tokens' outputs, sums over the
+// lanes, are added by halving (15 exchanges instead of 64), which leaves token j's in
+// lane j.  B and C come 16 tokens at a time through LDS, turned to a state's tokens.
+// No wave needs another's work.
+constexpr int kLanes = 16;
+constexpr int kLanePad = 20;  // floats from one state's tokens to the next's in LDS
+
+template <int K> __device__ __forceinline__ float from_lane(float v) {
+    return __uint_as_float(__builtin_amdgcn_mov_dpp(static_cast<int>(__float_as_uint(v)),
+                                                    0x150 + K, 0xf, 0xf, true));
+}
+
+template <typename WT, int N> struct LaneWalk {
+    static constexpr int S = N / kLanes;   // states a lane
+    static constexpr int V = N / 2;        // values of B or C that a lane brings
+    float h[S], a2[S];
+    float y[kLanes];
+
+    template <int K>
+    __device__ __forceinline__ void token(float delta, float u, const float (&b)[S], const float (&c)[S]) {
+        y[K] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const float e = __builtin_amdgcn_exp2f(from_lane<K>(delta) * a2[i]);
+            h[i] = __builtin_fmaf(e, h[i], from_lane<K>(u) * b[i]);
+            y[K] = i ? __builtin_fmaf(h[i], c[i], y[K]) : h[i] * c[i];
+        }
+    }
+    // Tokens 4 Q to 4 Q + 3 of the block in work; lds: B's states, then C's.
+    template <int Q> __device__ __forceinline__ void four(float delta, float u, const float* lds, int j) {
+        float b[4][S], c[4][S];
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            const float* at = lds + (j * S + i) * kLanePad + 4 * Q;
+            const float4 p = *reinterpret_cast<const float4*>(at);
+            const float4 q = *reinterpret_cast<const float4*>(at + N * kLanePad);
+            b[0][i] = p.x; b[1][i] = p.y; b[2][i] = p.z; b[3][i] = p.w;
+            c[0][i] = q.x; c[1][i] = q.y; c[2][i] = q.z; c[3][i] = q.w;
+        }
+        token<4 * Q>(delta, u, b[0], c[0]);
+        token<4 * Q + 1>(delta, u, b[1], c[1]);
+        token<4 * Q + 2>(delta, u, b[2], c[2]);
+        token<4 * Q + 3>(delta, u, b[3], c[3]);
+    }
+    // Lane j's: the sum over the channel's lanes of their y[j].
+    __device__ __forceinline__ float sum(int j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = halve<0x128>(j & 8, y[i], y[i + 8]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = halve<0x141>(j & 4, y[i], y[i + 4]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) y[i] = halve<0x4E>(j & 2, y[i], y[i + 2]);
+        return halve<0xB1>(j & 1, y[0], y[1]);
+    }
+};
+
+template <typename WT, typename ST, int N>
+__global__ void __launch_bounds__(kScanThreads) scan_lanes(const ScanParams p) {
+    typedef LaneWalk<WT, N> Walk;
+    constexpr int S = Walk::S, V = Walk::V;
+    __shared__ __attribute__((aligned(16))) float staged[kScanThreads / 64][2 * N * kLanePad];
+    const int tiles = (p.D + kScanLaneChannels - 1) / kScanLaneChannels;
+    const int row = blockIdx.x / tiles;
+    int tile = blockIdx.x - row * tiles;
+    // Four neighbouring tiles of bf16 share the lines of a token: the dies take workgroups
+    // in turn, so that every eighth gets the next of four.
+    if (tile < (tiles & ~31)) tile = (tile & ~31) | ((tile & 7) << 2) | ((tile >> 3) & 3);
+    const int t0 = static_cast<int>(scan_index(p.offsets, row));
+    const int n = static_cast<int>(scan_index(p.offsets, row + 1)) - t0;
+    if (n <= p.narrow_most || n > p.lane_most) return;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int first = tile * kScanLaneChannels + wave * 4;  // of the wave's channels
+    if (first >= p.D) return;
+    const int lane = threadIdx.x & 63, j = lane & (kLanes - 1);
+    const int d = first + (lane >> 4), g = first / p.gd;    // groups are whole fours
+    const uint32_t slot = p.slot_idx ? scan_index(p.slot_idx, row) : static_cast<uint32_t>(row);
+    const ScanRows orow = {p.out, p.o_tok};
+    if (p.slot_idx != nullptr && slot == kPadSlot) {
+        for (int t = j; t < n; t += kLanes)
+            scan_put(static_cast<WT*>(p.out) + static_cast<int64_t>(t0 + t) * p.o_tok + d, 0.0f);
+        return;
+    }
+    const int64_t at = static_cast<int64_t>(d) * N + j * S;
+    Walk w;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        w.a2[i] = p.A[at + i] * kScanLog2e;
+        w.h[i] = p.in.p ? scan_value(static_cast<const ST*>(p.in.p)[static_cast<int64_t>(slot) * p.in.outer + at + i])
+                        : 0.0f;
+    }
+    const float bias = p.bias ? p.bias[d] : 0.0f, skip = p.skip ? p.skip[d] : 0.0f;
+    const bool gated = p.z.p != nullptr;
+    const ScanRows zrow = gated ? p.z : p.x;
+    // token j's operands, and a quarter of token lane / 4's B or C
+    const uint32_t off = static_cast<uint32_t>(d) * sizeof(WT);
+    const uint32_t sx = scan_step<WT>(p.x), sd = scan_step<WT>(p.dt), sz = scan_step<WT>(zrow),
+                   so = scan_step<WT>(orow);
+    const int mine = lane >> 2, part = lane & 3;
+    const ScanHeads bc = part < 2 ? p.b : p.c;
+    const WT* bcp = static_cast<const WT*>(bc.p) + static_cast<int64_t>(t0) * bc.tok +
+                    static_cast<int64_t>(g) * bc.grp + (part & 1) * V;
+    float* to = staged[wave] + ((part >> 1) * N + (part & 1) * V) * kLanePad + mine;
+    WT xs, ds, zs;
+    float bcs[V];
+    auto fetch = [&](int t) {
+        const uint32_t k = min(j, n - 1 - t);
+        xs = scan_at<WT>(scan_base<WT>(p.x, t0 + t), off + k * sx);
+        ds = scan_at<WT>(scan_base<WT>(p.dt, t0 + t), off + k * sd);
+        zs = scan_at<WT>(scan_base<WT>(zrow, t0 + t), off + k * sz);
+        scan_load<V>(bcp + static_cast<int64_t>(min(t + mine, n - 1)) * bc.tok, bcs);
+    };
+    fetch(0);
+    for (int t = 0; t < n; t += kLanes) {
+        const float x = scan_value(xs), z = scan_value(zs);
+        float delta = scan_value(ds) + bias;
+        __builtin_amdgcn_wave_barrier();  // the block before has been read (LDS serves a wave in order)
+#pragma unroll
+        for (int i = 0; i < V; ++i) to[i * kLanePad] = bcs[i];
+        if (t + kLanes < n) fetch(t + kLanes);
+        if (p.softplus) delta = scan_softplus(delta);
+        const bool in = t + j < n;  // tokens past the row's end have no step
+        delta = in ? delta : 0.0f;
+        const float u = in ? delta * x : 0.0f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        w.template four<0>(delta, u, staged[wave], j);
+        w.template four<1>(delta, u, staged[wave], j);
+        w.template four<2>(delta, u, staged[wave], j);
+        w.template four<3>(delta, u, staged[wave], j);
+        float y = __builtin_fmaf(skip, x, w.sum(j));
+        if (gated) y *= z * scan_sigmoid(z);
+        if (in) scan_put(reinterpret_cast<WT*>(const_cast<char*>(scan_base<WT>(orow, t0 + t)) + off + j * so), y);
+    }
+    if (p.last && !p.keep) {
+        ST* last = static_cast<ST*>(p.last) + static_cast<int64_t>(slot) * p.last_outer + at;
+#pragma unroll
+        for (int i = 0; i < S; ++i) scan_put(last + i, w.h[i]);
+    }
+}
+
+template <typename WT, typename ST> hipError_t lanes_n(const ScanParams& p, hipStream_t s) {
+    const dim3 grid(static_cast<unsigned>(p.B) * ((p.D + kScanLaneChannels - 1) / kScanLaneChannels));
+    switch (p.N) {
+        case 16: hipLaunchKernelGGL((scan_lanes<WT, ST, 16>), grid, dim3(kScanThreads), 0, s, p); break;
+        case 32: hipLaunchKernelGGL((scan_lanes<WT, ST, 32>), grid, dim3(kScanThreads), 0, s, p); break;
+        case 64: hipLaunchKernelGGL((scan_lanes<WT, ST, 64>), grid, dim3(kScanThreads), 0, s, p); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
 // seg_state of a cut row: from the segments' own end states to the states that
 // they start from.
 __global__ void __launch_bounds__(256) scan_chain(const ScanParams p) {
@@ -391,6 +543,12 @@ hipError_t launch_scan_narrow(const ScanParams& p, bool work_bf16, hipStream_t s
     if (work_bf16)
         return p.in.bf16 ? narrow_n<uint16_t, uint16_t>(p, s) : narrow_n<uint16_t, float>(p, s);
     return p.in.bf16 ? narrow_n<float, uint16_t>(p, s) : narrow_n<float, float>(p, s);
+}
+
+hipError_t launch_scan_lanes(const ScanParams& p, bool work_bf16, hipStream_t s) {
+    if (work_bf16)
+        return p.in.bf16 ? lanes_n<uint16_t, uint16_t>(p, s) : lanes_n<uint16_t, float>(p, s);
+    return p.in.bf16 ? lanes_n<float, uint16_t>(p, s) : lanes_n<float, float>(p, s);
 }
 
 hipError_t launch_scan_wide(const ScanParams& p, bool work_bf16, bool sums, hipStream_t s) {

@@ -192,20 +192,25 @@ int64_t narrow_blocks(const ScanDims& d, bool state_bf16) {
 // How a forward is cut: rows up to `narrow` tokens take the narrow walk, longer ones the
 // wide one in segments of seg_len tokens (0: uncut).
 struct FwdPlan {
-    int64_t narrow, seg_len, segs, state, delta, end;
+    int64_t narrow, lane, seg_len, segs, state, delta, end;
     bool wide;
 };
 
 constexpr int64_t kNarrowAll = 64;  // tokens of a call up to which every row goes narrowly
 
+constexpr int64_t kLaneCap = 1 << 30;
+
 FwdPlan fwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
     FwdPlan p{};
     const int64_t ctiles = G * ceil_div(D / G, 64);
     p.narrow = T <= kNarrowAll ? kNarrowAll : B > 8 ? 16 : 0;
-    p.wide = T > kNarrowAll;
+    p.lane = p.narrow;
     p.segs = B;
+    if (T <= kNarrowAll) return p;
+    const bool full = B * ctiles >= 2048;
+    if (!full && N >= 16) p.lane = std::max(p.narrow, kLaneCap);
+    p.wide = T > p.lane;
     if (p.wide) {
-        const bool full = B * ctiles >= 2048;
         const int64_t want = std::max<int64_t>(1, (full ? 1024 : 8192) / ctiles);
         const int64_t len = std::max<int64_t>(16, round_up(ceil_div(T, want), 16));
         if (len < T) {
@@ -375,7 +380,8 @@ int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr
     set_states(p, initial_state, final_state, state);
     p.narrow_most = static_cast<int32_t>(pl.narrow);
     p.hand_on = present(final_state);  // also of rows without tokens
-    p.seg_skip = p.narrow_most;
+    p.lane_most = static_cast<int32_t>(pl.lane);
+    p.seg_skip = p.lane_most;
     p.seg_len = static_cast<int32_t>(pl.seg_len);
     p.segs = static_cast<int32_t>(pl.segs);
     if (pl.seg_len) {
@@ -383,6 +389,8 @@ int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr
         p.seg_delta = p.seg_state + pl.delta;
     }
     if ((rc = check_grid(fn, narrow_blocks(d, p.in.bf16), kScanNarrowThreads)) ||
+        (pl.lane > pl.narrow &&
+         (rc = check_grid(fn, d.B * ceil_div(d.D, kScanLaneChannels), kScanThreads))) ||
         (pl.wide && (rc = check_grid(fn, ceil_div(pl.segs * d.G * d.tiles(), 4), kScanThreads))) ||
         (pl.seg_len && (rc = check_grid(fn, d.B * ceil_div(d.D * d.N, 256), 256))) ||
         (rc = run_debug_check(fn, d.B, index_check(d, input_row_offsets, state, slot_idx), stream)))
@@ -392,6 +400,7 @@ int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr
     const bool b16 = d.work == GDR_DTYPE_BF16;
     hipError_t e = hipSuccess;
     if (pl.narrow || p.hand_on) e = launch_scan_narrow(p, b16, s);
+    if (e == hipSuccess && pl.lane > pl.narrow) e = launch_scan_lanes(p, b16, s);
     if (e == hipSuccess && pl.seg_len) {
         e = launch_scan_wide(p, b16, true, s);
         if (e == hipSuccess) e = launch_scan_chain(p, s);

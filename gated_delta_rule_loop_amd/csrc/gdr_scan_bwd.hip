@@ -261,16 +261,6 @@ __global__ void __launch_bounds__(256) grad_chains(const ScanParams p, const Sca
 
 // ------------------------------------------------------------- 3: gradients ---
 
-template <int CTRL> __device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)),
-                                                       CTRL, 0xf, 0xf, false));
-}
-// What a lane and its partner (named by CTRL) hold of x and y, added: x's in the
-// lanes where `up` is false, y's in their partners.
-template <int CTRL> __device__ __forceinline__ float halve(bool up, float x, float y) {
-    return (up ? y : x) + dpp<CTRL>(up ? x : y);
-}
-
 // Sums over the wave of x[0..15] and y[0..15]: lane l gets that of x[(l / 2) % 16]
 // below 32 and of y[...] from there on.
 __device__ __forceinline__ float sums32(float (&x)[16], float (&y)[16]) {

@@ -73,6 +73,16 @@ template <int n> __device__ __forceinline__ void scan_store(uint16_t* p, const f
     }
 }
 
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)),
+                                                       CTRL, 0xf, 0xf, false));
+}
+// What a lane and its partner (named by CTRL) hold of x and y, added: x's in the
+// lanes where `up` is false, y's in their partners.
+template <int CTRL> __device__ __forceinline__ float halve(bool up, float x, float y) {
+    return (up ? y : x) + dpp<CTRL>(up ? x : y);
+}
+
 // The value `off` bytes behind a wave-uniform base: one 32-bit register a lane.
 template <typename WT> __device__ __forceinline__ WT scan_at(const char* base, uint32_t off) {
     return *reinterpret_cast<const WT*>(base + off);
