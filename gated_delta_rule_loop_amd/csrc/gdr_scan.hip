@@ -4,18 +4,26 @@
 // for every channel d and its N states n, in float32.  The decay is a number of
 // its own for every token, channel and state, so there is no form as matrix
 // products: the work is 6 vector-unit slots a token, channel and state (product,
-// exponential, which takes two, product, two multiply-adds).
+// exponential, which takes two, product, two multiply-adds).  At 39e12 slots a second,
+// what the unit issues, they bound every walk over long rows.
 //
 // Wide walk (prompts): a lane owns a channel and all its states, in registers;
 // B and C of a token are the same for the whole wave and come through scalar
 // loads.  Long rows are cut into segments so that few channels still fill the
 // chip: one launch takes each segment's own end state from zero and the sum of
 // its step sizes (a segment's decay is exp(A sum delta)), one chains them to the
-// states the segments start from, and the walk follows.
+// states the segments start from, and the walk follows.  16384 bf16 tokens of 4096
+// channels of 16 states 471 us, where the 275 slots a token and channel of both passes
+// take 469; 32 rows of 512, enough for one piece a row, 351 (150 slots, 256 us).
+//
+// Lane walk (prompts of few tokens or many states): 16 lanes own a channel, so that
+// one launch has 16 times the waves and nothing is walked twice.  97 tokens of 4096
+// channels of 16 states 17 us (segments 25), 1500 of 2048 channels of 64 122 (168).
 //
 // Narrow walk (single tokens, drafted windows, folds): a lane owns 16 bytes of a
 // channel's state, so that states are read and written in whole lines; the
-// output is summed over a channel's 1 to 16 lanes by lane permutations.
+// output is summed over a channel's 1 to 16 lanes by lane permutations.  256 single
+// tokens of 4096 channels of 16 bf16 states: 19 us for 74 MB.
 #include <type_traits>
 
 #include "gdr_scan_dev.h"
@@ -343,9 +351,11 @@ template <typename WT, int N> struct LaneWalk {
     float h[S], a2[S];
     float y[kLanes];
 
-    template <int K>
-    __device__ __forceinline__ void token(float delta, float u, const float (&b)[S], const float (&c)[S]) {
+    template <int K, bool FULL>
+    __device__ __forceinline__ void token(float delta, float u, const float (&b)[S], const float (&c)[S],
+                                          int left) {
         y[K] = 0.0f;
+        if (!FULL && K >= left) return;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             const float e = __builtin_amdgcn_exp2f(from_lane<K>(delta) * a2[i]);
@@ -353,8 +363,10 @@ template <typename WT, int N> struct LaneWalk {
             y[K] = i ? __builtin_fmaf(h[i], c[i], y[K]) : h[i] * c[i];
         }
     }
-    // Tokens 4 Q to 4 Q + 3 of the block in work; lds: B's states, then C's.
-    template <int Q> __device__ __forceinline__ void four(float delta, float u, const float* lds, int j) {
+    // Tokens 4 Q to 4 Q + 3 of the block in work, of which the first `left` are the row's;
+    // lds: B's states, then C's.
+    template <int Q, bool FULL>
+    __device__ __forceinline__ void four(float delta, float u, const float* lds, int j, int left) {
         float b[4][S], c[4][S];
 #pragma unroll
         for (int i = 0; i < S; ++i) {
@@ -364,10 +376,10 @@ template <typename WT, int N> struct LaneWalk {
             b[0][i] = p.x; b[1][i] = p.y; b[2][i] = p.z; b[3][i] = p.w;
             c[0][i] = q.x; c[1][i] = q.y; c[2][i] = q.z; c[3][i] = q.w;
         }
-        token<4 * Q>(delta, u, b[0], c[0]);
-        token<4 * Q + 1>(delta, u, b[1], c[1]);
-        token<4 * Q + 2>(delta, u, b[2], c[2]);
-        token<4 * Q + 3>(delta, u, b[3], c[3]);
+        token<4 * Q, FULL>(delta, u, b[0], c[0], left);
+        token<4 * Q + 1, FULL>(delta, u, b[1], c[1], left);
+        token<4 * Q + 2, FULL>(delta, u, b[2], c[2], left);
+        token<4 * Q + 3, FULL>(delta, u, b[3], c[3], left);
     }
     // Lane j's: the sum over the channel's lanes of their y[j].
     __device__ __forceinline__ float sum(int j) {
@@ -385,7 +397,7 @@ template <typename WT, typename ST, int N>
 __global__ void __launch_bounds__(kScanThreads) scan_lanes(const ScanParams p) {
     typedef LaneWalk<WT, N> Walk;
     constexpr int S = Walk::S, V = Walk::V;
-    __shared__ __attribute__((aligned(16))) float staged[kScanThreads / 64][2 * N * kLanePad];
+    __shared__ __attribute__((aligned(16))) float staged[kScanThreads / 64][2][2 * N * kLanePad];
     const int tiles = (p.D + kScanLaneChannels - 1) / kScanLaneChannels;
     const int row = blockIdx.x / tiles;
     int tile = blockIdx.x - row * tiles;
@@ -426,38 +438,60 @@ __global__ void __launch_bounds__(kScanThreads) scan_lanes(const ScanParams p) {
     const ScanHeads bc = part < 2 ? p.b : p.c;
     const WT* bcp = static_cast<const WT*>(bc.p) + static_cast<int64_t>(t0) * bc.tok +
                     static_cast<int64_t>(g) * bc.grp + (part & 1) * V;
-    float* to = staged[wave] + ((part >> 1) * N + (part & 1) * V) * kLanePad + mine;
-    WT xs, ds, zs;
-    float bcs[V];
+    const int to = ((part >> 1) * N + (part & 1) * V) * kLanePad + mine;
+    // Three blocks are in work at once: the operands of the one after the next are being
+    // loaded, the next one's go to LDS and through softplus and gate, and this one's
+    // states are stepped.
+    const int final = (n - 1) / kLanes * kLanes;  // the last block's first token
+    struct Raw {
+        WT x, dt, z;
+        float bc[V];
+    };
+    struct Ready {
+        float x, delta, u, gate;
+    };
+    Raw raw;
+    Ready next;
     auto fetch = [&](int t) {
+        t = min(t, final);
         const uint32_t k = min(j, n - 1 - t);
-        xs = scan_at<WT>(scan_base<WT>(p.x, t0 + t), off + k * sx);
-        ds = scan_at<WT>(scan_base<WT>(p.dt, t0 + t), off + k * sd);
-        zs = scan_at<WT>(scan_base<WT>(zrow, t0 + t), off + k * sz);
-        scan_load<V>(bcp + static_cast<int64_t>(min(t + mine, n - 1)) * bc.tok, bcs);
+        raw.x = scan_at<WT>(scan_base<WT>(p.x, t0 + t), off + k * sx);
+        raw.dt = scan_at<WT>(scan_base<WT>(p.dt, t0 + t), off + k * sd);
+        raw.z = scan_at<WT>(scan_base<WT>(zrow, t0 + t), off + k * sz);
+        scan_load<V>(bcp + static_cast<int64_t>(min(t + mine, n - 1)) * bc.tok, raw.bc);
+    };
+    auto ready = [&](int t) {  // of block t, which was loaded last
+        float* lds = staged[wave][(t / kLanes) & 1] + to;
+#pragma unroll
+        for (int i = 0; i < V; ++i) lds[i * kLanePad] = raw.bc[i];
+        const float dt = scan_value(raw.dt) + bias, z = scan_value(raw.z);
+        const float delta = p.softplus ? scan_softplus(dt) : dt;
+        next.x = scan_value(raw.x);
+        next.delta = delta;
+        next.u = delta * next.x;
+        next.gate = gated ? z * scan_sigmoid(z) : 1.0f;
     };
     fetch(0);
-    for (int t = 0; t < n; t += kLanes) {
-        const float x = scan_value(xs), z = scan_value(zs);
-        float delta = scan_value(ds) + bias;
-        __builtin_amdgcn_wave_barrier();  // the block before has been read (LDS serves a wave in order)
-#pragma unroll
-        for (int i = 0; i < V; ++i) to[i * kLanePad] = bcs[i];
-        if (t + kLanes < n) fetch(t + kLanes);
-        if (p.softplus) delta = scan_softplus(delta);
-        const bool in = t + j < n;  // tokens past the row's end have no step
-        delta = in ? delta : 0.0f;
-        const float u = in ? delta * x : 0.0f;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        w.template four<0>(delta, u, staged[wave], j);
-        w.template four<1>(delta, u, staged[wave], j);
-        w.template four<2>(delta, u, staged[wave], j);
-        w.template four<3>(delta, u, staged[wave], j);
-        float y = __builtin_fmaf(skip, x, w.sum(j));
-        if (gated) y *= z * scan_sigmoid(z);
-        if (in) scan_put(reinterpret_cast<WT*>(const_cast<char*>(scan_base<WT>(orow, t0 + t)) + off + j * so), y);
-    }
+    ready(0);
+    fetch(kLanes);
+    auto block = [&](int t, auto full) __attribute__((always_inline)) {
+        constexpr bool FULL = decltype(full)::value;
+        const Ready now = next;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // LDS serves a wave in order
+        ready(t + kLanes);
+        fetch(t + 2 * kLanes);
+        const float* lds = staged[wave][(t / kLanes) & 1];
+        w.template four<0, FULL>(now.delta, now.u, lds, j, n - t);
+        w.template four<1, FULL>(now.delta, now.u, lds, j, n - t);
+        w.template four<2, FULL>(now.delta, now.u, lds, j, n - t);
+        w.template four<3, FULL>(now.delta, now.u, lds, j, n - t);
+        const float y = __builtin_fmaf(skip, now.x, w.sum(j)) * now.gate;
+        if (FULL || t + j < n)
+            scan_put(reinterpret_cast<WT*>(const_cast<char*>(scan_base<WT>(orow, t0 + t)) + off + j * so), y);
+    };
+    int t = 0;
+    for (; t + kLanes <= n; t += kLanes) block(t, std::true_type());
+    if (t < n) block(t, std::false_type());
     if (p.last && !p.keep) {
         ST* last = static_cast<ST*>(p.last) + static_cast<int64_t>(slot) * p.last_outer + at;
 #pragma unroll

@@ -189,8 +189,9 @@ int64_t narrow_blocks(const ScanDims& d, bool state_bf16) {
     return d.B * ceil_div(d.D, kScanNarrowThreads / (d.N / states));
 }
 
-// How a forward is cut: rows up to `narrow` tokens take the narrow walk, longer ones the
-// wide one in segments of seg_len tokens (0: uncut).
+// How a forward is cut: rows up to `narrow` tokens take the narrow walk, longer ones up to
+// `lane` the lane walk, and longer ones still the wide walk in segments of seg_len tokens
+// (0: uncut).
 struct FwdPlan {
     int64_t narrow, lane, seg_len, segs, state, delta, end;
     bool wide;
@@ -198,7 +199,18 @@ struct FwdPlan {
 
 constexpr int64_t kNarrowAll = 64;  // tokens of a call up to which every row goes narrowly
 
-constexpr int64_t kLaneCap = 1 << 30;
+// Whether the lane walk takes a call that is not full.  It goes along a row at about
+// 6 + 1.5 N ns a token after 10 us, whatever the width (too few waves to hide what a token
+// waits for); segments, their chain and the walk take 12 + 0.85 N us and D N / 2000 ns a
+// token.  Measured, lane walk and segments, us: 97 tokens of 4096 channels x 16 states 17
+// and 25, 800 of them 35 and 53, 1200 52 and 63, 2048 108 and 88; of 512 channels 350
+// tokens 18 and 26; of 8192 channels 2048 tokens 130 and 138, 12000 904 and 698.  32
+// states: 300 of 2048 channels 25 and 39, 1500 of 4096 104 and 116.  64 states: 300 of
+// 1024 channels 41 and 67, 700 87 and 82, 3000 of 4096 352 and 489.  The longest row is
+// not known here: all tokens may be one row's.
+bool lanes_first(int64_t T, int64_t D, int64_t N) {
+    return N >= 16 && T <= 96 * N && T * (12000 + 3000 * N - D * N) < 2000 * (2000 + 850 * N);
+}
 
 FwdPlan fwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
     FwdPlan p{};
@@ -208,7 +220,7 @@ FwdPlan fwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
     p.segs = B;
     if (T <= kNarrowAll) return p;
     const bool full = B * ctiles >= 2048;
-    if (!full && N >= 16) p.lane = std::max(p.narrow, kLaneCap);
+    if (!full && lanes_first(T, D, N)) p.lane = T;
     p.wide = T > p.lane;
     if (p.wide) {
         const int64_t want = std::max<int64_t>(1, (full ? 1024 : 8192) / ctiles);

@@ -414,6 +414,40 @@ def test_forward(case, soft):
     assert torch.equal(pool.cpu()[same], before.cpu()[same])
 
 
+WALKS = [  # rows, channels, states, groups, work, states' type
+    ([600], 40, 16, 1, "f32", "f32"), ([530, 0, 90, 17, 16, 1], 72, 16, 2, "bf16", "bf16"),
+    ([600], 24, 32, 1, "bf16", "f32"), ([33, 0, 570, 5], 24, 32, 2, "f32", "bf16"),
+    ([600], 24, 64, 1, "bf16", "f32"), ([580, 64, 0, 1], 40, 64, 2, "f32", "f32"),
+    ([65], 4, 16, 1, "f32", "f32"), ([79, 0, 1, 80, 15, 16], 24, 16, 6, "bf16", "bf16"),
+    ([81], 12, 32, 1, "f32", "f32"), ([31, 0, 48, 1, 2, 0], 40, 32, 1, "bf16", "bf16"),
+    ([66], 12, 64, 1, "f32", "bf16"), ([70, 3, 0, 17, 1], 24, 64, 1, "bf16", "f32"),
+    ([17, 1, 0, 33, 16, 18, 49, 2, 5, 64], 536, 16, 1, "f32", "f32"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", WALKS, ids=str)
+def test_forward_of_every_walk(case):
+    """Calls on either side of the rule between the lane walk and segments, blocks of
+    16 tokens that end early, channels that end inside a wave and a workgroup."""
+    test_forward(case, True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [8, 16, 64])
+@pytest.mark.parametrize("lens", [[1], [13], [70], [90, 7], [700, 1]], ids=str)
+def test_decays_of_minus_infinity_forget(lens, N):
+    """exp(delta A) is 0 there, also in the last tokens of a row; delta is positive."""
+    a, off, offs, r = inputs(lens, 24, N, 1, "f32")
+    a["A"][:, 0] = float("-inf")
+    a["A"][5] = float("-inf")
+    h0 = (0.3 * r(len(lens), 24, N)).to(CU)
+    out, end = gdr.gdr_selective_scan_fwd(*(a[k] for k in OPS), offs, softplus=True,
+                                          initial_state=h0, output_final_state=True,
+                                          **kernel_args(a))
+    check_forward(a, off, out, end, True, h0)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("work", ["f32", "bf16"])
 @pytest.mark.parametrize("lens", [[5, 0, 9], [100, 0, 3], [0, 0], [0, 500, 0]], ids=str)
@@ -682,6 +716,43 @@ def test_empty_batches():
         n, go = gdr.gdr_verify_drafts(torch.zeros(0, dtype=torch.int32, device=CU),
                                       torch.zeros(0, 10, device=CU), offs)
         assert n.tolist() == [0] * len(lens) and go.tolist() == [-1] * len(lens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[40, 0, 3, 25], [150]], ids=str)
+def test_a_layer_trains(lens):
+    """Conv1d with SiLU, the scan of its output, and both gradients back to the
+    convolution's input and weights, in float32, against the formulas in float64 of
+    the same chain.
+
+    The convolution's output x carries 2 (W + 9) u of its terms' sizes (W + 1 products
+    and sums, a sigmoid of 6 u), here |x| <= A_x; dx does not depend on x, dA, ddt and
+    dB are linear in it.  Bounds are linear too: a gradient of the scan is off by f A
+    (A of |x| replaced by A_x), and the convolution's gradient carries the error f A of
+    its dout on through absolute weights, besides its own."""
+    Dn, N, W = 24, 16, 4
+    a, off, offs, r = inputs(lens, Dn, N, 1, "f32")
+    T = off[-1]
+    w, b = (0.5 * r(Dn, W)).to(CU), (0.1 * r(Dn)).to(CU)
+    raw, do = r(T, Dn).to(CU), r(T, Dn).to(CU)
+    a["x"] = gdr.gdr_causal_conv1d(raw, w, offs, bias=b, silu=True)
+    g = dict(zip(GRADS, gdr.gdr_selective_scan_bwd(do, *(a[k] for k in OPS), offs, softplus=True,
+                                                   **kernel_args(a))))
+    dx, dw, db = gdr.gdr_causal_conv1d_bwd(g["dx"], raw, w, offs, bias=b, silu=True)
+    exact = ref.conv(raw, w, off, b, True)
+    size = ref.conv(raw.abs(), w.abs(), off, b.abs(), False)  # |silu(s)| <= |s|
+    full = [exact if k == "x" else a[k] for k in OPS]
+    kw = dict(soft=True, **ref_args(a))
+    want = ref.scan_grads(do, *full, off, **kw)
+    A = ref.scan_grads(do, *(size if k == "x" else a[k] for k in OPS), off, absolute=True, **kw)
+    f = (8 * max(lens) + N + Dn + 600 + 2 * (W + 9)) * U32
+    for k in ("dx", "ddt", "dA", "dB", "dC", "dD", "dz"):
+        close(k, g[k], want[k], A[k], f)
+    ends = ref.conv_grads(want["dx"], raw, w, off, b, True)
+    E = ref.conv_grads(A["dx"], raw, w, off, b, True, absolute=True)
+    fc = f + (8 * 8 * (W + 2) + 180) * U32  # the convolution's own, as it is tested alone
+    for name, p, q, e in zip(("dx", "dw", "db"), (dx, dw, db), ends, E):
+        close(name, p, q, e, fc)
 
 
 # ------------------------------------------------------------------- Conv1d ---
