@@ -381,16 +381,6 @@ template <typename WT, int N> struct LaneWalk {
         token<4 * Q + 2, FULL>(delta, u, b[2], c[2], left);
         token<4 * Q + 3, FULL>(delta, u, b[3], c[3], left);
     }
-    // Lane j's: the sum over the channel's lanes of their y[j].
-    __device__ __forceinline__ float sum(int j) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = halve<0x128>(j & 8, y[i], y[i + 8]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = halve<0x141>(j & 4, y[i], y[i + 4]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) y[i] = halve<0x4E>(j & 2, y[i], y[i + 2]);
-        return halve<0xB1>(j & 1, y[0], y[1]);
-    }
 };
 
 template <typename WT, typename ST, int N>
@@ -485,7 +475,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_lanes(const ScanParams p) {
         w.template four<1, FULL>(now.delta, now.u, lds, j, n - t);
         w.template four<2, FULL>(now.delta, now.u, lds, j, n - t);
         w.template four<3, FULL>(now.delta, now.u, lds, j, n - t);
-        const float y = __builtin_fmaf(skip, now.x, w.sum(j)) * now.gate;
+        const float y = __builtin_fmaf(skip, now.x, row_sums16(w.y)) * now.gate;
         if (FULL || t + j < n)
             scan_put(reinterpret_cast<WT*>(const_cast<char*>(scan_base<WT>(orow, t0 + t)) + off + j * so), y);
     };

@@ -14,11 +14,13 @@
 //      16 tokens' decays and states forward into registers (the part's local
 //      state plus what is left of the segment's start), then backward.  A lane
 //      owns a channel; dB and dC, sums over channels, are reduced over the wave by
-//      halving: 32 values in 64 lanes take 70 instructions, not 6 each;
+//      halving: 32 values in 64 lanes take about 75 slots, not 6 each;
 //   4. the parts of dB, dC (over channels), dA, dskip and dt_bias's gradient (over
 //      segments) are added in a fixed order.
 // Everything is float32; sums over segments are float64.  Bound by the vector
-// units: about 26 slots a token, channel and state.
+// units: a part takes about 310 slots a channel and state and 1900 a channel, the
+// first launch about 150 a token and channel of 16 states.  2 x 2048 bf16 tokens of
+// 4096 gated channels of 16 states: 355 us, of which the slots take 250.
 #include <type_traits>
 
 #include "gdr_scan_dev.h"
@@ -261,29 +263,15 @@ __global__ void __launch_bounds__(256) grad_chains(const ScanParams p, const Sca
 
 // ------------------------------------------------------------- 3: gradients ---
 
-// Sums over the wave of x[0..15] and y[0..15]: lane l gets that of x[(l / 2) % 16]
-// below 32 and of y[...] from there on.
+// Sums over the wave of x[0..15] and y[0..15]: lane l gets that of x[l % 16] below 32
+// and of y[l % 16] from there on.
 __device__ __forceinline__ float sums32(float (&x)[16], float (&y)[16]) {
-    const int lane = threadIdx.x & 63;
-    float r[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x[i]), __float_as_uint(y[i]),
-                                                        false, false);
-        r[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[i]),
-                                                        __float_as_uint(r[i + 8]), false, false);
-        r[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = halve<0x128>(lane & 8, r[i], r[i + 4]);  // 8 lanes round
-#pragma unroll
-    for (int i = 0; i < 2; ++i) r[i] = halve<0x141>(lane & 4, r[i], r[i + 2]);  // mirrored in 8
-    r[0] = halve<0x4E>(lane & 2, r[0], r[1]);
-    return r[0] + dpp<0xB1>(r[0]);
+    const uint32_t rx = __float_as_uint(row_sums16(x)), ry = __float_as_uint(row_sums16(y));
+    const auto s = __builtin_amdgcn_permlane32_swap(rx, ry, false, false);
+    const float r = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    const auto w = __builtin_amdgcn_permlane16_swap(__float_as_uint(r), __float_as_uint(r), false,
+                                                    false);
+    return __uint_as_float(w[0]) + __uint_as_float(w[1]);
 }
 
 // A part's raw operands, all loaded before the first is used; past the row's end
@@ -483,7 +471,7 @@ grad_walk(const ScanParams p, const ScanGrad q) {
             carry[wave][n][lane] = mu;
             da[wave][n][lane] += ga;
             const float sum = sums32(a, h);
-            if (!(lane & 1)) red[wave][n][lane >> 1] = sum;
+            if (!(lane & 16)) red[wave][n][(lane >> 5) * kPart + (lane & 15)] = sum;
         }
         // The raw operands once more (from the caches): kept through the loop above they
         // would take 48 registers that it does not have.
