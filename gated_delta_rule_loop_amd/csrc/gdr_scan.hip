@@ -14,13 +14,13 @@
 // its step sizes (a segment's decay is exp(A sum delta)), one chains them to the
 // states the segments start from, and the walk follows.  16384 bf16 tokens of 4096
 // channels of 16 states 471 us, where the 275 slots a token and channel of both passes
-// take 469; 32 rows of 512, enough for one piece a row, 351 (150 slots, 256 us).
+// take 469; 32 rows of 512, enough for one piece a row, 348 (150 slots, 256 us).
 //
 // Lane walk (prompts of few tokens or many states): 16 lanes own a channel, so that
 // one launch has 16 times the waves and nothing is walked twice.  97 tokens of 4096
 // channels of 16 states 17 us (segments 25), 1500 of 2048 channels of 64 122 (168).
 //
-// Narrow walk (single tokens, drafted windows, folds): a lane owns 16 bytes of a
+// Narrow walk (single tokens, folds): a lane owns 16 bytes of a
 // channel's state, so that states are read and written in whole lines; the
 // output is summed over a channel's 1 to 16 lanes by lane permutations.  256 single
 // tokens of 4096 channels of 16 bf16 states: 19 us for 74 MB.
@@ -167,12 +167,18 @@ hipError_t narrow_out(const ScanParams& p, hipStream_t s) {
     constexpr int S = N < static_cast<int>(16 / sizeof(ST)) ? N : 16 / sizeof(ST);
     const int per = kScanNarrowThreads / (N / S);
     const dim3 grid(static_cast<unsigned>(p.B) * ((p.D + per - 1) / per));
-    // rows of about one token have nothing to load ahead for
+    // Rows of about one token have nothing to load ahead for; longer ones come here in
+    // folds and, without a lane walk, in calls of few tokens (64 tokens of 8 states 32 us, one
+    // token ahead 38; the fold of 64 windows of 1 to 12 tokens 14 us with either).
     const bool one = p.T <= p.B + p.B / 2;
-    if (p.out && one)
+    if constexpr (N < 16) {
+        if (p.out && !one) {
+            hipLaunchKernelGGL((scan_narrow<WT, ST, N, true, 4>), grid, dim3(kScanNarrowThreads), 0, s, p);
+            return hipGetLastError();
+        }
+    }
+    if (p.out)
         hipLaunchKernelGGL((scan_narrow<WT, ST, N, true, 1>), grid, dim3(kScanNarrowThreads), 0, s, p);
-    else if (p.out)
-        hipLaunchKernelGGL((scan_narrow<WT, ST, N, true, 4>), grid, dim3(kScanNarrowThreads), 0, s, p);
     else if (one)
         hipLaunchKernelGGL((scan_narrow<WT, ST, N, false, 1>), grid, dim3(kScanNarrowThreads), 0, s, p);
     else

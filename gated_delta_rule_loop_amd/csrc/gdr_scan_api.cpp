@@ -191,15 +191,26 @@ int64_t narrow_blocks(const ScanDims& d, bool state_bf16) {
 
 // How a forward is cut: rows up to `narrow` tokens take the narrow walk, longer ones up to
 // `lane` the lane walk, and longer ones still the wide walk in segments of seg_len tokens
-// (0: uncut).
+// (0: uncut).  All walks leave the same bits in the states of rows that are not cut.
+//   - Calls of about a token a row go narrowly, those of few tokens too where there is no
+//     lane walk (4096 channels: 256 rows of 1 token 19 us, in the wide walk 51).
+//   - Calls whose rows fill the chip walk widely, rows cut only where they are longer than
+//     all tokens' share of 2048 waves: 64 windows of 1 to 12 tokens of 4096 channels of 16
+//     states 27 us (lane walk 32, narrow 37), 256 rows of 3 53 (113, 104), 32 rows of 512 348
+//     (cut 480).  32 rows of 12 to 1023 tokens 648, cut at twice the share 958.
+//   - Other calls take the lane walk or segments, as lanes_first says: 63 single tokens
+//     beside a row of 190 35 us, the single ones narrowly 45; 16 rows of 16 beside one of 200
+//     35 and 30.
+// Segments number as many as 8192 waves hold where the chip is not full: 16384 tokens of
+// 4096 channels 470 us (4096 waves 508, 16384 469), 8 ragged rows in float32 165 (184, 169).
 struct FwdPlan {
     int64_t narrow, lane, seg_len, segs, state, delta, end;
     bool wide;
 };
 
-constexpr int64_t kNarrowAll = 64;  // tokens of a call up to which every row goes narrowly
+constexpr int64_t kUncut = 64;  // tokens of a call up to which no row is cut
 
-// Whether the lane walk takes a call that is not full.  It goes along a row at about
+// Whether the lane walk takes a call whose rows do not fill the chip.  It goes along a row at about
 // 6 + 1.5 N ns a token after 10 us, whatever the width (too few waves to hide what a token
 // waits for); segments, their chain and the walk take 12 + 0.85 N us and D N / 2000 ns a
 // token.  Measured, lane walk and segments, us: 97 tokens of 4096 channels x 16 states 17
@@ -215,15 +226,16 @@ bool lanes_first(int64_t T, int64_t D, int64_t N) {
 FwdPlan fwd_plan(int64_t T, int64_t B, int64_t D, int64_t N, int64_t G) {
     FwdPlan p{};
     const int64_t ctiles = G * ceil_div(D / G, 64);
-    p.narrow = T <= kNarrowAll ? kNarrowAll : B > 8 ? 16 : 0;
-    p.lane = p.narrow;
     p.segs = B;
-    if (T <= kNarrowAll) return p;
-    const bool full = B * ctiles >= 2048;
+    const bool few = T <= kUncut;
+    p.narrow = T <= B + B / 2 || (few && N < 16) ? kUncut : 0;
+    p.lane = p.narrow;
+    if (T <= p.narrow) return p;
+    const bool full = !few && B * ctiles >= 2048;
     if (!full && lanes_first(T, D, N)) p.lane = T;
     p.wide = T > p.lane;
     if (p.wide) {
-        const int64_t want = std::max<int64_t>(1, (full ? 1024 : 8192) / ctiles);
+        const int64_t want = std::max<int64_t>(1, (full ? 2048 : 8192) / ctiles);
         const int64_t len = std::max<int64_t>(16, round_up(ceil_div(T, want), 16));
         if (len < T) {
             p.seg_len = len;

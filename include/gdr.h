@@ -544,8 +544,8 @@ int gdr_selective_scan_step(const gdr_tensor* out, const gdr_tensor* x, const gd
 /*
  * gdr_selective_scan_fold - advance each row's state over its accepted prefix:
  * what gdr_selective_scan_fwd leaves after the row's first accepted[b] tokens
- * (the same bits where the forward takes the row token by token in one piece:
- * calls of up to 64 tokens, rows of up to 16 in any call of more than 8 rows).
+ * (the same bits where the forward takes the row in one piece: calls of up to
+ * 64 tokens, rows of up to 16 in any call).
  *   accepted          [B] u32|i32 (device): 0 or above the row's length leaves
  *                     the row alone
  */

@@ -550,6 +550,30 @@ def test_window_then_fold(lens, work, st):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Dn,N,work,st", [
+    (2048, 16, "bf16", "bf16"), (2048, 8, "f32", "f32"), (40, 16, "f32", "f32"),
+    (40, 8, "bf16", "f32"), (24, 64, "bf16", "bf16"), (2048, 32, "bf16", "f32"),
+], ids=str)
+def test_folds_leave_the_bits_of_every_walk(Dn, N, work, st):
+    """70 windows of up to 16 tokens, enough rows to fill the chip and few channels: a fold
+    of whole rows leaves what the forward leaves, bit for bit."""
+    lens = [1 + 5 * i % 16 for i in range(68)] + [0, 16]
+    a, off, offs, r = inputs(lens, Dn, N, 1, work, seed=12)
+    pool = (0.3 * r(len(lens), Dn, N)).to(DT[st]).to(CU)
+    moved, kept = pool.clone(), pool.clone()
+    out, _ = gdr.gdr_selective_scan_fwd(*(a[k] for k in OPS), offs, state=moved, softplus=True,
+                                        **kernel_args(a))
+    again, _ = gdr.gdr_selective_scan_fwd(*(a[k] for k in OPS), offs, state=kept, softplus=True,
+                                          keep_state=True, **kernel_args(a))
+    assert torch.equal(kept, pool) and torch.equal(again, out)
+    acc = torch.tensor(lens, dtype=torch.int32, device=CU)
+    folded = gdr.gdr_selective_scan_fold(pool.clone(), a["x"], a["dt"], a["A"], a["B"], offs, acc,
+                                         dt_bias=a["bias"], softplus=True)
+    assert torch.equal(folded, moved)
+    check_forward(a, off, out, moved if st == "f32" else None, True, pool)
+
+
+@pytest.mark.gpu
 def test_prompt_then_tokens_continue_one_row():
     a, off, offs, r = inputs([300], 136, 16, 1, "f32")
     want, _ = ref.scan(*(a[k] for k in OPS), off, soft=True, **ref_args(a))
