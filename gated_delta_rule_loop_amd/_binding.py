@@ -659,7 +659,7 @@ def gdr_verify_drafts_workspace(tokens, rows, vocab):
 
 def gdr_verify_drafts(tokens, target, input_row_offsets, *, draft=None, uniform=None,
                       accepted=None, next_token=None, workspace=None, stream=None):
-    """Judge drafted tokens: a row's window (tokens [T], int32) holds a certain
+    """Verify drafted tokens: a row's window (tokens [T], int32) holds a certain
     token and then the drafts; target [T, V] says what follows each, draft
     [T, V] what each draft was drawn from (None: drafts without probabilities),
     uniform [T] float32 holds a random number for each draft and, at the row's
