@@ -1057,6 +1057,88 @@ def test_graphs_replay_to_the_eager_results():
         torch.ones(1000, device=CU).sum().item()
 
 
+# ------------------------------------------------- offsets that pass 32 bits ---
+
+def _spread(a, stride, columns=()):
+    """The operands, and outputs of x's shape named in `columns`, as columns of one
+    buffer with `stride` elements from token to token."""
+    T = a["x"].shape[0]
+    buf, at, wide = torch.empty(T * stride, dtype=a["x"].dtype, device=CU), 0, dict(a)
+    for k in ("x", "dt", "z", "B", "C", *columns):
+        like = a[k] if k in a else a["x"]
+        n = like[0].numel()
+        view = buf[at:].as_strided((T, n), (stride, 1)).unflatten(1, like.shape[1:])
+        if k in a:
+            view.copy_(like)
+        wide[k], at = view, at + n
+    return wide
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Dn,stride", [
+    ([65000, 0, 1000], 64, 65536),      # segments, the last rows behind 2^32 elements
+    ([300, 900], 16, 1 << 22),          # the lane walk
+    ([1] * 40 + [10] * 110, 16, 3 << 20),   # short rows
+], ids=["long", "short", "rows"])
+def test_far_tokens_scan_as_near_ones(lens, Dn, stride):
+    a, off, offs, r = inputs(lens, Dn, 16, 1, "bf16", packed=False)
+    if off[-1] * stride < 2 ** 32:
+        stride = 2 ** 32 // off[-1] // 8 * 8 + 8
+    assert stride < 2 ** 24 and off[-1] * stride >= 2 ** 32
+    far = _spread(a, stride, ("out", "dx", "ddt", "dz", "do"))
+    far["do"].copy_(r(*a["x"].shape).to(torch.bfloat16))
+    kw = dict(softplus=True)
+    near, end = gdr.gdr_selective_scan_fwd(*(a[k] for k in OPS), offs, output_final_state=True,
+                                           **kw, **kernel_args(a))
+    out, last = gdr.gdr_selective_scan_fwd(*(far[k] for k in OPS), offs, output_final_state=True,
+                                           out=far["out"], **kw, **kernel_args(far))
+    assert torch.isfinite(near).all() and torch.equal(out, near) and torch.equal(last, end)
+    g = gdr.gdr_selective_scan_bwd(far["do"].contiguous(), *(a[k] for k in OPS), offs, **kw,
+                                   **kernel_args(a))
+    f = gdr.gdr_selective_scan_bwd(far["do"], *(far[k] for k in OPS), offs, dx=far["dx"],
+                                   ddt=far["ddt"], dz=far["dz"], **kw, **kernel_args(far))
+    assert all(torch.equal(p, q) for p, q in zip(g[:8], f[:8]))
+    w = torch.full((Dn, 4), 0.5, device=CU)
+    c = gdr.gdr_causal_conv1d_bwd(far["do"].contiguous(), a["x"], w, offs, silu=True)
+    d = gdr.gdr_causal_conv1d_bwd(far["do"], far["x"], w, offs, silu=True, dx=far["dx"])
+    assert torch.equal(c[0], d[0]) and torch.equal(c[1], d[1])
+
+
+@pytest.mark.gpu
+def test_far_slots_and_vocabulary_rows():
+    Dn, N, slots = 4096, 16, 65600  # 2^32 elements and some
+    a, off, offs, r = inputs([1, 1, 1], Dn, N, 1, "bf16")
+    pool = torch.empty(slots, Dn, N, dtype=torch.bfloat16, device=CU)
+    at = torch.tensor([slots - 1, 7, slots - 30], dtype=torch.int32, device=CU)
+    small = (0.3 * r(3, Dn, N)).to(torch.bfloat16).to(CU)
+    for step in (True, False):
+        pool[at.long()] = small
+        near = small.clone()
+        if step:
+            args = [a[k] for k in OPS]
+            o = gdr.gdr_selective_scan_step(*args, near, softplus=True, **kernel_args(a))
+            p = gdr.gdr_selective_scan_step(*args, pool, at, softplus=True, **kernel_args(a))
+        else:
+            b, _, offs, _ = inputs([20, 30, 70], Dn, N, 1, "bf16")
+            args = [b[k] for k in OPS]
+            o = gdr.gdr_selective_scan_fwd(*args, offs, state=near, softplus=True, **kernel_args(b))[0]
+            p = gdr.gdr_selective_scan_fwd(*args, offs, state=pool, slot_idx=at, softplus=True,
+                                           **kernel_args(b))[0]
+        assert torch.equal(o, p) and torch.equal(pool[at.long()], near)
+    del pool
+    T, V, stride = 5, 5003, 2 ** 30 + 17
+    probs = torch.rand(T, V, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(CU)
+    buf = torch.empty((T - 1) * stride + V, dtype=torch.bfloat16, device=CU)
+    far = buf.as_strided((T, V), (stride, 1))
+    far.copy_(probs)
+    tok = probs.float().argmax(1).int().roll(1).contiguous()
+    _, offs = offsets_of([5])
+    for u01 in (None, torch.tensor([0.7, 0.1, 0.2, 0.3, 0.999], device=CU)):
+        n, go = gdr.gdr_verify_drafts(tok, probs, offs, uniform=u01)
+        m, gm = gdr.gdr_verify_drafts(tok, far, offs, uniform=u01)
+        assert torch.equal(n, m) and torch.equal(go, gm) and go[0] >= 0
+
+
 @pytest.mark.gpu
 def test_index_checks_cover_the_new_entries():
     a, off, offs, _ = inputs([3, 2], 16, 16, 1, "f32")
