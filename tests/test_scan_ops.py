@@ -1057,6 +1057,71 @@ def test_graphs_replay_to_the_eager_results():
         torch.ones(1000, device=CU).sum().item()
 
 
+def _of_walk(lens, Dn, N, seed, ws=None):
+    """A forward and a gradient as one call, into buffers of its own."""
+    a, off, offs, r = inputs(lens, Dn, N, 1, "f32", seed=seed)
+    state = (0.3 * r(len(lens), Dn, N)).to(CU)
+    do = r(*a["x"].shape).to(CU)
+    T = do.shape[0]
+    floats = max(gdr.gdr_selective_scan_workspace(T, len(lens), Dn, N, 1),
+                 gdr.gdr_selective_scan_workspace(T, len(lens), Dn, N, 1, True))
+    if ws is None:
+        ws = torch.full((floats,), float("nan"), device=CU)
+    out, end = torch.empty(T, Dn, device=CU), torch.empty_like(state)
+
+    def call(stream=None):
+        gdr.gdr_selective_scan_fwd(*(a[k] for k in OPS), offs, initial_state=state, final_state=end,
+                                   softplus=True, out=out, workspace=ws, stream=stream,
+                                   **kernel_args(a))
+        g = gdr.gdr_selective_scan_bwd(do, *(a[k] for k in OPS), offs, initial_state=state,
+                                       dfinal_state=state, softplus=True, workspace=ws,
+                                       stream=stream, **kernel_args(a))
+        return [out, end, *g]
+
+    return call, floats
+
+
+WALK_CALLS = [([600, 20], 40, 16), ([90, 0, 17], 72, 16), ([1] * 9, 64, 16), ([40, 600], 24, 64)]
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once():
+    calls = [_of_walk(*w, seed=i)[0] for i, w in enumerate(WALK_CALLS)]
+    want = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [c(streams[i % 2]) for i, c in enumerate(calls)]
+        torch.cuda.synchronize()
+        for p, q in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(p, q))
+
+
+@pytest.mark.gpu
+def test_graphs_that_share_a_workspace():
+    """Nothing in it is expected to be what an earlier call left."""
+    floats = max(_of_walk(*w, seed=i)[1] for i, w in enumerate(WALK_CALLS))
+    ws = torch.full((floats,), float("nan"), device=CU)
+    calls = [_of_walk(*w, seed=i, ws=ws)[0] for i, w in enumerate(WALK_CALLS)]
+    want = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    graphs = []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = c()
+        graphs.append((g, got))
+    for turn in range(3):
+        for i in (range(4), reversed(range(4)), (2, 0, 3, 1))[turn]:
+            g, got = graphs[i]
+            for t in got:
+                t.fill_(3)
+            ws.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(x, y) for x, y in zip(want[i], got))
+
+
 # ------------------------------------------------- offsets that pass 32 bits ---
 
 def _spread(a, stride, columns=()):
