@@ -433,6 +433,46 @@ def test_forward_of_every_walk(case):
     test_forward(case, True)
 
 
+MIXED = [  # single tokens and short rows beside cut ones: rows, channels, states, groups, work, states
+    ([1] * 250 + [40, 80], 4096, 16, 1, "bf16", "f32"),
+    ([80] + [1] * 250 + [40], 4096, 16, 1, "f32", "bf16"),
+    ([1] * 511 + [48, 200], 2048, 16, 2, "bf16", "bf16"),
+    ([1] * 300 + [40, 80], 64, 8, 1, "f32", "f32"),
+    ([1] * 400 + [80, 0] + [1] * 150 + [17, 64, 90], 40, 8, 1, "f32", "f32"),
+    ([1] * 260 + [100, 63, 33] + [1] * 360 + [65, 20], 72, 8, 3, "f32", "bf16"),
+    ([1] * 300 + [40, 70, 33], 2048, 64, 1, "bf16", "f32"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", MIXED, ids=lambda c: f"{len(c[0])}x{max(c[0])}-{c[1]}-{c[2]}")
+def test_forward_of_short_rows_beside_cut_ones(case):
+    """Rows longer than a segment that the narrow walk takes have no segment of their
+    own: before, between and behind rows that have some, those start from their own
+    states."""
+    test_forward(case, True)
+
+
+@pytest.mark.gpu
+def test_mixed_batch_on_dense_states():
+    """The same beside rows without tokens, which hand on their state; a cut row's
+    outputs have the bits that the rows beside it leave in a call of other values."""
+    lens = [1] * 150 + [0, 40, 0, 80] + [1] * 500 + [64, 130, 0, 17]
+    a, off, offs, r = inputs(lens, 64, 8, 1, "f32", packed=False)
+    h0 = (0.3 * r(len(lens), 64, 8)).to(CU)
+    call = lambda: gdr.gdr_selective_scan_fwd(  # noqa: E731
+        *(a[k] for k in OPS), offs, softplus=True, initial_state=h0, output_final_state=True,
+        **kernel_args(a))
+    out, end = call()
+    check_forward(a, off, out, end, True, h0)
+    a["x"][off[151]:off[152]] *= 100  # the row of 40, before the one of 80
+    other, _ = call()
+    rows = torch.ones(off[-1], dtype=torch.bool, device=CU)
+    rows[off[151]:off[152]] = False
+    assert torch.equal(out[rows], other[rows])
+    assert not torch.equal(out[~rows], other[~rows])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("N", [8, 16, 64])
 @pytest.mark.parametrize("lens", [[1], [13], [70], [90, 7], [700, 1]], ids=str)
