@@ -130,18 +130,27 @@ template <typename WT> __device__ __forceinline__ uint32_t scan_step(const ScanR
     return static_cast<uint32_t>(r.tok) * static_cast<uint32_t>(sizeof(WT));
 }
 
-// e^x for finite x to about one float32 rounding: what x log2(e) loses to its
-// rounding is put back as a factor (the compensated product: 2^hi (1 + lo ln 2)).
-// Results below 2^-126 are 0.
-__device__ __forceinline__ float scan_exp(float x) {
+// e^x = 2^hi 2^lo: hi, and in lo what x log2(e) loses when it is rounded to hi.
+__device__ __forceinline__ float scan_exponent(float x, float& lo) {
     const float hi = x * kScanLog2e;
-    const float lo = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, kScanLog2e, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi);
+    lo = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, kScanLog2e, -hi));
+    return hi;
+}
+// e^x to about one float32 rounding (the compensated product: 2^hi (1 + lo ln 2)) for
+// finite x up to 88; where 2^hi is infinite the sum would be no number.  Results
+// below 2^-126 are 0.
+__device__ __forceinline__ float scan_exp(float x) {
+    float lo;
+    const float e = __builtin_amdgcn_exp2f(scan_exponent(x, lo));
     return __builtin_fmaf(e, lo * 0.693147181f, e);
 }
-// 1 / (1 + e^-x); of NaN it is a number (callers multiply by x, which is none).
+// 1 / (1 + e^-x); of NaN it is a number (callers multiply by x, which is none).  e^-x
+// passes float32's largest value from -x = 88.8 on: as a product with a factor near 1,
+// which costs a rounding more than the sum, it is infinite there and the sigmoid 0.
 __device__ __forceinline__ float scan_sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + scan_exp(__builtin_amdgcn_fmed3f(-x, -150.0f, 128.0f)));
+    float lo;
+    const float e = __builtin_amdgcn_exp2f(scan_exponent(__builtin_amdgcn_fmed3f(-x, -150.0f, 128.0f), lo));
+    return __builtin_amdgcn_rcpf(1.0f + e * __builtin_fmaf(lo, 0.693147181f, 1.0f));
 }
 // log(1 + e^x) = max(x, 0) + log(1 + t), t = e^-|x|.  log(1 + t) = 2 atanh(s) with
 // s = t / (2 + t) <= 1/3: an odd series in s, its tail after s fitted by a cubic

@@ -653,6 +653,84 @@ def test_large_and_small_steps():
     check_forward(a, off, out, end, True, None)
 
 
+def wide_sweep(*shape, seed=0, least=-1e30):
+    """-200 to 200, half of it within -130 to -85, where e^-x passes float32's
+    largest value, in any order."""
+    n = 1
+    for s in shape:
+        n *= s
+    v = torch.cat([torch.linspace(-200, 200, n - n // 2), torch.linspace(-130, -85, n // 2)])
+    v = v[torch.randperm(n, generator=torch.Generator().manual_seed(seed))]
+    v[3] = least
+    return v.reshape(shape)
+
+
+# A sigmoid below 2^-126 is 0 in the kernels: an output is off by |z| 2^-126 times a
+# number of ordinary size, below the 1e-30 that close() lets through.
+@pytest.mark.gpu
+@pytest.mark.parametrize("work", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,N", [([60], 8), ([50, 0, 43], 16), ([90], 64), ([90, 30], 8)], ids=str)
+def test_gates_of_every_size(lens, N, work):
+    """Narrow, lane and wide walk."""
+    a, off, offs, _ = inputs(lens, 64, N, 1, work, packed=False)
+    a["z"] = wide_sweep(off[-1], 64).to(DT[work]).to(CU)
+    out, end = gdr.gdr_selective_scan_fwd(*(a[k] for k in OPS), offs, softplus=True,
+                                          output_final_state=True, **kernel_args(a))
+    check_forward(a, off, out, end, True, None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("work", ["f32", "bf16"])
+def test_step_gates_of_every_size(work):
+    a, off, offs, r = inputs([1] * 60, 64, 16, 1, work, packed=False)
+    a["z"] = wide_sweep(60, 64).to(DT[work]).to(CU)
+    pool = (0.3 * r(60, 64, 16)).to(CU)
+    h0 = pool.clone()
+    out = gdr.gdr_selective_scan_step(*(a[k] for k in OPS), pool, softplus=True, **kernel_args(a))
+    check_forward(a, off, out, pool, True, h0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("work", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [8, 16, 64])
+def test_backward_gates_of_every_size(N, work):
+    case = ([70, 1, 20], 64, N, 1, work, True, True, True)
+    a, off, offs, do, h0, dh = bwd_inputs(case, lead=0, tail=0)
+    a["z"] = wide_sweep(*do.shape).to(DT[work]).to(CU)
+    got = dict(zip(GRADS, gdr.gdr_selective_scan_bwd(do, *(a[k] for k in OPS), offs, softplus=True,
+                                                     initial_state=h0, dfinal_state=dh,
+                                                     **kernel_args(a))))
+    kw = dict(soft=True, h0=h0, dh=dh, **ref_args(a))
+    want = ref.scan_grads(do, *(a[k] for k in OPS), off, **kw)
+    A = ref.scan_grads(do, *(a[k] for k in OPS), off, absolute=True, **kw)
+    for k in GRADS:
+        close(k, got[k], want[k], A[k], (8 * 70 + N + 64 + 600) * U32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("work", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 4])
+def test_conv_backward_of_every_size(W, work):
+    """SiLU's slope s(p) = sig (1 + p (1 - sig)) changes by at most sig (1 - sig) (2 + |p|),
+    twice S = sig (1 + |p| (1 - sig)), which A holds; p is off by (W + 2) u of its terms'
+    size P.  Beside it 40 u, and a run's sums, as above."""
+    lens, C = [33, 0, 40, 1], 64
+    gen = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    off, offs = offsets_of(lens)
+    x, do = wide_sweep(off[-1], C, least=-200).to(DT[work]).to(CU), r(off[-1], C).to(DT[work]).to(CU)
+    w = 0.02 * r(C, W)
+    w[:, -1] = 1
+    w, b = w.to(CU), r(C).to(CU)
+    got = gdr.gdr_causal_conv1d_bwd(do, x, w, offs, bias=b, silu=True)
+    P = float(ref.conv(x.abs(), w.abs(), off, b.abs()).max())
+    f = (2 * P * (W + 2) + 40) * U32
+    want = ref.conv_grads(do, x, w, off, b, True)
+    A = ref.conv_grads(do, x, w, off, b, True, absolute=True)
+    for name, g, e, size, more in zip(("dx", "dw", "db"), got, want, A, (0, 140, 140)):
+        close(name, g, e, size, f + more * U32)
+
+
 # ---------------------------------------------------------------- gradients ---
 
 BWD = [  # rows, channels, states, groups, work, states, gate, skip and bias
