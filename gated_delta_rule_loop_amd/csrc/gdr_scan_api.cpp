@@ -553,9 +553,12 @@ int gdr_selective_scan_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gd
     p.seg_len = static_cast<int32_t>(pl.seg_len);
     p.segs = static_cast<int32_t>(pl.segs);
     float* ws = present(workspace) ? static_cast<float*>(workspace->data) : nullptr;
-    p.seg_state = ws + pl.state;
-    p.seg_delta = ws + pl.delta;
     ScanGrad g{};
+    if (pl.seg_len) {
+        p.seg_state = ws + pl.state;
+        p.seg_delta = ws + pl.delta;
+        g.seg_rev = ws + pl.rev;
+    }
     g.d_o = rows_of(dout);
     g.dx = rows_of(dx);
     g.ddt = rows_of(ddt);
@@ -573,7 +576,6 @@ int gdr_selective_scan_bwd(const gdr_tensor* dout, const gdr_tensor* x, const gd
     }
     g.tiles = static_cast<int32_t>(pl.gtiles);
     g.check = ws + pl.check;
-    g.seg_rev = ws + pl.rev;
     g.turned = ws + pl.turned;
     g.part_bc = ws + pl.bc;
     g.part_a = ws + pl.a;

@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kScanThreads, 3) grad_sums(const ScanParams p,
         if (ends) p.seg_state[mine + static_cast<int64_t>(k) * p.D] = h[k];
         if (rev) q.seg_rev[mine + static_cast<int64_t>(k) * p.D] = R[k];
     }
-    if (n0 == 0) p.seg_delta[static_cast<int64_t>(seg) * p.D + d] = total;
+    // Without cut rows the workspace has no place for it.
+    if (n0 == 0 && (ends || rev)) p.seg_delta[static_cast<int64_t>(seg) * p.D + d] = total;
 }
 
 // --------------------------------------------------------------- 2: chains ---

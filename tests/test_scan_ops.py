@@ -799,6 +799,22 @@ def test_backward(case, soft):
         near(k, g, w, (40 * U32 + (u(torch.bfloat16) if g.dtype == torch.bfloat16 else 0)) * n ** 0.5)
 
 
+UNCUT = [  # 520 groups are workgroups enough for whole rows: none is cut into segments
+    ([40] + [0] * 8 + [20], 2080, 8, 520, "f32", True, True, True),
+    ([50, 3] + [0] * 15 + [20, 33], 2080, 16, 520, "f32", False, True, True),
+    ([40] + [0] * 32 + [33, 17], 2080, 32, 520, "bf16", True, False, True),
+    ([40, 70] + [0] * 63 + [20, 1, 18], 2080, 64, 520, "bf16", True, True, False),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", UNCUT, ids=lambda c: f"{len(c[0])}-{c[2]}")
+def test_backward_of_uncut_rows(case):
+    """Rows of several parts in a call that cuts none: the states before their parts are
+    their own, whatever the rows behind them are."""
+    test_backward(case, True)
+
+
 @pytest.mark.gpu
 def test_backward_against_the_forwards_differences():
     """The kernels' own forward in float32: a step of 2^-7 along a direction, the
