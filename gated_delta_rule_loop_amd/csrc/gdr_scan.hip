@@ -516,12 +516,12 @@ __global__ void __launch_bounds__(256) scan_chain(const ScanParams p) {
     const int n = static_cast<int>(p.offsets[row + 1] - p.offsets[row]);
     // Uncut rows have nothing to chain, and rows that another walk takes no segment at all:
     // the places from scan_first_seg on would be the next cut row's.
-    const int count = scan_segs(n, p.seg_len, p.seg_skip);
-    if (count < 2) return;
+    if (n <= max(p.seg_len, p.seg_skip)) return;
     const int64_t first = scan_first_seg(p, row);
     if (i >= DN) return;
     const uint32_t slot = p.slot_idx ? p.slot_idx[row] : static_cast<uint32_t>(row);
     if (p.slot_idx != nullptr && slot == kPadSlot) return;
+    const int count = (n + p.seg_len - 1) / p.seg_len;
     const float a2 = p.A[i] * kScanLog2e;
     float h = 0.0f;
     if (p.in.p) {
