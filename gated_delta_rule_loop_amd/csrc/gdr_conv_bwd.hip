@@ -10,7 +10,7 @@
 // so that x and dout are read once and nothing else is, and keeps the run's part
 // of the weights' gradient in registers.  A second launch adds the runs' parts
 // in float64 in a fixed order.  A stream over x, dout and dx: bound by HBM.  4096 bf16
-// tokens of 8192 channels 49 us (201 MB, 4.1 TB/s; a copy 5.1) and 5 for the runs' parts.
+// tokens of 8192 channels 52 us (201 MB, 3.9 TB/s; a copy 5.1) and 5 for the runs' parts.
 #include <type_traits>
 
 #include "gdr_scan_dev.h"

@@ -13,8 +13,8 @@
 // chip: one launch takes each segment's own end state from zero and the sum of
 // its step sizes (a segment's decay is exp(A sum delta)), one chains them to the
 // states the segments start from, and the walk follows.  16384 bf16 tokens of 4096
-// channels of 16 states 471 us, where the 275 slots a token and channel of both passes
-// take 469; 32 rows of 512, enough for one piece a row, 348 (150 slots, 256 us).
+// channels of 16 states 471 us (183, 18 and 268), where the 275 slots a token and channel of
+// both passes take 469; 32 rows of 512, enough for one piece a row, 348 (150 slots, 256 us).
 //
 // Lane walk (prompts of few tokens or many states): 16 lanes own a channel, so that
 // one launch has 16 times the waves and nothing is walked twice.  97 tokens of 4096

@@ -26,7 +26,6 @@ struct ScanDims {
     int64_t tiles() const { return ceil_div(D / G, 64); }
 };
 
-// [T, D] operand: unit innermost stride, 16-byte rows.
 // Tokens are addressed by unsigned 32-bit offsets from a part's first.
 constexpr int64_t kMaxTokenStride = (int64_t{1} << 24) - 1;
 
@@ -37,6 +36,7 @@ int check_token_stride(const char* fn, const char* name, const gdr_tensor* t) {
     return GDR_OK;
 }
 
+// [T, D] operand: unit innermost stride, 16-byte rows.
 int check_rows(const char* fn, const char* name, const gdr_tensor* t, const ScanDims& d, bool out) {
     const int64_t shape[2] = {d.T, d.D};
     int rc = check_tensor(fn, name, t, 2, shape, true, true, false);
@@ -193,7 +193,11 @@ int64_t narrow_blocks(const ScanDims& d, bool state_bf16) {
 // `lane` the lane walk, and longer ones still the wide walk in segments of seg_len tokens
 // (0: uncut).  All walks leave the same bits in the states of rows that are not cut.
 //   - Calls of about a token a row go narrowly, those of few tokens too where there is no
-//     lane walk (4096 channels: 256 rows of 1 token 19 us, in the wide walk 51).
+//     lane walk: 64 rows of 1 token of 4096 channels of 16 states 13 us (widely 30). Above
+//     64 tokens the launches for longer rows, which may be among them, come behind it and
+//     both ways take about as long: 256 rows of 1 token 59 us (widely 53), of 64 states 172
+//     (208), 250 rows of 1 beside 40 and 80 tokens 95 (73), 511 beside 200 141 (145). A call
+//     of single tokens alone is gdr_selective_scan_step's (256 rows 19 us).
 //   - Calls whose rows fill the chip walk widely, rows cut only where they are longer than
 //     all tokens' share of 2048 waves: 64 windows of 1 to 12 tokens of 4096 channels of 16
 //     states 27 us (lane walk 32, narrow 37), 256 rows of 3 53 (113, 104), 32 rows of 512 348
@@ -201,6 +205,8 @@ int64_t narrow_blocks(const ScanDims& d, bool state_bf16) {
 //   - Other calls take the lane walk or segments, as lanes_first says: 63 single tokens
 //     beside a row of 190 35 us, the single ones narrowly 45; 16 rows of 16 beside one of 200
 //     35 and 30.
+// The wide walk's waves find their rows in time that grows with the number of rows (see
+// scan_locate).
 // Segments number as many as 8192 waves hold where the chip is not full: 16384 tokens of
 // 4096 channels 470 us (4096 waves 508, 16384 469), 8 ragged rows in float32 165 (184, 169).
 struct FwdPlan {

@@ -29,8 +29,9 @@ namespace gdr {
 namespace {
 
 constexpr int kPart = kScanPart;
-// Waves of a gradient's workgroup: carried sums of every state take 512 bytes of
-// LDS a wave and state, so that 64 states leave room for two.
+// Waves of a gradient's workgroup: what it holds of every state takes 1156 bytes of LDS a
+// wave and state (four floats a lane and 33 sums), 73984 a workgroup of 16 states or more, so
+// that two workgroups fit a compute unit.
 constexpr int grad_waves(int N) { return N > 32 ? 1 : N > 16 ? 2 : 4; }
 // States that one wave of the first launch carries.
 constexpr int sum_states(int N) { return N < 16 ? N : 16; }

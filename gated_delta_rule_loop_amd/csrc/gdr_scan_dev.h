@@ -262,7 +262,9 @@ struct ScanSpan {
 };
 
 // Which tokens segment `seg` spans; false past the last one.  The whole wave calls
-// it with one `seg`: rows are counted 64 at a time.
+// it with one `seg`: rows are counted 64 at a time, so that every wave's time grows with
+// the number of rows before its own (4096 channels, rows of 4 tokens: 1024 rows 282 us, 4096
+// 2.5 ms, 16384 31 ms).
 __device__ __forceinline__ bool scan_locate(const ScanParams& p, int seg, ScanSpan& o) {
     const int lane = threadIdx.x & 63;
     int before = 0;

@@ -521,6 +521,8 @@ int64_t gdr_selective_scan_workspace(int64_t tokens, int64_t rows, int64_t chann
  *   final_state       [B, D, N] (out) of the same dtype, or absent: dense
  *                     states instead of a pool
  *   flags             GDR_FLAG_DT_SOFTPLUS, GDR_FLAG_KEEP_STATE
+ * Where every row is one token, gdr_selective_scan_step takes one launch for up to
+ * four here.
  */
 int gdr_selective_scan_fwd(const gdr_tensor* out, const gdr_tensor* x, const gdr_tensor* dt,
                            const gdr_tensor* A, const gdr_tensor* B, const gdr_tensor* C,
